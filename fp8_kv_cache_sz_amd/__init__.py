@@ -7,6 +7,8 @@ run in the library.  Tensors:
 * BF16 data: ``torch.bfloat16`` (or ``int16``) tensors.
 * FP8 E5M2 data: ``torch.float8_e5m2`` or ``uint8`` tensors of raw bytes.
 * Streams: ``uint8`` device tensors.
+* Paged caches: ``[pages, 2, kv_heads, page_tokens, head_dim]`` tensors of
+  BF16, E5M2 or E4M3 (paged.py).
 """
 from __future__ import annotations
 
@@ -30,7 +32,9 @@ __all__ = ["BF16", "E5M2", "TOP16", "TOP8", "TOP15S", "Codebook", "SplitZipError
            "decode_workspace", "encode", "decode",
            "read_escape_count", "transfer", "transfer_buffers", "reference_copy", "reference_split",
            "reference_join", "profile_enable",
-           "profile_collect"]
+           "profile_collect",
+           "E4M3", "PagedCache", "PageBatch", "paged_cache", "cache_write", "cache_read", "cache_check",
+           "paged_attention", "attention_workspace"]
 
 # An sz_codebook in device memory: u32 dtype, 16 exponent bytes (20 bytes,
 # padded to 32 so that the tensor size keeps 16-byte multiples).
@@ -346,3 +350,7 @@ def profile_enable(on: bool = True) -> None:
 def profile_collect() -> dict:
     """{kernel name: (launches, total ms)} since the last collect/enable."""
     return _native.sz_profile_collect()
+
+
+from .paged import (E4M3, PageBatch, PagedCache, attention_workspace, cache_check, cache_read,  # noqa: E402
+                    cache_write, paged_attention, paged_cache)

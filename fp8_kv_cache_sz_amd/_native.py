@@ -23,6 +23,7 @@ lib = ctypes.CDLL(LIBRARY)
 
 SZ_BF16 = 0
 SZ_FP8_E5M2 = 1
+SZ_FP8_E4M3 = 2         # paged cache only
 
 ERRORS = {
     0: "SZ_OK", -1: "SZ_E_ARG", -2: "SZ_E_DTYPE", -3: "SZ_E_CAPACITY", -4: "SZ_E_ALIGN",
@@ -44,7 +45,21 @@ class sz_kernel_stat(ctypes.Structure):
                 ("total_ms", ctypes.c_double)]
 
 
+class sz_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_uint32), ("page_tokens", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("pages", ctypes.c_uint64), ("data", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
+class sz_batch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("seqs", ctypes.c_uint32), ("table_width", ctypes.c_uint32), ("tokens", ctypes.c_uint32),
+                ("max_new", ctypes.c_uint32), ("max_kv", ctypes.c_uint32)]
+
+
 _u64, _i32, _vp = ctypes.c_uint64, ctypes.c_int, ctypes.c_void_p
+_u32, _f32 = ctypes.c_uint32, ctypes.c_float
+_cache_p, _batch_p = ctypes.POINTER(sz_cache), ctypes.POINTER(sz_batch)
 
 lib.sz_calibrate.argtypes = [_i32, _vp, _u64, ctypes.POINTER(sz_codebook)]
 lib.sz_calibrate.restype = _i32
@@ -93,13 +108,28 @@ lib.sz_reference_split.argtypes = [_i32, _vp, _u64, _vp, _vp, _vp]
 lib.sz_reference_split.restype = _i32
 lib.sz_reference_join.argtypes = [_i32, _vp, _vp, _u64, _vp, _vp]
 lib.sz_reference_join.restype = _i32
+lib.sz_cache_write.argtypes = [_cache_p, _batch_p, _vp, _u64, _u64, _vp, _u64, _u64, _vp, _vp]
+lib.sz_cache_write.restype = _i32
+lib.sz_cache_read.argtypes = [_cache_p, _batch_p, _vp, _u64, _u64, _vp, _u64, _u64, _vp, _vp]
+lib.sz_cache_read.restype = _i32
+lib.sz_cache_check_workspace_size.argtypes = [_cache_p]
+lib.sz_cache_check_workspace_size.restype = _u64
+lib.sz_cache_check.argtypes = [_cache_p, _batch_p, _vp, _u64, _vp, _vp]
+lib.sz_cache_check.restype = _i32
+lib.sz_paged_attention_workspace_size.argtypes = [_cache_p, _batch_p, _u32]
+lib.sz_paged_attention_workspace_size.restype = _u64
+lib.sz_paged_attention.argtypes = [_cache_p, _batch_p, _vp, _u32, _u64, _u64, _f32, _u32, _vp, _vp, _vp, _u64, _vp,
+                                   _vp]
+lib.sz_paged_attention.restype = _i32
 
 EXPORTS = ("sz_calibrate", "sz_encoded_size", "sz_workspace_size", "sz_workspace_size_format",
            "sz_decode_workspace_size", "sz_encode", "sz_encode_devcb",
            "sz_calibrate_workspace_size", "sz_calibrate_device", "sz_decode", "sz_encoded_size_format",
            "sz_encode_format", "sz_decode_format", "sz_transfer_workspace_size", "sz_transfer_host_bytes",
            "sz_transfer", "sz_profile_enable", "sz_profile_collect", "sz_reference_copy",
-           "sz_reference_split", "sz_reference_join", "sz_decode_noalloc_max_elems", "sz_decode_noalloc")
+           "sz_reference_split", "sz_reference_join", "sz_decode_noalloc_max_elems", "sz_decode_noalloc",
+           "sz_cache_write", "sz_cache_read", "sz_cache_check_workspace_size", "sz_cache_check",
+           "sz_paged_attention_workspace_size", "sz_paged_attention")
 
 SZ_FORMAT_TOP16 = 1
 SZ_FORMAT_TOP8 = 2
@@ -196,6 +226,33 @@ def sz_decode_noalloc_max_elems() -> int:
 
 def sz_decode_noalloc(d_in, in_bytes, dtype, d_out, n, d_status, stream) -> int:
     return int(lib.sz_decode_noalloc(d_in, in_bytes, dtype, d_out, n, d_status, stream))
+
+
+# cache and batch: sz_cache and sz_batch, or byref() of them
+def sz_cache_write(cache, batch, d_k, k_token, k_head, d_v, v_token, v_head, d_status, stream) -> int:
+    return lib.sz_cache_write(cache, batch, d_k, k_token, k_head, d_v, v_token, v_head, d_status, stream)
+
+
+def sz_cache_read(cache, batch, d_k, k_token, k_head, d_v, v_token, v_head, d_status, stream) -> int:
+    return lib.sz_cache_read(cache, batch, d_k, k_token, k_head, d_v, v_token, v_head, d_status, stream)
+
+
+def sz_cache_check_workspace_size(cache) -> int:
+    return int(lib.sz_cache_check_workspace_size(cache))
+
+
+def sz_cache_check(cache, batch, d_ws, ws_bytes, d_status, stream) -> int:
+    return lib.sz_cache_check(cache, batch, d_ws, ws_bytes, d_status, stream)
+
+
+def sz_paged_attention_workspace_size(cache, batch, q_heads) -> int:
+    return int(lib.sz_paged_attention_workspace_size(cache, batch, q_heads))
+
+
+def sz_paged_attention(cache, batch, d_q, q_heads, q_token, q_head, scale, window, d_out, d_lse, d_ws, ws_bytes,
+                       d_status, stream) -> int:
+    return lib.sz_paged_attention(cache, batch, d_q, q_heads, q_token, q_head, scale, window, d_out, d_lse, d_ws,
+                                  ws_bytes, d_status, stream)
 
 
 def sz_reference_copy(d_src, d_dst, nbytes, stream) -> int:

@@ -7,8 +7,9 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", name) for name in
-           ("encode.hip", "decode.hip", "calibrate.hip", "runtime.hip", "transfer.hip")]
-HEADERS = [os.path.join(ROOT, "include", "splitzip.h"), os.path.join(HERE, "csrc", "common.hpp")]
+           ("encode.hip", "decode.hip", "calibrate.hip", "runtime.hip", "transfer.hip", "cache.hip", "attention.hip")]
+HEADERS = [os.path.join(ROOT, "include", "splitzip.h"), os.path.join(HERE, "csrc", "common.hpp"),
+           os.path.join(HERE, "csrc", "paged.hpp")]
 LIBRARY = os.path.join(HERE, "libsplitzip.so")
 ARCH = "gfx950"
 

@@ -1,0 +1,957 @@
+// Attention of new tokens over the paged KV cache.
+//
+// For a new token at position p of its sequence and query head h (KV head
+// h / G), over the visible keys j, max(0, p - window + 1) <= j <= p:
+//   s_j = scale q . K_j      m = max s_j      l = sum exp(s_j - m)
+//   o   = sum exp(s_j - m) V_j / l            lse = m + ln l
+// computed in one pass over the keys with a running m and l (in powers of
+// two: exp(s - m) = 2^(c s - m'), c = scale log2 e).  m' need not be the
+// maximum itself, only near enough that no power overflows: it is raised,
+// and the sums scaled, only when a score exceeds it by more than 2^kSlack,
+// which is rare after the first keys.  Scores, m, l and o are 32 bits; the
+// probabilities are rounded to BF16 (relative 2^-9 each, errors of either
+// sign) because the matrix instructions take BF16, and K and V enter as the
+// exact BF16 values that sz_cache_read returns.
+//
+// Rows are (token, head of the KV head's group), so one K/V row read serves
+// the G query heads of its KV head.  Both kernels compute S^T = K Q^T, whose
+// result layout gives each lane one row's scores (maxima and sums stay in
+// the lane) and is, keys renumbered, the operand layout of O^T = V^T P^T: P
+// never leaves its registers.
+//   sz_attn_rows  sequences with at most 16 rows per KV head (single tokens,
+//                 drafts): bound by reading K and V.
+//   sz_attn_tiles the others: 128 rows a workgroup, bound by the matrix and
+//                 vector units.
+// Where there are few rows the keys are split into chunks whose partial
+// (m, l, o) sz_attn_join joins, always in the order of the chunks.
+#include "paged.hpp"
+
+namespace sz {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kAttnThreads = 256;
+constexpr uint32_t kRowsMax = 16;        // rows of sz_attn_rows
+constexpr uint32_t kTileRows = 128;      // rows of sz_attn_tiles
+constexpr uint32_t kTileKeys = 64;
+constexpr uint32_t kKeyAlign = 64;       // chunks start at multiples of this
+constexpr float kSlack = 8.0f;
+constexpr float kNone = -__builtin_huge_valf();
+
+struct AttnArgs {
+    PagedCache c;
+    PagedBatch b;
+    const uint16_t *q;
+    uint64_t q_token, q_head;
+    uint16_t *out;            // [tokens][q_heads][D]
+    float *lse;               // [tokens][q_heads] or null
+    float *part;              // [splits][tokens][q_heads][D], o before the division by l
+    float2 *part_ml;          // [splits][tokens][q_heads] (m', l)
+    float c2;                 // scale log2 e
+    uint32_t group, q_heads;
+    int32_t window;           // 0: none
+    uint32_t rows_limit;      // sequences of up to so many rows are sz_attn_rows's
+    uint32_t rows_chunk, rows_splits;      // keys of a chunk, chunks (sz_attn_rows)
+    uint32_t tile_chunk, tile_splits;      // (sz_attn_tiles)
+};
+
+// First key of sequence s that any of its new tokens sees, rounded down.
+__device__ __forceinline__ int32_t first_key(const Sequence &s, int32_t window)
+{
+    const int32_t lo = window > 0 ? max(0, s.len - s.n - window + 1) : 0;
+    return lo & ~(int32_t)(kKeyAlign - 1);
+}
+
+// The visible keys [lo, hi] of position p; none (hi < lo) for p < 0.
+__device__ __forceinline__ void visible(int32_t p, int32_t window, int32_t &lo, int32_t &hi)
+{
+    hi = p;
+    lo = window > 0 ? max(0, p - window + 1) : 0;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ bool any_not_finite(uint32_t w)       // either BF16 of a pair
+{
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// Writes one row's EL consecutive values at d: the result, or a chunk's partial.
+template <int D, int EL>
+__device__ __forceinline__ void store_row(const AttnArgs &a, bool whole, uint32_t split, uint32_t token,
+                                          uint32_t head, uint32_t d, const float (&o)[EL], float inv)
+{
+    const uint64_t r = (uint64_t)token * a.q_heads + head;
+    if (whole) {
+        uint32_t w[EL / 2];
+#pragma unroll
+        for (int e = 0; e < EL / 2; ++e) w[e] = bf16_pair(o[2 * e] * inv, o[2 * e + 1] * inv);
+        uint32_t *p = reinterpret_cast<uint32_t *>(a.out + r * D + d);
+        if constexpr (EL == 8)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+        float *p = a.part + ((uint64_t)split * a.b.tokens * a.q_heads + r) * D + d;
+#pragma unroll
+        for (int e = 0; e < EL; e += 4)
+            *reinterpret_cast<float4 *>(p + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    }
+}
+
+// A row's statistics: its lse, or a chunk's (m', l).
+__device__ __forceinline__ void store_stats(const AttnArgs &a, bool whole, uint32_t split, uint32_t token,
+                                            uint32_t head, bool empty, float m, float l)
+{
+    const uint64_t r = (uint64_t)token * a.q_heads + head;
+    if (!whole)
+        a.part_ml[(uint64_t)split * a.b.tokens * a.q_heads + r] = make_float2(m, l);
+    else if (a.lse)
+        a.lse[r] = empty ? kNone : (m + __log2f(l)) * 0.69314718055994530942f;
+}
+
+// ---------------------------------------------------------------------------
+// sz_attn_rows: at most 16 rows.  A workgroup takes one chunk of one KV
+// head's keys; its four waves take 32-key blocks in turn, each with its own
+// (m', l, o) and no barrier, and meet in LDS at the end.  K and V go straight
+// to registers in 16-byte loads, the next block's issued before the current
+// one is used.  Per 32 keys a wave runs 2 D/32 + D/16 16x16x32 products.
+//   K, 16 keys at a time: lane (key = lane % 16, g = lane / 16) holds d =
+//     32 s + 8 g + 0..7 of step s (FP8: a 16-byte load covers two steps, d =
+//     64 i + 16 g + 8 h + 0..7; q is loaded in the same order).
+//   S^T: lane (row = lane % 16, g) holds keys 16 b + 4 g + 0..3, b = 0, 1.
+//   V: lane (c = lane % 16, g) loads D/16 values of rows 16 b + 4 g + 0..3 at
+//     d = c D/16; byte permutes turn its 8 rows x D/16 values into D/16
+//     operands of 8 keys each.
+// ---------------------------------------------------------------------------
+template <int DT, int D>
+struct KeyBlock {
+    static constexpr int KL = DT == SZ_BF16 ? D / 32 : D / 64;             // 16-byte loads per 16 keys
+    static constexpr int VW = (D / 16) * (DT == SZ_BF16 ? 2 : 1) / 4;      // dwords per lane and V row
+    u32x4 k[2][KL];
+    uint32_t v[8][VW];
+    uint32_t ks[2], vs[2];     // scale bytes: K of the lane's key, V of its four rows
+};
+
+template <int DT, int D>
+__device__ __forceinline__ void load_block(const AttnArgs &a, uint32_t head, const uint32_t (&page)[2], int32_t kb,
+                                           KeyBlock<DT, D> &x)
+{
+    constexpr uint32_t ES = DT == SZ_BF16 ? 2 : 1;
+    const uint32_t lane = lane_id(), m = lane % 16, g = lane / 16;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const uint32_t row0 = (uint32_t)(kb + 16 * b) & ((1u << a.c.lg_page) - 1);
+        const uint64_t kr = row_index(a.c, page[b], 0, head, row0);
+        const uint64_t vr = row_index(a.c, page[b], 1, head, row0);
+        const uint8_t *kp = a.c.data + kr * (D * ES);
+        const uint8_t *vp = a.c.data + vr * (D * ES);
+#pragma unroll
+        for (int i = 0; i < KeyBlock<DT, D>::KL; ++i)
+            x.k[b][i] = *reinterpret_cast<const u32x4 *>(kp + (m * (D * ES) + 64 * i + 16 * g));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t off = (4 * g + r) * (D * ES) + m * (D / 16 * ES);
+            if constexpr (KeyBlock<DT, D>::VW == 4) {
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(vp + off);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x.v[4 * b + r][e] = w[e];
+            } else if constexpr (KeyBlock<DT, D>::VW == 2) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(vp + off);
+                x.v[4 * b + r][0] = w.x;
+                x.v[4 * b + r][1] = w.y;
+            } else {
+                x.v[4 * b + r][0] = *reinterpret_cast<const uint32_t *>(vp + off);
+            }
+        }
+        if constexpr (DT != SZ_BF16) {
+            x.ks[b] = a.c.scales[kr + m];
+            x.vs[b] = *reinterpret_cast<const uint32_t *>(a.c.scales + vr + 4 * g);
+        }
+    }
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_rows(AttnArgs a)
+{
+    using Block = KeyBlock<DT, D>;
+    constexpr int VD = D / 16;                      // d values of a lane
+    __shared__ float lds_o[4][kRowsMax][D + 4];
+    __shared__ float2 lds_ml[4][kRowsMax];
+
+    const uint32_t head = blockIdx.x % a.c.heads;
+    const uint32_t seq = blockIdx.x / a.c.heads % a.b.seqs;
+    const uint32_t split = blockIdx.x / a.c.heads / a.b.seqs;
+    const Sequence s = sequence(a.b, seq);
+    const uint32_t rows = (uint32_t)s.n * a.group;
+    if (s.n == 0 || (uint32_t)s.n > kRowsMax || rows > kRowsMax) return;
+    const bool whole = a.rows_splits == 1;
+    const int64_t begin64 = (int64_t)first_key(s, a.window) + (int64_t)split * a.rows_chunk;
+    if (split > 0 && begin64 >= s.len) return;
+    const int32_t begin = (int32_t)begin64;
+    const int32_t end = (int32_t)min((int64_t)s.len, begin64 + a.rows_chunk);
+
+    const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / 64);
+    const uint32_t n = lane % 16, g = lane / 16;
+    const uint32_t tok = n / a.group;
+    const int32_t pos = s.len - s.n + (int32_t)tok;
+    int32_t lo, hi;
+    visible(pos, a.window, lo, hi);
+    if (n >= rows) {                                // a row that is not there sees what the last one sees
+        visible(s.len - 1, a.window, lo, hi);
+    }
+
+    // q as the products' second operand, in K's order of d
+    bf16x8 q[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        u32x4 w = {0, 0, 0, 0};
+        if (n < rows) {
+            const uint32_t d = DT == SZ_BF16 ? 32 * i + 8 * g : 64 * (i / 2) + 16 * g + 8 * (i % 2);
+            w = *reinterpret_cast<const u32x4 *>(a.q + (uint64_t)(s.start + tok) * a.q_token +
+                                                 (uint64_t)(head * a.group + n % a.group) * a.q_head + d);
+        }
+        q[i] = __builtin_bit_cast(bf16x8, w);
+    }
+
+    f32x4 o[VD];
+#pragma unroll
+    for (int j = 0; j < VD; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = kNone, l = 0.f;
+
+    // pages of a block; positions behind the end take the last position's page (their keys are hidden)
+    auto pages_at = [&](int32_t kb, uint32_t (&page)[2]) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) page[b] = uniform(page_of(a.c, a.b, seq, (uint32_t)min(kb + 16 * b, s.len - 1)));
+    };
+
+    const int32_t all_lo = a.window > 0 ? max(0, s.len - a.window) : 0;      // every row sees [all_lo, all_hi]
+    const int32_t all_hi = s.len - s.n;
+
+    int32_t kb = begin + 32 * (int32_t)wave;
+    Block cur, next;
+    uint32_t page[2];
+    if (kb < end) {
+        pages_at(kb, page);
+        load_block<DT, D>(a, head, page, kb, cur);
+        pages_at(min(kb + 128, s.len - 1), page);
+    }
+    for (; kb < end; kb += 128) {
+        const bool more = kb + 128 < end;
+        if (more) {
+            load_block<DT, D>(a, head, page, kb + 128, next);
+            pages_at(min(kb + 256, s.len - 1), page);
+        }
+
+        // scores
+        f32x4 st[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            st[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                u32x4 w;
+                if constexpr (DT == SZ_BF16) {
+                    w = cur.k[b][i];
+                } else {
+                    const uint32_t sc = cur.ks[b] << 23;
+                    const uint32_t w0 = cur.k[b][i / 2][2 * (i % 2)], w1 = cur.k[b][i / 2][2 * (i % 2) + 1];
+                    w = u32x4{fp8_pair_to_bf16<DT, false>(w0, sc), fp8_pair_to_bf16<DT, true>(w0, sc),
+                              fp8_pair_to_bf16<DT, false>(w1, sc), fp8_pair_to_bf16<DT, true>(w1, sc)};
+                }
+                st[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[i], st[b], 0, 0, 0);
+            }
+        }
+
+        // V rows as BF16
+        uint32_t v[8][VD / 2];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if constexpr (DT == SZ_BF16) {
+#pragma unroll
+                for (int e = 0; e < VD / 2; ++e) v[r][e] = cur.v[r][e];
+            } else {
+                const uint32_t sc = ((cur.vs[r / 4] >> (8 * (r % 4))) & 0xFFu) << 23;
+#pragma unroll
+                for (int e = 0; e < VD / 4; ++e) {
+                    v[r][2 * e] = fp8_pair_to_bf16<DT, false>(cur.v[r][e], sc);
+                    v[r][2 * e + 1] = fp8_pair_to_bf16<DT, true>(cur.v[r][e], sc);
+                }
+            }
+        }
+
+        // Hidden keys: their scores are -inf whatever K holds; V rows that no
+        // row sees (behind the end, before the window) become zeros, since 0
+        // times a NaN is one.  Rows that some see are checked further down.
+        const bool masked = kb < all_lo || kb + 31 > all_hi;
+        bool wild = false;
+        if (masked) {
+            const int32_t any_lo = a.window > 0 ? max(0, all_hi - a.window + 1) : 0;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int32_t key = kb + 16 * (r / 4) + 4 * (int32_t)g + r % 4;
+                if (key < lo || key > hi) st[r / 4][r % 4] = kNone;
+                const bool dead = key < any_lo || key >= s.len;
+#pragma unroll
+                for (int e = 0; e < VD / 2; ++e) {
+                    if (dead) v[r][e] = 0;
+                    wild = wild || any_not_finite(v[r][e]);
+                }
+            }
+            wild = __any(wild);
+        }
+
+        // running maximum, raised only when some row needs it
+        float top = kNone;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) top = fmaxf(top, st[r / 4][r % 4]);
+        top *= a.c2;
+        if (__any(top > m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float raised = fmaxf(m, top);
+            const float f = raised == kNone ? 1.f : exp2_fast(m - raised);
+            m = raised;
+            l *= f;
+#pragma unroll
+            for (int j = 0; j < VD; ++j) o[j] *= f;
+        }
+        const float base = m == kNone ? 0.f : m;
+        float p[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            p[r] = exp2_fast(__builtin_fmaf(st[r / 4][r % 4], a.c2, -base));
+            l += p[r];
+        }
+        const u32x4 pw = {bf16_pair(p[0], p[1]), bf16_pair(p[2], p[3]), bf16_pair(p[4], p[5]), bf16_pair(p[6], p[7])};
+        const bf16x8 pb = __builtin_bit_cast(bf16x8, pw);
+
+        if (__builtin_expect(!wild, 1)) {
+#pragma unroll
+            for (int j = 0; j < VD; ++j) {
+                const uint32_t sel = j % 2 ? 0x07060302u : 0x05040100u;
+                const u32x4 w = {perm(v[1][j / 2], v[0][j / 2], sel), perm(v[3][j / 2], v[2][j / 2], sel),
+                                 perm(v[5][j / 2], v[4][j / 2], sel), perm(v[7][j / 2], v[6][j / 2], sel)};
+                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pb, o[j], 0, 0, 0);
+            }
+        } else {
+            // NaN or infinity in a row that is hidden from some rows: one row
+            // at a time, with the V rows that it sees and zeros for the others.
+#pragma unroll 1
+            for (uint32_t row = 0; row < rows; ++row) {
+                const int32_t rlo = __shfl(lo, (int)row, 64), rhi = __shfl(hi, (int)row, 64);
+                uint32_t even = 0x05040100u;
+                asm volatile("" : "+s"(even));       // built again for each row: not kept in registers for all
+#pragma unroll
+                for (int j = 0; j < VD; ++j) {
+                    const uint32_t sel = even + (j % 2 ? 0x02020202u : 0u);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int32_t key = kb + 16 * (e / 2) + 4 * (int32_t)g + 2 * (e % 2);
+                        const uint32_t keep = (key >= rlo && key <= rhi ? 0x0000FFFFu : 0u) |
+                                              (key + 1 >= rlo && key + 1 <= rhi ? 0xFFFF0000u : 0u);
+                        w[e] = perm(v[2 * e + 1][j / 2], v[2 * e][j / 2], sel) & keep;
+                    }
+                    const u32x4 ww = {w[0], w[1], w[2], w[3]};
+                    const f32x4 t =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ww), pb, o[j], 0, 0, 0);
+                    if (n == row) o[j] = t;
+                }
+            }
+        }
+        if (more) cur = next;
+    }
+
+    // the four waves' sums meet in LDS
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (g == 0) lds_ml[wave][n] = make_float2(m, l);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < VD; j += 4)
+            *reinterpret_cast<float4 *>(&lds_o[wave][n][(4 * g + r) * VD + j]) =
+                make_float4(o[j][r], o[j + 1][r], o[j + 2][r], o[j + 3][r]);
+    __syncthreads();
+    const uint32_t row = threadIdx.x / 16, d = threadIdx.x % 16 * VD;
+    if (row >= rows) return;
+    float mw[4], top = kNone, sum = 0.f, acc[VD];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        mw[w] = lds_ml[w][row].x;
+        top = fmaxf(top, mw[w]);
+    }
+    const float base = top == kNone ? 0.f : top;
+#pragma unroll
+    for (int j = 0; j < VD; ++j) acc[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = exp2_fast(mw[w] - base);
+        sum += lds_ml[w][row].y * f;
+#pragma unroll
+        for (int j = 0; j < VD; ++j) acc[j] += lds_o[w][row][d + j] * f;
+    }
+    const uint32_t rtok = row / a.group;
+    const bool empty = s.len - s.n + (int32_t)rtok < 0;
+    const uint32_t rhead = head * a.group + row % a.group;
+    store_row<D, VD>(a, whole, split, s.start + rtok, rhead, d, acc, empty ? 0.f : 1.f / sum);
+    if (d == 0) store_stats(a, whole, split, s.start + rtok, rhead, empty, top, sum);
+}
+
+// ---------------------------------------------------------------------------
+// sz_attn_tiles: 128 rows of one KV head, a wave 32 of them, over 64-key
+// tiles in LDS, two tiles deep.  BF16 tiles go from HBM to LDS without
+// registers (16 bytes a lane, whole rows; the lane picks which 16 bytes of
+// the row it fetches so that the LDS reads meet no bank twice); FP8 tiles
+// pass through registers, where one instruction converts and scales two
+// values, once for all four waves.  Products are 32x32x16: K rows from LDS as
+// 16-byte reads, V transposed on the way out of LDS.
+//   S^T: lane (row = lane % 32, g = lane / 32) holds keys 32 b + 8 i + 4 g +
+//     0..3, b = 0, 1, i = 0..3.
+// ---------------------------------------------------------------------------
+// 16-byte pieces of a row are stored at piece ^ swizzle(row): K reads take
+// the same piece of 32 rows, V reads four pieces of 8 rows.
+template <int D>
+__device__ __forceinline__ uint32_t k_swizzle(uint32_t row)
+{
+    return D == 128 ? row & 15u : (row >> 1) & 7u;
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_swizzle(uint32_t row)
+{
+    return D == 128 ? (row & 3u) << 2 : (row & 2u) << 1;
+}
+
+template <int D>
+struct TileLds {
+    uint16_t k[2][kTileKeys * D];
+    uint16_t v[2][kTileKeys * D];
+    uint32_t wild;
+};
+
+template <int DT, int D>
+struct TileRegs {               // an FP8 tile on its way: 32 values of one K and one V row per lane (D = 128)
+    static constexpr int W = D / 64;
+    u32x4 k[W], v[W];
+    uint32_t ks, vs;
+};
+
+// BF16: wave w fetches rows 16 w .. 16 w + 15 of the tile.
+template <int D>
+__device__ __forceinline__ void fetch_tile_bf16(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0,
+                                                uint32_t wave, uint16_t *k, uint16_t *v)
+{
+    constexpr uint32_t PIECES = D / 8, RPI = 64 / PIECES;       // 16-byte pieces of a row, rows per instruction
+    const uint32_t lane = lane_id();
+    const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
+    const uint16_t *kp = reinterpret_cast<const uint16_t *>(a.c.data) + row_index(a.c, page, 0, head, row0) * D;
+    const uint16_t *vp = reinterpret_cast<const uint16_t *>(a.c.data) + row_index(a.c, page, 1, head, row0) * D;
+#pragma unroll
+    for (uint32_t i = 0; i < 16 / RPI; ++i) {
+        const uint32_t r = i * RPI + lane / PIECES;              // of this wave's 16
+        const uint32_t row = 16 * wave + r;
+        const uint32_t at = (16 * wave + i * RPI) * D;
+        typedef __attribute__((address_space(3))) void *lds_ptr;
+        typedef const __attribute__((address_space(1))) void *global_ptr;
+        __builtin_amdgcn_global_load_lds((global_ptr)(kp + r * D + 8 * ((lane % PIECES) ^ k_swizzle<D>(row))),
+                                         (lds_ptr)(k + at), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((global_ptr)(vp + r * D + 8 * ((lane % PIECES) ^ v_swizzle<D>(row))),
+                                         (lds_ptr)(v + at), 16, 0, 0);
+    }
+}
+
+// FP8: thread t loads a quarter of row t / 4.
+template <int DT, int D>
+__device__ __forceinline__ void fetch_tile_fp8(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0,
+                                               TileRegs<DT, D> &x)
+{
+    const uint32_t r = lane_id() / 4, piece = lane_id() % 4;
+    const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
+    const uint64_t kr = row_index(a.c, page, 0, head, row0) + r, vr = row_index(a.c, page, 1, head, row0) + r;
+#pragma unroll
+    for (int i = 0; i < TileRegs<DT, D>::W; ++i) {
+        x.k[i] = *reinterpret_cast<const u32x4 *>(a.c.data + kr * D + piece * (D / 4) + 16 * i);
+        x.v[i] = *reinterpret_cast<const u32x4 *>(a.c.data + vr * D + piece * (D / 4) + 16 * i);
+    }
+    x.ks = a.c.scales[kr];
+    x.vs = a.c.scales[vr];
+}
+
+template <int DT, int D>
+__device__ __forceinline__ void place_tile_fp8(const TileRegs<DT, D> &x, uint32_t wave, uint16_t *k, uint16_t *v)
+{
+    const uint32_t row = 16 * wave + lane_id() / 4, piece = lane_id() % 4;
+    const uint32_t ks = x.ks << 23, vs = x.vs << 23;
+#pragma unroll
+    for (int i = 0; i < TileRegs<DT, D>::W; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t c = piece * (D / 32) + 2 * i + e;     // 16-byte piece of the BF16 row
+            const uint32_t k0 = x.k[i][2 * e], k1 = x.k[i][2 * e + 1], v0 = x.v[i][2 * e], v1 = x.v[i][2 * e + 1];
+            *reinterpret_cast<u32x4 *>(k + row * D + 8 * (c ^ k_swizzle<D>(row))) =
+                u32x4{fp8_pair_to_bf16<DT, false>(k0, ks), fp8_pair_to_bf16<DT, true>(k0, ks),
+                      fp8_pair_to_bf16<DT, false>(k1, ks), fp8_pair_to_bf16<DT, true>(k1, ks)};
+            *reinterpret_cast<u32x4 *>(v + row * D + 8 * (c ^ v_swizzle<D>(row))) =
+                u32x4{fp8_pair_to_bf16<DT, false>(v0, vs), fp8_pair_to_bf16<DT, true>(v0, vs),
+                      fp8_pair_to_bf16<DT, false>(v1, vs), fp8_pair_to_bf16<DT, true>(v1, vs)};
+        }
+}
+
+// V^T of 16 keys and 32 d as a product's first operand: keys base + 4 g + 0..3
+// and base + 8 + 4 g + 0..3 of d = 32 db + lane % 32.  Each 16 lanes of a
+// transposing read take 4 rows x 16 d.
+template <int D>
+__device__ __forceinline__ bf16x8 v_operand(const uint16_t *v, uint32_t base, uint32_t db)
+{
+    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+    const uint32_t lane = lane_id(), i = lane % 16, g = lane / 32, half = lane / 16 % 2;
+    const uint32_t col = 32 * db + 16 * half + 4 * (i % 4);
+    const uint32_t r0 = base + 4 * g + i / 4, r1 = r0 + 8;
+    const s16x4 w0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_ptr)(v + r0 * D + 8 * ((col / 8) ^ v_swizzle<D>(r0)) + col % 8));
+    const s16x4 w1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_ptr)(v + r1 * D + 8 * ((col / 8) ^ v_swizzle<D>(r1)) + col % 8));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uint32_t slots)
+{
+    constexpr int DB = D / 32;
+    __shared__ TileLds<D> lds;
+
+    const uint32_t head = blockIdx.x % a.c.heads;
+    const uint32_t slot = slots - 1 - blockIdx.x / a.c.heads % slots;          // later tiles see more keys: first
+    const uint32_t split = blockIdx.x / a.c.heads / slots;
+
+    // Sequence i owns the slots from floor(starts[i] G / 128) + i on: at least as many as its rows fill.
+    const auto first_slot = [&](uint32_t i) {
+        return (int64_t)(((uint64_t)(uint32_t)max(a.b.starts[i], 0) * a.group) / kTileRows) + i;
+    };
+    const int32_t found = wave_last_not_above(a.b.seqs, slot, first_slot);
+    if (found < 0) return;
+    const uint32_t seq = uniform((uint32_t)found);
+    const Sequence s = sequence(a.b, seq);
+    const uint64_t all_rows = (uint64_t)s.n * a.group;
+    if (all_rows <= a.rows_limit) return;                                      // none, or sz_attn_rows takes them
+    const uint64_t row0 = (uint64_t)(slot - first_slot(seq)) * kTileRows;
+    if (row0 >= all_rows) return;
+    const uint32_t rows = (uint32_t)min((uint64_t)kTileRows, all_rows - row0);
+
+    const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / 64);
+    const uint32_t n = lane % 32, g = lane / 32;
+    const int32_t tok_first = (int32_t)(row0 / a.group), tok_last = (int32_t)((row0 + rows - 1) / a.group);
+    const uint64_t my_row = row0 + min(wave * 32 + n, rows - 1);
+    const bool mine = wave * 32 + n < rows;
+    const int32_t tok = (int32_t)(my_row / a.group);
+    const uint32_t q_head = head * a.group + (uint32_t)(my_row % a.group);
+    const int32_t pos = s.len - s.n + tok;
+    int32_t lo, hi;
+    visible(pos, a.window, lo, hi);
+
+    // the keys of this tile of rows, and of its chunk
+    const int32_t p_first = s.len - s.n + tok_first, p_last = s.len - s.n + tok_last;
+    const bool whole = a.tile_splits == 1;
+    const int64_t chunk0 = (int64_t)first_key(s, a.window) + (int64_t)split * a.tile_chunk;
+    const int32_t any_lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;  // some row sees [any_lo, p_last]
+    const int32_t begin = (int32_t)max(chunk0, (int64_t)(any_lo & ~(int32_t)(kTileKeys - 1)));
+    const int32_t end = (int32_t)min((int64_t)p_last + 1, chunk0 + a.tile_chunk);
+    if (!whole && begin >= end) return;                                        // no row's chunk: nobody reads it
+    const int32_t all_lo = a.window > 0 ? max(0, p_last - a.window + 1) : 0;   // every row sees [all_lo, p_first]
+
+    bf16x8 q[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        u32x4 w = {0, 0, 0, 0};
+        if (mine)
+            w = *reinterpret_cast<const u32x4 *>(a.q + (uint64_t)(s.start + tok) * a.q_token +
+                                                 (uint64_t)q_head * a.q_head + 16 * i + 8 * g);
+        q[i] = __builtin_bit_cast(bf16x8, w);
+    }
+
+    f32x16 o[DB];
+#pragma unroll
+    for (int j = 0; j < DB; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[j][r] = 0.f;
+    float m = kNone, l = 0.f;
+
+    // A wave fetches 16 rows of a tile: one page (or part of one).  Rows behind
+    // the sequence's end come from its last page and are hidden.
+    const auto page_at = [&](int32_t key) {
+        return uniform(page_of(a.c, a.b, seq, (uint32_t)min(key, s.len - 1)));
+    };
+    TileRegs<DT, D> regs;
+    uint32_t page = 0;
+    if (begin < end) {
+        page = page_at(begin + 16 * (int32_t)wave);
+        if constexpr (DT == SZ_BF16) {
+            fetch_tile_bf16<D>(a, head, page, begin + 16 * (int32_t)wave, wave, lds.k[0], lds.v[0]);
+        } else {
+            fetch_tile_fp8<DT, D>(a, head, page, begin + 16 * (int32_t)wave, regs);
+            place_tile_fp8<DT, D>(regs, wave, lds.k[0], lds.v[0]);
+        }
+        page = page_at(begin + (int32_t)kTileKeys + 16 * (int32_t)wave);
+    }
+    uint32_t buf = 0;
+    for (int32_t kb = begin; kb < end; kb += kTileKeys, buf ^= 1) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                       // this wave's loads into LDS are done
+        __syncthreads();                                                       // this tile is in LDS, the other is free
+        const bool more = kb + (int32_t)kTileKeys < end;
+        if (more) {
+            const int32_t key0 = kb + (int32_t)kTileKeys + 16 * (int32_t)wave;
+            if constexpr (DT == SZ_BF16)
+                fetch_tile_bf16<D>(a, head, page, key0, wave, lds.k[buf ^ 1], lds.v[buf ^ 1]);
+            else
+                fetch_tile_fp8<DT, D>(a, head, page, key0, regs);
+            page = page_at(key0 + (int32_t)kTileKeys);
+        }
+        const uint16_t *kt = lds.k[buf];
+        uint16_t *vt = lds.v[buf];
+
+        // scores
+        f32x16 st[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) st[b][r] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t row = 32 * b + n;
+                const u32x4 w =
+                    *reinterpret_cast<const u32x4 *>(kt + row * D + 8 * ((uint32_t)(2 * i + g) ^ k_swizzle<D>(row)));
+                st[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), q[i], st[b], 0, 0, 0);
+            }
+        }
+
+        // Hidden keys, as in sz_attn_rows: -inf scores; V rows that no row of
+        // this tile sees become zeros in LDS; NaN or infinity in V rows that
+        // only some see takes the slow path.
+        const bool masked = kb < all_lo || kb + (int32_t)kTileKeys - 1 > p_first;
+        bool wild = false;
+        if (masked) {
+            if (threadIdx.x == 0) lds.wild = 0;
+            __syncthreads();
+            const uint32_t row = threadIdx.x / 4;
+            const int32_t key = kb + (int32_t)row;
+            const bool dead = key < any_lo || key > p_last;
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                u32x4 *p = reinterpret_cast<u32x4 *>(vt + row * D + (threadIdx.x % 4) * (D / 4) + 8 * i);
+                if (dead)
+                    *p = u32x4{0, 0, 0, 0};
+                else {
+                    const u32x4 w = *p;
+                    bad = bad || any_not_finite(w[0]) || any_not_finite(w[1]) || any_not_finite(w[2]) ||
+                          any_not_finite(w[3]);
+                }
+            }
+            if (bad) lds.wild = 1;
+            __syncthreads();
+            wild = lds.wild != 0;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int32_t k = kb + 32 * b + 8 * (r / 4) + 4 * (int32_t)g + r % 4;
+                    if (k < lo || k > hi) st[b][r] = kNone;
+                }
+        }
+
+        // running maximum
+        float top = kNone;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, st[b][r]);
+        top *= a.c2;
+        if (__any(top > m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float raised = fmaxf(m, top);
+            const float f = raised == kNone ? 1.f : exp2_fast(m - raised);
+            m = raised;
+            l *= f;
+#pragma unroll
+            for (int j = 0; j < DB; ++j) o[j] *= f;
+        }
+        const float base = m == kNone ? 0.f : m;
+        bf16x8 p[2][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p0 = exp2_fast(__builtin_fmaf(st[b][8 * t + 2 * e], a.c2, -base));
+                    const float p1 = exp2_fast(__builtin_fmaf(st[b][8 * t + 2 * e + 1], a.c2, -base));
+                    l += p0 + p1;
+                    w[e] = bf16_pair(p0, p1);
+                }
+                p[b][t] = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+            }
+
+        if (__builtin_expect(!wild, 1)) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < DB; ++j)
+                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_operand<D>(vt, 32 * b + 16 * t, j), p[b][t],
+                                                                        o[j], 0, 0, 0);
+        } else {
+#pragma unroll 1
+            for (uint32_t row = 0; row < 32; ++row) {
+                const int32_t rlo = __shfl(lo, (int)row, 64), rhi = __shfl(hi, (int)row, 64);
+                asm volatile("" ::: "memory");       // read again for each row: not kept in registers for all
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int j = 0; j < DB; ++j) {
+                            u32x4 w = __builtin_bit_cast(u32x4, v_operand<D>(vt, 32 * b + 16 * t, j));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int32_t k = kb + 32 * b + 16 * t + 8 * (e / 2) + 4 * (int32_t)g + 2 * (e % 2);
+                                w[e] &= (k >= rlo && k <= rhi ? 0x0000FFFFu : 0u) |
+                                        (k + 1 >= rlo && k + 1 <= rhi ? 0xFFFF0000u : 0u);
+                            }
+                            const f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
+                                                                                     p[b][t], o[j], 0, 0, 0);
+                            if (n == row) o[j] = x;
+                        }
+            }
+        }
+        if constexpr (DT != SZ_BF16)
+            if (more) place_tile_fp8<DT, D>(regs, wave, lds.k[buf ^ 1], lds.v[buf ^ 1]);
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (!mine) return;
+    const bool empty = pos < 0;
+    const float inv = empty ? 0.f : 1.f / l;
+#pragma unroll
+    for (int j = 0; j < DB; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float w[4] = {o[j][4 * i], o[j][4 * i + 1], o[j][4 * i + 2], o[j][4 * i + 3]};
+            store_row<D, 4>(a, whole, split, s.start + tok, q_head, 32 * j + 8 * i + 4 * g, w, inv);
+        }
+    if (g == 0) store_stats(a, whole, split, s.start + tok, q_head, empty, m, l);
+}
+
+// ---------------------------------------------------------------------------
+// sz_attn_join: a wave joins the chunks of one (token, head) row that hold
+// visible keys, in order:  M = max m'_s;  o = sum 2^(m'_s - M) o_s / sum
+// 2^(m'_s - M) l_s.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a)
+{
+    const uint64_t r = (uint64_t)blockIdx.x * (kAttnThreads / 64) + uniform(threadIdx.x / 64);
+    const uint32_t t = (uint32_t)(r / a.q_heads), head = (uint32_t)(r % a.q_heads);
+    if (t >= a.b.tokens) return;
+    const int32_t i = wave_last_not_above(a.b.seqs + 1, t, [&](uint32_t j) { return (int64_t)a.b.starts[j]; });
+    if (i < 0 || i >= (int32_t)a.b.seqs) return;
+    const Sequence s = sequence(a.b, uniform((uint32_t)i));
+    if ((int32_t)t < s.start || (int32_t)t >= s.start + s.n) return;
+    const bool few = (uint64_t)s.n * a.group <= a.rows_limit;
+    if ((few ? a.rows_splits : a.tile_splits) == 1) return;                    // already whole
+    const uint32_t chunk = few ? a.rows_chunk : a.tile_chunk;
+    int32_t lo, hi;
+    visible(s.len - s.n + ((int32_t)t - s.start), a.window, lo, hi);
+    const bool empty = hi < 0;
+    const int32_t first = first_key(s, a.window);
+    const uint32_t s0 = empty ? 0 : (uint32_t)(lo - first) / chunk, s1 = empty ? 0 : (uint32_t)(hi - first) / chunk + 1;
+
+    const uint32_t lane = lane_id();
+    const uint64_t stride = (uint64_t)a.b.tokens * a.q_heads;
+    float top = kNone;
+    for (uint32_t k = s0 + lane; k < s1; k += 64) top = fmaxf(top, a.part_ml[k * stride + r].x);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d, 64));
+    const float base = top == kNone ? 0.f : top;
+    float o[2] = {0.f, 0.f}, l = 0.f;
+    constexpr uint32_t E = D / 64;                                             // values of a lane
+#pragma unroll 4
+    for (uint32_t k = s0; k < s1; ++k) {
+        const float2 ml = a.part_ml[k * stride + r];
+        const float *p = a.part + (k * stride + r) * D + lane * E;
+        const float f = exp2_fast(ml.x - base);
+        l += ml.y * f;
+        if constexpr (E == 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(p);
+            o[0] += v.x * f;
+            o[1] += v.y * f;
+        } else {
+            o[0] += *p * f;
+        }
+    }
+    const float inv = empty ? 0.f : 1.f / l;
+    uint16_t *out = a.out + r * D + lane * E;
+    if constexpr (E == 2)
+        *reinterpret_cast<uint32_t *>(out) = bf16_pair(o[0] * inv, o[1] * inv);
+    else
+        *out = (uint16_t)bf16_pair(o[0] * inv, 0.f);
+    if (lane == 0) store_stats(a, true, 0, t, head, empty, top, l);
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+struct AttnPlan {
+    bool rows, tiles;                 // which kernels the batch can need
+    uint32_t rows_chunk, rows_splits, tile_chunk, tile_splits, slots;
+};
+
+constexpr uint64_t kRowsGroups = 1024;        // workgroups that sz_attn_rows wants
+constexpr uint32_t kRowsMinChunk = 256;
+constexpr uint64_t kTileGroups = 512;
+constexpr uint32_t kTileMinChunk = 512;
+
+uint64_t splits_wanted(uint64_t groups, uint64_t want) { return std::max<uint64_t>(1, want / groups); }
+
+// Splits of `span` keys so that `groups` workgroups become `want`, in chunks
+// of at least `least` keys.
+void split_keys(uint64_t span, uint64_t groups, uint64_t want, uint32_t least, uint32_t &chunk, uint32_t &splits)
+{
+    const uint64_t n = splits_wanted(groups, want);
+    uint64_t c = std::max<uint64_t>(least, (span + n - 1) / n);
+    c = (c + 127) / 128 * 128;
+    chunk = (uint32_t)c;
+    splits = (uint32_t)std::max<uint64_t>(1, (span + c - 1) / c);
+}
+
+AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint32_t window)
+{
+    AttnPlan p{};
+    // chunks start at a multiple of kKeyAlign: up to kKeyAlign - 1 keys more than the visible ones
+    uint64_t span = b.max_kv;
+    if (window) span = std::min<uint64_t>(span, (uint64_t)window + b.max_new + kKeyAlign - 1);
+    p.tiles = (uint64_t)b.max_new * group > kRowsMax;
+    p.rows = !p.tiles || b.seqs > 1;      // a single sequence's rows all go the same way
+    p.slots = (uint32_t)std::min<uint64_t>((uint64_t)b.tokens * group / kTileRows + b.seqs, 0x7FFFFFFFu);
+    p.rows_splits = p.tile_splits = 1;
+    if (p.rows)
+        split_keys(span, (uint64_t)b.seqs * c->kv_heads, kRowsGroups, kRowsMinChunk, p.rows_chunk, p.rows_splits);
+    if (p.tiles)
+        split_keys(span, (uint64_t)p.slots * c->kv_heads, kTileGroups, kTileMinChunk, p.tile_chunk, p.tile_splits);
+    return p;
+}
+
+uint64_t attn_ws_bytes(uint32_t splits, uint64_t rows, uint32_t head_dim)
+{
+    return splits == 1 ? 0 : up256(splits * rows * head_dim * 4) + up256(splits * rows * 8);
+}
+
+template <int DT, int D>
+int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
+{
+    if (p.rows) {
+        const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits;
+        if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
+        LaunchScope scope("sz_attn_rows", s);
+        hipLaunchKernelGGL((sz_attn_rows<DT, D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+    }
+    if (p.tiles) {
+        const uint64_t groups = (uint64_t)a.c.heads * p.slots * p.tile_splits;
+        if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
+        LaunchScope scope("sz_attn_tiles", s);
+        hipLaunchKernelGGL((sz_attn_tiles<DT, D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a, p.slots);
+    }
+    if (p.rows_splits > 1 || p.tile_splits > 1) {
+        const uint64_t groups = ((uint64_t)a.b.tokens * a.q_heads + 3) / 4;
+        if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
+        LaunchScope scope("sz_attn_join", s);
+        hipLaunchKernelGGL((sz_attn_join<D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+    }
+    return hipGetLastError() == hipSuccess ? SZ_OK : SZ_E_HIP;
+}
+
+}  // namespace
+}  // namespace sz
+
+using namespace sz;
+
+extern "C" uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, const sz_batch *batch, uint32_t q_heads)
+{
+    if (!cache || !batch || cache->kv_heads == 0 || q_heads == 0 || q_heads % cache->kv_heads) return 0;
+    PagedBatch b{};
+    b.seqs = batch->seqs;
+    b.tokens = batch->tokens;
+    b.max_new = std::min(batch->max_new, batch->tokens);
+    b.max_kv = batch->max_kv;
+    if (b.seqs == 0 || b.tokens == 0) return 256;
+    // the most chunks that any window gives
+    const AttnPlan p = attn_plan(cache, b, q_heads / cache->kv_heads, 0);
+    uint64_t splits = 1;
+    if (p.rows)
+        splits = std::max(splits, std::min(splits_wanted((uint64_t)b.seqs * cache->kv_heads, kRowsGroups),
+                                           ((uint64_t)b.max_kv + kRowsMinChunk - 1) / kRowsMinChunk));
+    if (p.tiles)
+        splits = std::max(splits, std::min(splits_wanted((uint64_t)p.slots * cache->kv_heads, kTileGroups),
+                                           ((uint64_t)b.max_kv + kTileMinChunk - 1) / kTileMinChunk));
+    return std::max<uint64_t>(256, attn_ws_bytes((uint32_t)splits, (uint64_t)b.tokens * q_heads, cache->head_dim));
+}
+
+extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void *d_q, uint32_t q_heads,
+                                  uint64_t q_token_stride, uint64_t q_head_stride, float scale, uint32_t window,
+                                  void *d_out, float *d_lse, void *d_ws, uint64_t ws_bytes, int32_t *d_status,
+                                  void *stream)
+{
+    AttnArgs a{};
+    int rc = check_paged(cache, batch, d_status, a.c, a.b);
+    if (rc != SZ_OK) return rc;
+    if (q_heads == 0 || q_heads > 0xFFFFu || q_heads % a.c.heads) return SZ_E_ARG;
+    if (!(scale > 0.f) || !(scale <= 3.4e38f) || window > 0x7FFFFFFFu) return SZ_E_ARG;
+    if ((rc = check_rows(d_q, q_token_stride, q_head_stride, a.b.tokens, q_heads)) != SZ_OK) return rc;
+    if (a.b.tokens && !d_out) return SZ_E_ARG;
+    if (!aligned16(d_out) || !aligned16(d_ws) || (reinterpret_cast<uintptr_t>(d_lse) & 3u)) return SZ_E_ALIGN;
+    if (a.b.tokens == 0 || a.b.seqs == 0 || a.b.max_new == 0) return SZ_OK;
+    a.group = q_heads / a.c.heads;
+    const AttnPlan p = attn_plan(cache, a.b, a.group, window);
+    const uint32_t splits = std::max(p.rows_splits, p.tile_splits);
+    const uint64_t rows = (uint64_t)a.b.tokens * q_heads;
+    if (splits > 1 && !d_ws) return SZ_E_ARG;
+    if (ws_bytes < attn_ws_bytes(splits, rows, cache->head_dim)) return SZ_E_WORKSPACE;
+    a.q = static_cast<const uint16_t *>(d_q);
+    a.q_token = q_token_stride;
+    a.q_head = q_head_stride;
+    a.out = static_cast<uint16_t *>(d_out);
+    a.lse = d_lse;
+    a.part = static_cast<float *>(d_ws);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(d_ws) + up256(splits * rows * cache->head_dim * 4));
+    a.c2 = scale * 1.44269504088896340736f;
+    a.q_heads = q_heads;
+    a.window = (int32_t)window;
+    a.rows_limit = p.rows ? kRowsMax : 0;
+    a.rows_chunk = p.rows_chunk;
+    a.rows_splits = p.rows_splits;
+    a.tile_chunk = p.tile_chunk;
+    a.tile_splits = p.tile_splits;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const bool wide = cache->head_dim == 128;
+    switch (cache->dtype) {
+    case SZ_BF16: return wide ? launch_attention<SZ_BF16, 128>(a, p, s) : launch_attention<SZ_BF16, 64>(a, p, s);
+    case SZ_FP8_E5M2:
+        return wide ? launch_attention<SZ_FP8_E5M2, 128>(a, p, s) : launch_attention<SZ_FP8_E5M2, 64>(a, p, s);
+    default: return wide ? launch_attention<SZ_FP8_E4M3, 128>(a, p, s) : launch_attention<SZ_FP8_E4M3, 64>(a, p, s);
+    }
+}

@@ -1,0 +1,278 @@
+"""The paged KV cache: writing new tokens' K and V into pages, reading them
+back, and attention of new tokens over the pages (sz_cache_write,
+sz_cache_read, sz_paged_attention in include/splitzip.h).
+
+A ``PagedCache`` is one layer's ``[pages, 2, kv_heads, page_tokens, head_dim]``
+tensor (keys, then values) of BF16, E5M2 or E4M3, with a scale byte for each
+FP8 row.  E5M2 and BF16 pages are the codec's element types:
+``encode(cache.data[first:last], codebook)`` compresses pages as they lie.
+
+A ``PageBatch`` says which tokens a call is about: sequence i has
+``kv_lens[i]`` tokens in the cache, the new ones included, and its new tokens
+are ``starts[i]:starts[i + 1]`` of the packed axis of k, v, q and outputs.
+The three arrays stay on the device; they may be changed in place between
+calls and between replays of a captured graph.
+
+Every call only enqueues unless ``check`` is true, which waits for the device
+and raises ``SplitZipError`` if the batch was found wrong.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _native
+from ._native import SZ_BF16, SZ_FP8_E4M3, SZ_FP8_E5M2, SplitZipError
+
+E4M3 = SZ_FP8_E4M3
+
+_ELEMENT = {SZ_BF16: torch.bfloat16, SZ_FP8_E5M2: torch.float8_e5m2, SZ_FP8_E4M3: torch.float8_e4m3fn}
+
+
+class PagedCache:
+    """One layer's pages.  ``data``: a contiguous device tensor ``[pages, 2,
+    kv_heads, page_tokens, head_dim]`` of the element type (FP8 also as
+    ``uint8``); ``scales``: ``uint8`` ``[pages, 2, kv_heads, page_tokens]``
+    for FP8, None for BF16.  The tensors stay the caller's.  ``status`` is the
+    device int32 that the calls report into."""
+
+    def __init__(self, dtype: int, data: torch.Tensor, scales: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None):
+        if dtype not in _ELEMENT:
+            raise ValueError("a paged cache holds BF16, E5M2 or E4M3, got dtype %r" % (dtype,))
+        if data.dtype != _ELEMENT[dtype] and not (dtype != SZ_BF16 and data.dtype == torch.uint8):
+            raise TypeError("data is %s, the cache's element type is %s" % (data.dtype, _ELEMENT[dtype]))
+        if data.dim() != 5 or data.shape[1] != 2 or not data.is_contiguous():
+            raise ValueError("data is a contiguous [pages, 2, kv_heads, page_tokens, head_dim] tensor")
+        if dtype == SZ_BF16:
+            if scales is not None:
+                raise ValueError("a BF16 cache has no scales")
+        else:
+            if scales is None:
+                raise ValueError("an FP8 cache needs scales")
+            if scales.dtype != torch.uint8 or scales.shape != data.shape[:-1] or not scales.is_contiguous():
+                raise ValueError("scales is a contiguous uint8 tensor of data's shape without the last axis")
+            if scales.device != data.device:
+                raise ValueError("data and scales are on different devices")
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=data.device)
+        elif status.dtype != torch.int32 or status.numel() != 1 or status.device != data.device:
+            raise ValueError("status is one int32 on the cache's device")
+        self.dtype, self.data, self.scales, self.status = dtype, data, scales, status
+        self.device = data.device
+        self.pages, _, self.kv_heads, self.page_tokens, self.head_dim = data.shape
+        c = _native.sz_cache(dtype, self.page_tokens, self.kv_heads, self.head_dim, self.pages, data.data_ptr(),
+                             scales.data_ptr() if scales is not None else None)
+        self._c, self._ref, self._status = c, ctypes.byref(c), status.data_ptr()
+
+    def raise_status(self) -> None:
+        """Waits for the current stream, raises if a call found its batch
+        wrong, and clears the word."""
+        status = int(self.status.item())
+        if status != 0:
+            self.status.zero_()
+            raise SplitZipError("paged cache (device check of the batch)", status)
+
+
+def paged_cache(pages: int, page_tokens: int, kv_heads: int, head_dim: int, dtype: int = SZ_BF16,
+                device="cuda") -> PagedCache:
+    """An empty cache; every row reads as zeros."""
+    if dtype not in _ELEMENT:
+        raise ValueError("a paged cache holds BF16, E5M2 or E4M3, got dtype %r" % (dtype,))
+    shape = (pages, 2, kv_heads, page_tokens, head_dim)
+    if dtype == SZ_BF16:
+        return PagedCache(dtype, torch.zeros(shape, dtype=torch.bfloat16, device=device))
+    data = torch.zeros(shape, dtype=torch.uint8, device=device).view(_ELEMENT[dtype])
+    return PagedCache(dtype, data, torch.full(shape[:-1], 127, dtype=torch.uint8, device=device))
+
+
+class PageBatch:
+    """The tokens of a call.  ``page_table`` int32 ``[seqs, width]``,
+    ``kv_lens`` int32 ``[seqs]``, ``starts`` int32 ``[seqs + 1]``, contiguous,
+    on one device; ``tokens`` the length of the packed axis.  ``max_new`` and
+    ``max_kv`` bound a sequence's new tokens and length; without them the
+    launches are shaped for ``tokens`` and for full tables."""
+
+    def __init__(self, page_table: torch.Tensor, kv_lens: torch.Tensor, starts: torch.Tensor, tokens: int,
+                 max_new: int | None = None, max_kv: int | None = None):
+        if page_table.dim() != 2:
+            raise ValueError("page_table is [seqs, width]")
+        seqs, width = page_table.shape
+        if kv_lens.shape != (seqs,) or starts.shape != (seqs + 1,):
+            raise ValueError("kv_lens is [seqs] and starts [seqs + 1], with seqs = %d from page_table" % seqs)
+        for name, t in (("page_table", page_table), ("kv_lens", kv_lens), ("starts", starts)):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise TypeError("%s is a contiguous int32 tensor" % name)
+            if t.device != page_table.device:
+                raise ValueError("page_table, kv_lens and starts are on different devices")
+        if tokens < 0 or (max_new is not None and max_new < 0) or (max_kv is not None and max_kv < 0):
+            raise ValueError("tokens, max_new and max_kv count from 0")
+        self.page_table, self.kv_lens, self.starts = page_table, kv_lens, starts
+        self.device, self.seqs, self.width, self.tokens = page_table.device, seqs, width, tokens
+        self.max_new = tokens if max_new is None else max_new
+        self.max_kv = max_kv
+        self._by_page = {}
+
+    def _ref(self, page_tokens: int):
+        """The sz_batch for caches of this page size (max_kv defaults to a
+        full table's tokens)."""
+        ref = self._by_page.get(page_tokens)
+        if ref is None:
+            top = 2 ** 32 - 1
+            max_kv = min(self.width * page_tokens, 1 << 30) if self.max_kv is None else self.max_kv
+            if max(self.tokens, self.seqs, self.width, self.max_new, max_kv) > top:
+                raise ValueError("the batch is too large")
+            b = _native.sz_batch(self.page_table.data_ptr(), self.kv_lens.data_ptr(), self.starts.data_ptr(),
+                                 self.seqs, self.width, self.tokens, self.max_new, max_kv)
+            ref = self._by_page[page_tokens] = ctypes.byref(b)
+        return ref
+
+
+def _rows(name, t, tokens, heads, cache):
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s is a bfloat16 tensor, got %s" % (name, t.dtype))
+    if t.shape != (tokens, heads, cache.head_dim):
+        raise ValueError("%s is [%d, %d, %d], got %s" % (name, tokens, heads, cache.head_dim, tuple(t.shape)))
+    if t.device != cache.device:
+        raise ValueError("%s is on %s, the cache on %s" % (name, t.device, cache.device))
+    stride = t.stride()
+    if stride[2] != 1 and t.numel():
+        raise ValueError("%s needs contiguous rows (a last stride of 1)" % name)
+    return t.data_ptr(), stride[0], stride[1]
+
+
+class _Launch:
+    """The stream of a call, with the cache's device current while it is
+    launched, as sz.encode's: memory that the call allocates is handed over to
+    a stream other than the current one."""
+
+    def __init__(self, cache, batch, stream):
+        if batch.device != cache.device:
+            raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
+        if cache.device.type != "cuda":
+            raise ValueError("the cache is on %s; its calls run on the GPU" % cache.device)
+        current = torch.cuda.current_stream(cache.device)
+        self.side = None if stream is None or stream == current else stream
+        self.current = current
+        self.stream = (current if stream is None else stream).cuda_stream
+        self.guard = None if torch.cuda.current_device() == cache.device.index else torch.cuda.device(cache.device)
+
+    def run(self, name, call, *args, owned=()):
+        if self.side is not None and owned:
+            self.side.wait_stream(self.current)
+        if self.guard is None:
+            rc = call(*args, self.stream)
+        else:
+            with self.guard:
+                rc = call(*args, self.stream)
+        if rc:
+            _native.check(name, rc)
+        if self.side is not None:
+            for t in owned:
+                t.record_stream(self.side)
+
+    def raise_status(self, cache):
+        if self.side is not None:
+            self.side.synchronize()
+        cache.raise_status()
+
+
+def cache_check(cache: PagedCache, batch: PageBatch, stream=None) -> None:
+    """Raises ``SplitZipError`` unless the batch fits the cache and no page is
+    written from two places (sz_cache_check); waits for the device."""
+    on = _Launch(cache, batch, stream)
+    ws = torch.empty(_native.sz_cache_check_workspace_size(cache._ref), dtype=torch.uint8, device=cache.device)
+    on.run("sz_cache_check", _native.sz_cache_check, cache._ref, batch._ref(cache.page_tokens), ws.data_ptr(),
+           ws.numel(), cache._status, owned=(ws,))
+    on.raise_status(cache)
+
+
+def cache_write(cache: PagedCache, batch: PageBatch, k: torch.Tensor, v: torch.Tensor, stream=None,
+                check: bool = True) -> None:
+    """Writes the batch's tokens (bfloat16 ``[tokens, kv_heads, head_dim]``,
+    any token and head strides that keep rows 16-byte aligned) into their
+    pages, FP8 caches quantised with a power-of-two scale for each row
+    (sz_cache_write).  With ``check`` the batch is checked first
+    (``cache_check``) and nothing is written if it is wrong."""
+    kp = _rows("k", k, batch.tokens, cache.kv_heads, cache)
+    vp = _rows("v", v, batch.tokens, cache.kv_heads, cache)
+    if check:
+        cache_check(cache, batch, stream)
+    on = _Launch(cache, batch, stream)
+    on.run("sz_cache_write", _native.sz_cache_write, cache._ref, batch._ref(cache.page_tokens), *kp, *vp,
+           cache._status)
+
+
+def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check: bool = True):
+    """The batch's tokens out of their pages: bfloat16 ``(k, v)``, each
+    ``[tokens, kv_heads, head_dim]`` (sz_cache_read).  ``out``: such a pair to
+    read into.  Rows of tokens that belong to no sequence keep what they
+    held."""
+    owned = ()
+    on = _Launch(cache, batch, stream)
+    if out is None:
+        shape = (batch.tokens, cache.kv_heads, cache.head_dim)
+        out = owned = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device),
+                       torch.empty(shape, dtype=torch.bfloat16, device=cache.device))
+    k, v = out
+    on.run("sz_cache_read", _native.sz_cache_read, cache._ref, batch._ref(cache.page_tokens),
+           *_rows("out[0]", k, batch.tokens, cache.kv_heads, cache),
+           *_rows("out[1]", v, batch.tokens, cache.kv_heads, cache), cache._status, owned=owned)
+    if check:
+        on.raise_status(cache)
+    return k, v
+
+
+def attention_workspace(cache: PagedCache, batch: PageBatch, q_heads: int) -> torch.Tensor:
+    """A workspace for ``paged_attention`` of this batch's bounds, with any window."""
+    if q_heads <= 0 or q_heads % cache.kv_heads:
+        raise ValueError("q_heads is a multiple of the cache's %d KV heads, got %d" % (cache.kv_heads, q_heads))
+    n = _native.sz_paged_attention_workspace_size(cache._ref, batch._ref(cache.page_tokens), q_heads)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale: float | None = None,
+                    window: int = 0, out: torch.Tensor | None = None, lse=False, ws: torch.Tensor | None = None,
+                    stream=None, check: bool = True):
+    """Causal attention of the batch's tokens over their sequences' cached
+    keys and values, the tokens' own included (sz_paged_attention).  ``q``:
+    bfloat16 ``[tokens, q_heads, head_dim]``; ``scale`` defaults to
+    head_dim**-0.5; with ``window`` > 0 a token sees the last ``window``
+    positions up to its own.  Returns bfloat16 ``out``, or ``(out, lse)`` with
+    ``lse`` true or a float32 ``[tokens, q_heads]`` tensor to write into."""
+    if q.dim() != 3:
+        raise ValueError("q is [tokens, q_heads, head_dim]")
+    q_heads = q.shape[1]
+    qp, q_token, q_head = _rows("q", q, batch.tokens, q_heads, cache)
+    if q_heads == 0 or q_heads % cache.kv_heads:
+        raise ValueError("q has %d heads, not a multiple of the cache's %d KV heads" % (q_heads, cache.kv_heads))
+    if window < 0:
+        raise ValueError("window counts from 0 (0: none)")
+    on = _Launch(cache, batch, stream)
+    owned = []
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+        owned.append(out)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != cache.device:
+        raise ValueError("out is a contiguous bfloat16 tensor of q's shape on the cache's device")
+    want_lse = lse is not False and lse is not None
+    if want_lse and lse is True:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device)
+        owned.append(lse)
+    elif want_lse and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()
+                       or lse.device != cache.device):
+        raise ValueError("lse is a contiguous float32 [tokens, q_heads] tensor on the cache's device")
+    if ws is None:
+        ws = attention_workspace(cache, batch, q_heads)
+        owned.append(ws)
+    elif not ws.is_contiguous() or ws.device != cache.device:
+        raise ValueError("ws is a contiguous tensor on the cache's device")
+    on.run("sz_paged_attention", _native.sz_paged_attention, cache._ref, batch._ref(cache.page_tokens), qp, q_heads,
+           q_token, q_head, 1.0 / math.sqrt(cache.head_dim) if scale is None else scale, min(window, 1 << 30),
+           out.data_ptr(), lse.data_ptr() if want_lse else None, ws.data_ptr(), ws.numel() * ws.element_size(),
+           cache._status, owned=owned)
+    if check:
+        on.raise_status(cache)
+    return (out, lse) if want_lse else out

@@ -279,6 +279,129 @@ uint64_t sz_decode_noalloc_max_elems(void);
 int sz_decode_noalloc(const void *d_in, uint64_t in_bytes, int dtype, void *d_out, uint64_t n_elems,
                       int32_t *d_status, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged KV cache: where a serving process keeps one layer's keys and values,
+ * in the codec's element types, and the attention that reads them.  E5M2
+ * pages hold the bytes that sz_encode codes, so a cache, or any run of its
+ * pages, is an SZ_FP8_E5M2 (BF16: SZ_BF16) tensor for the codec and the
+ * transfer as it lies.
+ *
+ * sz_cache: data is [pages][2][kv_heads][page_tokens][head_dim] values of
+ * dtype (index 0 of the second axis keys, 1 values), contiguous, 16-byte
+ * aligned.  FP8 caches keep one scale byte for each row (one token's one
+ * head, K or V) in scales, [pages][2][kv_heads][page_tokens], 16-byte
+ * aligned: a row's values are q * 2^(byte - 127).  head_dim is 64 or 128,
+ * page_tokens a power of two from 16 to 1024, kv_heads at most 1024.
+ *
+ * sz_batch (device arrays, int32, 4-byte aligned): sequence i has kv_lens[i]
+ * tokens in the cache, the new ones included, and its new tokens are
+ * [starts[i], starts[i + 1]) of the packed axis of `tokens` tokens that k, v,
+ * q and the outputs have.  New token t stands at position p = kv_lens[i] -
+ * (starts[i + 1] - starts[i]) + (t - starts[i]), in row p % page_tokens of
+ * page page_table[i][p / page_tokens]; the table has table_width entries a
+ * sequence.  Tokens before starts[0] or from starts[seqs] on belong to no
+ * sequence, and p < 0 is no place: nothing is read or written for them (a
+ * row of attention with p < 0 sees no keys).  max_new and max_kv are the
+ * host's upper bounds of a sequence's new tokens and of kv_lens (max_kv <=
+ * table_width * page_tokens): the host does not see the lengths, so launch
+ * shapes follow from these, and tight bounds are faster ones.  Up to 2^30
+ * tokens in a batch and in a sequence.
+ *
+ * The calls only enqueue, allocate nothing, issue no memset and can be
+ * captured into a HIP graph, with lengths and tables that change between
+ * replays.  d_status is a caller-owned device int32 that the kernels set to
+ * SZ_E_FORMAT when the batch contradicts itself, the host's bounds or the
+ * cache (starts that descend or leave [0, tokens], a length outside [0,
+ * max_kv], more than max_new new tokens, a page number outside the cache).
+ * It is never cleared, except by sz_cache_check, so one word can stand for a
+ * whole step.  Such a sequence (or token) is skipped, and what it would have
+ * written keeps its old contents or, where a page number is wrong, is
+ * unspecified in the outputs; memory outside the cache, the outputs and the
+ * workspace is never touched.  Calls that share a workspace, or write pages
+ * that another call uses, must not overlap.
+ * ------------------------------------------------------------------------- */
+
+/* FP8 E4M3 (1.4.3, largest finite value 448, no infinities): a type of the
+ * paged cache, not of the codec. */
+enum { SZ_FP8_E4M3 = 2 };
+
+typedef struct sz_cache {
+    uint32_t dtype; /* SZ_BF16, SZ_FP8_E5M2 or SZ_FP8_E4M3 */
+    uint32_t page_tokens;
+    uint32_t kv_heads;
+    uint32_t head_dim;
+    uint64_t pages;
+    void *data;
+    void *scales; /* FP8; not read for SZ_BF16 */
+} sz_cache;
+
+typedef struct sz_batch {
+    const int32_t *page_table; /* [seqs][table_width] */
+    const int32_t *kv_lens;    /* [seqs] */
+    const int32_t *starts;     /* [seqs + 1] */
+    uint32_t seqs;
+    uint32_t table_width;
+    uint32_t tokens;
+    uint32_t max_new;
+    uint32_t max_kv;
+} sz_batch;
+
+/* Writes the new tokens' K and V (BF16, [tokens][kv_heads][head_dim] with
+ * strides in elements; rows contiguous and 16-byte aligned) into their
+ * places.  FP8 caches: with a the largest magnitude of the row's finite
+ * values and MAX the type's largest finite value (57344, 448), k is the
+ * smallest integer >= -126 with a <= MAX * 2^k, each value x becomes
+ * x * 2^-k rounded to nearest even, and the scale byte is k + 127.  NaN stays
+ * NaN; infinities stay infinite in E5M2 and become NaN in E4M3.  The places
+ * of one call must be distinct: of two tokens with the same place, which
+ * one's values and scale remain is unspecified, each by itself
+ * (sz_cache_check finds such batches).  Everything else in the cache is left
+ * as it is.  Returns SZ_OK, SZ_E_DTYPE, SZ_E_ARG (null pointers, sizes out of
+ * range), SZ_E_ALIGN or SZ_E_HIP. */
+int sz_cache_write(const sz_cache *cache, const sz_batch *batch, const void *d_k, uint64_t k_token_stride,
+                   uint64_t k_head_stride, const void *d_v, uint64_t v_token_stride, uint64_t v_head_stride,
+                   int32_t *d_status, void *stream);
+
+/* Reads the tokens' K and V back as BF16, into tensors of the same layout:
+ * q * 2^(byte - 127), exact while it is in BF16's range.  A batch whose
+ * starts hold all of each sequence's tokens reads whole sequences.  Return
+ * codes as sz_cache_write. */
+int sz_cache_read(const sz_cache *cache, const sz_batch *batch, void *d_k, uint64_t k_token_stride,
+                  uint64_t k_head_stride, void *d_v, uint64_t v_token_stride, uint64_t v_head_stride,
+                  int32_t *d_status, void *stream);
+
+/* Checks a batch before it is used: everything that the calls above and
+ * below check as they go, for all pages of all sequences, and that every
+ * page that a new token falls into is named only once among such pages.
+ * Sets *d_status to SZ_OK or SZ_E_FORMAT.  d_ws: ws_bytes >=
+ * sz_cache_check_workspace_size(cache), 4 bytes a page. */
+uint64_t sz_cache_check_workspace_size(const sz_cache *cache);
+int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uint64_t ws_bytes, int32_t *d_status,
+                   void *stream);
+
+/* Attention of the new tokens over their sequences' keys and values, which
+ * include their own (write them first).  d_q: BF16 [tokens][q_heads]
+ * [head_dim] with strides in elements, rows contiguous and 16-byte aligned;
+ * query head h reads KV head h / (q_heads / kv_heads).  A token at position p
+ * sees the keys j with j <= p and, for window > 0, j > p - window:
+ *   s_j = scale * q.K_j,  out = sum exp(s_j) V_j / sum exp(s_j),
+ *   lse = ln sum exp(s_j)
+ * with K and V the values that sz_cache_read returns.  d_out: BF16
+ * [tokens][q_heads][head_dim], contiguous.  d_lse: float [tokens][q_heads]
+ * or NULL.  A token that sees no key gets 0 and -inf.  Keys that a token does
+ * not see do not reach its result, NaN and infinities included.  Sums,
+ * scores and lse are 32-bit; probabilities are rounded to BF16.  The result
+ * does not depend on what runs beside it, bit for bit; it depends on max_new
+ * and max_kv in its last bits, through the split of the keys.  scale must be
+ * finite and above 0.  d_ws: ws_bytes >=
+ * sz_paged_attention_workspace_size(cache, batch, q_heads) (0 for heads that
+ * do not divide; host fields of cache and batch only).  Returns SZ_OK,
+ * SZ_E_DTYPE, SZ_E_ARG, SZ_E_ALIGN, SZ_E_WORKSPACE or SZ_E_HIP. */
+uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, const sz_batch *batch, uint32_t q_heads);
+int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void *d_q, uint32_t q_heads,
+                       uint64_t q_token_stride, uint64_t q_head_stride, float scale, uint32_t window, void *d_out,
+                       float *d_lse, void *d_ws, uint64_t ws_bytes, int32_t *d_status, void *stream);
+
 /* Instrumentation (not part of the codec).  While enabled, every kernel the
  * library launches is bracketed by a pair of HIP events recorded on the
  * launch stream.  sz_profile_collect waits for the recorded events, writes
