@@ -228,31 +228,12 @@ def sz_decode_noalloc(d_in, in_bytes, dtype, d_out, n, d_status, stream) -> int:
     return int(lib.sz_decode_noalloc(d_in, in_bytes, dtype, d_out, n, d_status, stream))
 
 
-# cache and batch: sz_cache and sz_batch, or byref() of them
-def sz_cache_write(cache, batch, d_k, k_token, k_head, d_v, v_token, v_head, d_status, stream) -> int:
-    return lib.sz_cache_write(cache, batch, d_k, k_token, k_head, d_v, v_token, v_head, d_status, stream)
-
-
-def sz_cache_read(cache, batch, d_k, k_token, k_head, d_v, v_token, v_head, d_status, stream) -> int:
-    return lib.sz_cache_read(cache, batch, d_k, k_token, k_head, d_v, v_token, v_head, d_status, stream)
-
-
 def sz_cache_check_workspace_size(cache) -> int:
     return int(lib.sz_cache_check_workspace_size(cache))
 
 
-def sz_cache_check(cache, batch, d_ws, ws_bytes, d_status, stream) -> int:
-    return lib.sz_cache_check(cache, batch, d_ws, ws_bytes, d_status, stream)
-
-
 def sz_paged_attention_workspace_size(cache, batch, q_heads) -> int:
     return int(lib.sz_paged_attention_workspace_size(cache, batch, q_heads))
-
-
-def sz_paged_attention(cache, batch, d_q, q_heads, q_token, q_head, scale, window, d_out, d_lse, d_ws, ws_bytes,
-                       d_status, stream) -> int:
-    return lib.sz_paged_attention(cache, batch, d_q, q_heads, q_token, q_head, scale, window, d_out, d_lse, d_ws,
-                                  ws_bytes, d_status, stream)
 
 
 def sz_reference_copy(d_src, d_dst, nbytes, stream) -> int:

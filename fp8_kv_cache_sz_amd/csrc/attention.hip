@@ -26,6 +26,8 @@
 // (m, l, o) sz_attn_join joins, always in the order of the chunks.
 #include "paged.hpp"
 
+#include <type_traits>
+
 namespace sz {
 namespace {
 
@@ -83,9 +85,39 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ bool any_not_finite(uint32_t w)       // either BF16 of a pair
+// Bits 15 and 31 tell whether the BF16 halves of a pair are NaN or infinite.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
+constexpr uint32_t kNotFinite = 0x80008000u;
+
+// NaN and infinities among V rows that some rows of a tile see and others do
+// not: the tile's product may not meet them, since 0 times either is a NaN.
+// They are counted instead, by a product of their own: kinds(w) has 1 for
+// +inf, 128 for -inf and 16384 for a NaN in either BF16 of a pair and else 0,
+// a row's second operand is 1 where it sees the key, and the sums over at
+// most 64 keys hold the three counts, exactly.  from_kinds(sum) is what the
+// counted values add up to; finite(w) is what is left for the tile's product.
+__device__ __forceinline__ uint32_t kinds(uint32_t w)
 {
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+    const auto kind = [](uint32_t h) {
+        const uint32_t a = h & 0x7FFFu;
+        return a < 0x7F80u ? 0u : a > 0x7F80u ? 0x4680u : h & 0x8000u ? 0x4300u : 0x3F80u;
+    };
+    return kind(w & 0xFFFFu) | kind(w >> 16) << 16;
+}
+__device__ __forceinline__ float from_kinds(float sum)
+{
+    const uint32_t c = (uint32_t)sum;
+    const bool plus = c & 127u, minus = c & 16383u & ~127u;
+    return c >= 16384u || (plus && minus) ? __builtin_nanf("") : minus ? kNone : plus ? -kNone : 0.f;
+}
+__device__ __forceinline__ uint32_t finite(uint32_t w)
+{
+    return w & ~(((not_finite(w) & kNotFinite) >> 15) * 0xFFFFu);
+}
+// 1.0 in the halves of a pair of keys that [lo, hi] holds
+__device__ __forceinline__ uint32_t seen_pair(int32_t key, int32_t lo, int32_t hi)
+{
+    return (key >= lo && key <= hi ? 0x3F80u : 0u) | (key + 1 >= lo && key + 1 <= hi ? 0x3F800000u : 0u);
 }
 
 // Writes one row's EL consecutive values at d: the result, or a chunk's partial.
@@ -138,58 +170,65 @@ __device__ __forceinline__ void store_stats(const AttnArgs &a, bool whole, uint3
 // ---------------------------------------------------------------------------
 template <int DT, int D>
 struct KeyBlock {
-    static constexpr int KL = DT == SZ_BF16 ? D / 32 : D / 64;             // 16-byte loads per 16 keys
-    static constexpr int VW = (D / 16) * (DT == SZ_BF16 ? 2 : 1) / 4;      // dwords per lane and V row
+    static constexpr uint32_t ES = DT == SZ_BF16 ? 2 : 1;
+    static constexpr int KL = D * ES / 64;               // 16-byte loads per 16 keys
+    static constexpr int VW = D / 16 * ES / 4;           // dwords per lane and V row
     u32x4 k[2][KL];
     uint32_t v[8][VW];
-    uint32_t ks[2], vs[2];     // scale bytes: K of the lane's key, V of its four rows
+    uint32_t ks[2], vs[2];                               // scale bytes: K of the lane's key, V of its four rows
 };
 
 template <int DT, int D>
-__device__ __forceinline__ void load_block(const AttnArgs &a, uint32_t head, const uint32_t (&page)[2], int32_t kb,
-                                           KeyBlock<DT, D> &x)
+__device__ __forceinline__ void load_keys(const AttnArgs &a, uint32_t head, const uint32_t (&page)[2], int32_t kb,
+                                          KeyBlock<DT, D> &x)
 {
-    constexpr uint32_t ES = DT == SZ_BF16 ? 2 : 1;
+    constexpr uint32_t ES = KeyBlock<DT, D>::ES;
     const uint32_t lane = lane_id(), m = lane % 16, g = lane / 16;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        const uint32_t row0 = (uint32_t)(kb + 16 * b) & ((1u << a.c.lg_page) - 1);
-        const uint64_t kr = row_index(a.c, page[b], 0, head, row0);
-        const uint64_t vr = row_index(a.c, page[b], 1, head, row0);
-        const uint8_t *kp = a.c.data + kr * (D * ES);
-        const uint8_t *vp = a.c.data + vr * (D * ES);
+        const uint64_t r = row_index(a.c, page[b], 0, head, (uint32_t)(kb + 16 * b) & ((1u << a.c.lg_page) - 1));
+        const uint8_t *p = a.c.data + r * (D * ES) + (m * (D * ES) + 16 * g);
 #pragma unroll
-        for (int i = 0; i < KeyBlock<DT, D>::KL; ++i)
-            x.k[b][i] = *reinterpret_cast<const u32x4 *>(kp + (m * (D * ES) + 64 * i + 16 * g));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint32_t off = (4 * g + r) * (D * ES) + m * (D / 16 * ES);
-            if constexpr (KeyBlock<DT, D>::VW == 4) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(vp + off);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x.v[4 * b + r][e] = w[e];
-            } else if constexpr (KeyBlock<DT, D>::VW == 2) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(vp + off);
-                x.v[4 * b + r][0] = w.x;
-                x.v[4 * b + r][1] = w.y;
-            } else {
-                x.v[4 * b + r][0] = *reinterpret_cast<const uint32_t *>(vp + off);
-            }
-        }
-        if constexpr (DT != SZ_BF16) {
-            x.ks[b] = a.c.scales[kr + m];
-            x.vs[b] = *reinterpret_cast<const uint32_t *>(a.c.scales + vr + 4 * g);
-        }
+        for (int i = 0; i < KeyBlock<DT, D>::KL; ++i) x.k[b][i] = *reinterpret_cast<const u32x4 *>(p + 64 * i);
+        if constexpr (DT != SZ_BF16) x.ks[b] = a.c.scales[r + m];
     }
 }
 
 template <int DT, int D>
-__global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_rows(AttnArgs a)
+__device__ __forceinline__ void load_values(const AttnArgs &a, uint32_t head, const uint32_t (&page)[2], int32_t kb,
+                                            KeyBlock<DT, D> &x)
 {
-    using Block = KeyBlock<DT, D>;
+    constexpr uint32_t ES = KeyBlock<DT, D>::ES;
+    const uint32_t lane = lane_id(), m = lane % 16, g = lane / 16;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const uint64_t r0 = row_index(a.c, page[b], 1, head, (uint32_t)(kb + 16 * b) & ((1u << a.c.lg_page) - 1));
+        const uint8_t *p = a.c.data + r0 * (D * ES) + (4 * g * (D * ES) + m * (D / 16 * ES));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t off = r * (D * ES);
+            if constexpr (KeyBlock<DT, D>::VW == 4) {
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(p + off);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x.v[4 * b + r][e] = w[e];
+            } else if constexpr (KeyBlock<DT, D>::VW == 2) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(p + off);
+                x.v[4 * b + r][0] = w.x;
+                x.v[4 * b + r][1] = w.y;
+            } else {
+                x.v[4 * b + r][0] = *reinterpret_cast<const uint32_t *>(p + off);
+            }
+        }
+        if constexpr (DT != SZ_BF16) x.vs[b] = *reinterpret_cast<const uint32_t *>(a.c.scales + r0 + 4 * g);
+    }
+}
+
+template <int DT, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void sz_attn_rows(AttnArgs a)
+{
     constexpr int VD = D / 16;                      // d values of a lane
-    __shared__ float lds_o[4][kRowsMax][D + 4];
-    __shared__ float2 lds_ml[4][kRowsMax];
+    __shared__ float lds_o[WAVES][kRowsMax][D + 4];
+    __shared__ float2 lds_ml[WAVES][kRowsMax];
 
     const uint32_t head = blockIdx.x % a.c.heads;
     const uint32_t seq = blockIdx.x / a.c.heads % a.b.seqs;
@@ -231,29 +270,40 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_rows(AttnArgs a)
     for (int j = 0; j < VD; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = kNone, l = 0.f;
 
-    // pages of a block; positions behind the end take the last position's page (their keys are hidden)
-    auto pages_at = [&](int32_t kb, uint32_t (&page)[2]) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) page[b] = uniform(page_of(a.c, a.b, seq, (uint32_t)min(kb + 16 * b, s.len - 1)));
-    };
-
     const int32_t all_lo = a.window > 0 ? max(0, s.len - a.window) : 0;      // every row sees [all_lo, all_hi]
     const int32_t all_hi = s.len - s.n;
 
+    constexpr int32_t STEP = 32 * WAVES;
     int32_t kb = begin + 32 * (int32_t)wave;
-    Block cur, next;
+    KeyBlock<DT, D> cur;
+    // The pages of this wave's next 32 blocks, two lanes to a block: one load,
+    // so that no block's loads wait for its page number.  Positions behind the
+    // end take the last one's page; their keys are hidden.
+    uint32_t ahead = 0, at = 0;
+    const auto look_ahead = [&](int32_t from) {
+        ahead = page_of(a.c, a.b, seq,
+                        (uint32_t)min((int64_t)from + (int64_t)(lane / 2) * STEP + 16 * (lane % 2), (int64_t)s.len - 1));
+        at = 0;
+    };
     uint32_t page[2];
+    const auto next_pages = [&]() {
+        page[0] = __builtin_amdgcn_readlane(ahead, at);
+        page[1] = __builtin_amdgcn_readlane(ahead, at + 1);
+        at += 2;
+    };
     if (kb < end) {
-        pages_at(kb, page);
-        load_block<DT, D>(a, head, page, kb, cur);
-        pages_at(min(kb + 128, s.len - 1), page);
+        look_ahead(kb);
+        next_pages();
+        load_keys<DT, D>(a, head, page, kb, cur);
+        __builtin_amdgcn_sched_barrier(0);       // keys always before values: a wait for keys leaves values in flight
+        load_values<DT, D>(a, head, page, kb, cur);
     }
-    for (; kb < end; kb += 128) {
-        const bool more = kb + 128 < end;
-        if (more) {
-            load_block<DT, D>(a, head, page, kb + 128, next);
-            pages_at(min(kb + 256, s.len - 1), page);
-        }
+    // One block.  MASKED: some row does not see some key of it; a path of its
+    // own, so that the common one has the registers to itself.  more: another
+    // block follows; the common path knows, so that its waits can count on the
+    // loads behind the ones they wait for.
+    const auto block = [&](auto masked_path, auto more) {
+        constexpr bool MASKED = decltype(masked_path)::value;
 
         // scores
         f32x4 st[2];
@@ -273,6 +323,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_rows(AttnArgs a)
                 }
                 st[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[i], st[b], 0, 0, 0);
             }
+        }
+        if (more) {
+            if (at == 64) look_ahead(kb + STEP);
+            next_pages();
+            if (!MASKED) load_keys<DT, D>(a, head, page, kb + STEP, cur);
         }
 
         // V rows as BF16
@@ -294,10 +349,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_rows(AttnArgs a)
 
         // Hidden keys: their scores are -inf whatever K holds; V rows that no
         // row sees (behind the end, before the window) become zeros, since 0
-        // times a NaN is one.  Rows that some see are checked further down.
-        const bool masked = kb < all_lo || kb + 31 > all_hi;
+        // times a NaN is one.  NaN and infinities in the others are counted
+        // further down.
         bool wild = false;
-        if (masked) {
+        if constexpr (MASKED) {
+            uint32_t found = 0;
             const int32_t any_lo = a.window > 0 ? max(0, all_hi - a.window + 1) : 0;
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
@@ -307,10 +363,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_rows(AttnArgs a)
 #pragma unroll
                 for (int e = 0; e < VD / 2; ++e) {
                     if (dead) v[r][e] = 0;
-                    wild = wild || any_not_finite(v[r][e]);
+                    found |= not_finite(v[r][e]);
                 }
             }
-            wild = __any(wild);
+            wild = __any((found & kNotFinite) != 0);
         }
 
         // running maximum, raised only when some row needs it
@@ -338,44 +394,53 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_rows(AttnArgs a)
         const u32x4 pw = {bf16_pair(p[0], p[1]), bf16_pair(p[2], p[3]), bf16_pair(p[4], p[5]), bf16_pair(p[6], p[7])};
         const bf16x8 pb = __builtin_bit_cast(bf16x8, pw);
 
-        if (__builtin_expect(!wild, 1)) {
-#pragma unroll
+        if (MASKED && wild) {
+            const int32_t key = kb + 4 * (int32_t)g;
+            const u32x4 sw = {seen_pair(key, lo, hi), seen_pair(key + 2, lo, hi), seen_pair(key + 16, lo, hi),
+                              seen_pair(key + 18, lo, hi)};
+            uint32_t even = 0x05040100u;
+            asm volatile("" : "+s"(even));       // these permutes are not shared with the ones below, which would
+#pragma unroll                                   // keep all of them in registers
             for (int j = 0; j < VD; ++j) {
-                const uint32_t sel = j % 2 ? 0x07060302u : 0x05040100u;
-                const u32x4 w = {perm(v[1][j / 2], v[0][j / 2], sel), perm(v[3][j / 2], v[2][j / 2], sel),
-                                 perm(v[5][j / 2], v[4][j / 2], sel), perm(v[7][j / 2], v[6][j / 2], sel)};
-                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pb, o[j], 0, 0, 0);
-            }
-        } else {
-            // NaN or infinity in a row that is hidden from some rows: one row
-            // at a time, with the V rows that it sees and zeros for the others.
-#pragma unroll 1
-            for (uint32_t row = 0; row < rows; ++row) {
-                const int32_t rlo = __shfl(lo, (int)row, 64), rhi = __shfl(hi, (int)row, 64);
-                uint32_t even = 0x05040100u;
-                asm volatile("" : "+s"(even));       // built again for each row: not kept in registers for all
+                const uint32_t sel = even + (j % 2 ? 0x02020202u : 0u);
+                const u32x4 w = {kinds(perm(v[1][j / 2], v[0][j / 2], sel)), kinds(perm(v[3][j / 2], v[2][j / 2], sel)),
+                                 kinds(perm(v[5][j / 2], v[4][j / 2], sel)), kinds(perm(v[7][j / 2], v[6][j / 2], sel))};
+                const f32x4 c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, sw), f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-                for (int j = 0; j < VD; ++j) {
-                    const uint32_t sel = even + (j % 2 ? 0x02020202u : 0u);
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int32_t key = kb + 16 * (e / 2) + 4 * (int32_t)g + 2 * (e % 2);
-                        const uint32_t keep = (key >= rlo && key <= rhi ? 0x0000FFFFu : 0u) |
-                                              (key + 1 >= rlo && key + 1 <= rhi ? 0xFFFF0000u : 0u);
-                        w[e] = perm(v[2 * e + 1][j / 2], v[2 * e][j / 2], sel) & keep;
-                    }
-                    const u32x4 ww = {w[0], w[1], w[2], w[3]};
-                    const f32x4 t =
-                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ww), pb, o[j], 0, 0, 0);
-                    if (n == row) o[j] = t;
-                }
+                for (int r = 0; r < 4; ++r) o[j][r] += from_kinds(c[r]);
             }
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int e = 0; e < VD / 2; ++e) v[r][e] = finite(v[r][e]);
         }
-        if (more) cur = next;
+#pragma unroll
+        for (int j = 0; j < VD; ++j) {
+            const uint32_t sel = j % 2 ? 0x07060302u : 0x05040100u;
+            const u32x4 w = {perm(v[1][j / 2], v[0][j / 2], sel), perm(v[3][j / 2], v[2][j / 2], sel),
+                             perm(v[5][j / 2], v[4][j / 2], sel), perm(v[7][j / 2], v[6][j / 2], sel)};
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pb, o[j], 0, 0, 0);
+        }
+        if (more) {
+            if (MASKED) {
+                load_keys<DT, D>(a, head, page, kb + STEP, cur);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            load_values<DT, D>(a, head, page, kb + STEP, cur);
+        }
+    };
+    while (kb < end) {
+        for (; kb + STEP < end && kb >= all_lo && kb + 31 <= all_hi; kb += STEP)
+            block(std::false_type{}, std::true_type{});
+        if (kb >= all_lo && kb + 31 <= all_hi)
+            block(std::false_type{}, std::false_type{});
+        else
+            block(std::true_type{}, kb + STEP < end);
+        kb += STEP;
     }
 
-    // the four waves' sums meet in LDS
+    // the waves' sums meet in LDS
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     if (g == 0) lds_ml[wave][n] = make_float2(m, l);
@@ -386,21 +451,20 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_rows(AttnArgs a)
             *reinterpret_cast<float4 *>(&lds_o[wave][n][(4 * g + r) * VD + j]) =
                 make_float4(o[j][r], o[j + 1][r], o[j + 2][r], o[j + 3][r]);
     __syncthreads();
+    // 256 threads, each VD values of one row
     const uint32_t row = threadIdx.x / 16, d = threadIdx.x % 16 * VD;
     if (row >= rows) return;
-    float mw[4], top = kNone, sum = 0.f, acc[VD];
+    float top = kNone, sum = 0.f, acc[VD];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        mw[w] = lds_ml[w][row].x;
-        top = fmaxf(top, mw[w]);
-    }
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, lds_ml[w][row].x);
     const float base = top == kNone ? 0.f : top;
 #pragma unroll
     for (int j = 0; j < VD; ++j) acc[j] = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = exp2_fast(mw[w] - base);
-        sum += lds_ml[w][row].y * f;
+#pragma unroll 4
+    for (int w = 0; w < WAVES; ++w) {
+        const float2 ml = lds_ml[w][row];
+        const float f = exp2_fast(ml.x - base);
+        sum += ml.y * f;
 #pragma unroll
         for (int j = 0; j < VD; ++j) acc[j] += lds_o[w][row][d + j] * f;
     }
@@ -590,36 +654,35 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
         for (int r = 0; r < 16; ++r) o[j][r] = 0.f;
     float m = kNone, l = 0.f;
 
-    // A wave fetches 16 rows of a tile: one page (or part of one).  Rows behind
-    // the sequence's end come from its last page and are hidden.
-    const auto page_at = [&](int32_t key) {
-        return uniform(page_of(a.c, a.b, seq, (uint32_t)min(key, s.len - 1)));
+    // A wave fetches 16 rows of a tile: one page (or part of one).  The pages
+    // of its next 64 tiles, a lane each, in one load.  Rows behind the
+    // sequence's end come from its last page and are hidden.
+    uint32_t ahead = 0, at = 0;
+    const auto look_ahead = [&](int32_t from) {
+        ahead = page_of(a.c, a.b, seq,
+                        (uint32_t)min((int64_t)from + (int64_t)lane * kTileKeys + 16 * wave, (int64_t)s.len - 1));
+        at = 0;
     };
     TileRegs<DT, D> regs;
-    uint32_t page = 0;
+    const auto fetch = [&](int32_t from, uint32_t into) {
+        if (at == 64) look_ahead(from);
+        const uint32_t page = __builtin_amdgcn_readlane(ahead, at++);
+        if constexpr (DT == SZ_BF16)
+            fetch_tile_bf16<D>(a, head, page, from + 16 * (int32_t)wave, wave, lds.k[into], lds.v[into]);
+        else
+            fetch_tile_fp8<DT, D>(a, head, page, from + 16 * (int32_t)wave, regs);
+    };
     if (begin < end) {
-        page = page_at(begin + 16 * (int32_t)wave);
-        if constexpr (DT == SZ_BF16) {
-            fetch_tile_bf16<D>(a, head, page, begin + 16 * (int32_t)wave, wave, lds.k[0], lds.v[0]);
-        } else {
-            fetch_tile_fp8<DT, D>(a, head, page, begin + 16 * (int32_t)wave, regs);
-            place_tile_fp8<DT, D>(regs, wave, lds.k[0], lds.v[0]);
-        }
-        page = page_at(begin + (int32_t)kTileKeys + 16 * (int32_t)wave);
+        look_ahead(begin);
+        fetch(begin, 0);
+        if constexpr (DT != SZ_BF16) place_tile_fp8<DT, D>(regs, wave, lds.k[0], lds.v[0]);
     }
     uint32_t buf = 0;
     for (int32_t kb = begin; kb < end; kb += kTileKeys, buf ^= 1) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                       // this wave's loads into LDS are done
         __syncthreads();                                                       // this tile is in LDS, the other is free
         const bool more = kb + (int32_t)kTileKeys < end;
-        if (more) {
-            const int32_t key0 = kb + (int32_t)kTileKeys + 16 * (int32_t)wave;
-            if constexpr (DT == SZ_BF16)
-                fetch_tile_bf16<D>(a, head, page, key0, wave, lds.k[buf ^ 1], lds.v[buf ^ 1]);
-            else
-                fetch_tile_fp8<DT, D>(a, head, page, key0, regs);
-            page = page_at(key0 + (int32_t)kTileKeys);
-        }
+        if (more) fetch(kb + (int32_t)kTileKeys, buf ^ 1);
         const uint16_t *kt = lds.k[buf];
         uint16_t *vt = lds.v[buf];
 
@@ -639,8 +702,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
         }
 
         // Hidden keys, as in sz_attn_rows: -inf scores; V rows that no row of
-        // this tile sees become zeros in LDS; NaN or infinity in V rows that
-        // only some see takes the slow path.
+        // this tile sees become zeros in LDS; NaN and infinities in the others
+        // are counted further down.
         const bool masked = kb < all_lo || kb + (int32_t)kTileKeys - 1 > p_first;
         bool wild = false;
         if (masked) {
@@ -649,7 +712,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
             const uint32_t row = threadIdx.x / 4;
             const int32_t key = kb + (int32_t)row;
             const bool dead = key < any_lo || key > p_last;
-            bool bad = false;
+            uint32_t found = 0;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 u32x4 *p = reinterpret_cast<u32x4 *>(vt + row * D + (threadIdx.x % 4) * (D / 4) + 8 * i);
@@ -657,11 +720,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
                     *p = u32x4{0, 0, 0, 0};
                 else {
                     const u32x4 w = *p;
-                    bad = bad || any_not_finite(w[0]) || any_not_finite(w[1]) || any_not_finite(w[2]) ||
-                          any_not_finite(w[3]);
+                    found |= not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3]);
                 }
             }
-            if (bad) lds.wild = 1;
+            if (found & kNotFinite) lds.wild = 1;
             __syncthreads();
             wild = lds.wild != 0;
 #pragma unroll
@@ -706,39 +768,46 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
                 p[b][t] = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
             }
 
-        if (__builtin_expect(!wild, 1)) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int j = 0; j < DB; ++j)
-                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_operand<D>(vt, 32 * b + 16 * t, j), p[b][t],
-                                                                        o[j], 0, 0, 0);
-        } else {
+        if (__builtin_expect(wild, 0)) {
 #pragma unroll 1
-            for (uint32_t row = 0; row < 32; ++row) {
-                const int32_t rlo = __shfl(lo, (int)row, 64), rhi = __shfl(hi, (int)row, 64);
-                asm volatile("" ::: "memory");       // read again for each row: not kept in registers for all
+            for (int j = 0; j < DB; ++j) {
+                f32x16 c;
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int r = 0; r < 16; ++r) c[r] = 0.f;
+#pragma unroll 1
+                for (int t = 0; t < 4; ++t) {
+                    const int32_t key = kb + 16 * t + 4 * (int32_t)g;
+                    const u32x4 sw = {seen_pair(key, lo, hi), seen_pair(key + 2, lo, hi), seen_pair(key + 8, lo, hi),
+                                      seen_pair(key + 10, lo, hi)};
+                    u32x4 w = __builtin_bit_cast(u32x4, v_operand<D>(vt, 16 * t, j));
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                    for (int e = 0; e < 4; ++e) w[e] = kinds(w[e]);
+                    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
+                                                                __builtin_bit_cast(bf16x8, sw), c, 0, 0, 0);
+                }
 #pragma unroll
-                        for (int j = 0; j < DB; ++j) {
-                            u32x4 w = __builtin_bit_cast(u32x4, v_operand<D>(vt, 32 * b + 16 * t, j));
+                for (int jj = 0; jj < DB; ++jj)
+                    if (jj == j)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int32_t k = kb + 32 * b + 16 * t + 8 * (e / 2) + 4 * (int32_t)g + 2 * (e % 2);
-                                w[e] &= (k >= rlo && k <= rhi ? 0x0000FFFFu : 0u) |
-                                        (k + 1 >= rlo && k + 1 <= rhi ? 0xFFFF0000u : 0u);
-                            }
-                            const f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
-                                                                                     p[b][t], o[j], 0, 0, 0);
-                            if (n == row) o[j] = x;
-                        }
+                        for (int r = 0; r < 16; ++r) o[jj][r] += from_kinds(c[r]);
             }
+            __syncthreads();                                                   // every wave has counted
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                u32x4 *x = reinterpret_cast<u32x4 *>(vt + threadIdx.x / 4 * D + threadIdx.x % 4 * (D / 4) + 8 * i);
+                const u32x4 w = *x;
+                *x = u32x4{finite(w[0]), finite(w[1]), finite(w[2]), finite(w[3])};
+            }
+            __syncthreads();
         }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < DB; ++j)
+                    o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_operand<D>(vt, 32 * b + 16 * t, j), p[b][t], o[j],
+                                                                    0, 0, 0);
         if constexpr (DT != SZ_BF16)
             if (more) place_tile_fp8<DT, D>(regs, wave, lds.k[buf ^ 1], lds.v[buf ^ 1]);
     }
@@ -758,20 +827,34 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
 }
 
 // ---------------------------------------------------------------------------
-// sz_attn_join: a wave joins the chunks of one (token, head) row that hold
-// visible keys, in order:  M = max m'_s;  o = sum 2^(m'_s - M) o_s / sum
-// 2^(m'_s - M) l_s.
+// sz_attn_join: a workgroup joins the chunks of one (token, head) row that
+// hold visible keys:  M = max m'_s;  o = sum 2^(m'_s - M) o_s / sum
+// 2^(m'_s - M) l_s.  D/4 lanes take a partial in 16-byte loads, so 8 (D = 64:
+// 16) partials are read at once, each such group of lanes keeping a running
+// maximum over every 8th (16th) chunk; the groups meet in LDS, in order.
+// With per_seq > 0 only sequences of sz_attn_rows were split: the grid is
+// their tokens, at most per_seq each; else it is all tokens.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a)
+__global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_t per_seq)
 {
-    const uint64_t r = (uint64_t)blockIdx.x * (kAttnThreads / 64) + uniform(threadIdx.x / 64);
-    const uint32_t t = (uint32_t)(r / a.q_heads), head = (uint32_t)(r % a.q_heads);
-    if (t >= a.b.tokens) return;
-    const int32_t i = wave_last_not_above(a.b.seqs + 1, t, [&](uint32_t j) { return (int64_t)a.b.starts[j]; });
-    if (i < 0 || i >= (int32_t)a.b.seqs) return;
-    const Sequence s = sequence(a.b, uniform((uint32_t)i));
-    if ((int32_t)t < s.start || (int32_t)t >= s.start + s.n) return;
+    constexpr uint32_t LANES = D / 4, GROUPS = kAttnThreads / LANES;
+    __shared__ float4 lds_o[GROUPS][LANES];
+    __shared__ float2 lds_ml[GROUPS];
+    const uint32_t head = blockIdx.x % a.q_heads;
+    uint32_t t = blockIdx.x / a.q_heads;
+    Sequence s;
+    if (per_seq > 0) {
+        s = sequence(a.b, t / per_seq);
+        const uint32_t i = t % per_seq;
+        if (i >= (uint32_t)s.n) return;
+        t = (uint32_t)s.start + i;
+    } else {
+        const int32_t i = wave_last_not_above(a.b.seqs + 1, t, [&](uint32_t j) { return (int64_t)a.b.starts[j]; });
+        if (i < 0 || i >= (int32_t)a.b.seqs) return;
+        s = sequence(a.b, uniform((uint32_t)i));
+        if ((int32_t)t < s.start || (int32_t)t >= s.start + s.n) return;
+    }
     const bool few = (uint64_t)s.n * a.group <= a.rows_limit;
     if ((few ? a.rows_splits : a.tile_splits) == 1) return;                    // already whole
     const uint32_t chunk = few ? a.rows_chunk : a.tile_chunk;
@@ -781,36 +864,41 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a)
     const int32_t first = first_key(s, a.window);
     const uint32_t s0 = empty ? 0 : (uint32_t)(lo - first) / chunk, s1 = empty ? 0 : (uint32_t)(hi - first) / chunk + 1;
 
-    const uint32_t lane = lane_id();
-    const uint64_t stride = (uint64_t)a.b.tokens * a.q_heads;
-    float top = kNone;
-    for (uint32_t k = s0 + lane; k < s1; k += 64) top = fmaxf(top, a.part_ml[k * stride + r].x);
+    const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const uint64_t r = (uint64_t)t * a.q_heads + head, stride = (uint64_t)a.b.tokens * a.q_heads;
+    float m = kNone, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto add = [&](float2 ml, float4 v) {
+        const float raised = fmaxf(m, ml.x);
+        const float base = raised == kNone ? 0.f : raised;
+        const float f = exp2_fast(m - base), g = exp2_fast(ml.x - base);
+        m = raised;
+        l = l * f + ml.y * g;
+        o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
+    };
+    constexpr int AHEAD = 4;
+    for (uint32_t k = s0 + group; k < s1; k += AHEAD * GROUPS) {
+        float2 ml[AHEAD];
+        float4 v[AHEAD];
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d, 64));
-    const float base = top == kNone ? 0.f : top;
-    float o[2] = {0.f, 0.f}, l = 0.f;
-    constexpr uint32_t E = D / 64;                                             // values of a lane
-#pragma unroll 4
-    for (uint32_t k = s0; k < s1; ++k) {
-        const float2 ml = a.part_ml[k * stride + r];
-        const float *p = a.part + (k * stride + r) * D + lane * E;
-        const float f = exp2_fast(ml.x - base);
-        l += ml.y * f;
-        if constexpr (E == 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(p);
-            o[0] += v.x * f;
-            o[1] += v.y * f;
-        } else {
-            o[0] += *p * f;
+        for (int e = 0; e < AHEAD; ++e) {
+            const uint64_t at = min(k + e * GROUPS, s1 - 1) * stride + r;
+            ml[e] = a.part_ml[at];
+            v[e] = *reinterpret_cast<const float4 *>(a.part + at * D + lane * 4);
         }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e)
+            if (k + e * GROUPS < s1) add(ml[e], v[e]);
     }
-    const float inv = empty ? 0.f : 1.f / l;
-    uint16_t *out = a.out + r * D + lane * E;
-    if constexpr (E == 2)
-        *reinterpret_cast<uint32_t *>(out) = bf16_pair(o[0] * inv, o[1] * inv);
-    else
-        *out = (uint16_t)bf16_pair(o[0] * inv, 0.f);
-    if (lane == 0) store_stats(a, true, 0, t, head, empty, top, l);
+    lds_o[group][lane] = o;
+    if (lane == 0) lds_ml[group] = make_float2(m, l);
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (uint32_t g = 1; g < GROUPS; ++g) add(lds_ml[g], lds_o[g][lane]);
+    const float w[4] = {o.x, o.y, o.z, o.w};
+    store_row<D, 4>(a, true, 0, t, head, lane * 4, w, empty ? 0.f : 1.f / l);
+    if (lane == 0) store_stats(a, true, 0, t, head, empty, m, l);
 }
 
 // ---------------------------------------------------------------------------
@@ -818,14 +906,18 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a)
 // ---------------------------------------------------------------------------
 struct AttnPlan {
     bool rows, tiles;                 // which kernels the batch can need
+    uint32_t rows_waves;
     uint32_t rows_chunk, rows_splits, tile_chunk, tile_splits, slots;
 };
 
-constexpr uint64_t kRowsGroups = 1024;        // workgroups that sz_attn_rows wants
-constexpr uint32_t kRowsMinChunk = 256;
+constexpr uint64_t kRowsGroups = 2048;        // workgroups that sz_attn_rows wants
+constexpr uint32_t kRowsMinChunk = 512;
+constexpr uint32_t kWideKeys = 2048;          // sz_attn_rows with 8 waves and no chunks up to here
+constexpr uint64_t kWideGroups = 256;
 constexpr uint64_t kTileGroups = 512;
 constexpr uint32_t kTileMinChunk = 512;
 
+// Chunks of the batch's keys so that `groups` workgroups become `want`.
 uint64_t splits_wanted(uint64_t groups, uint64_t want) { return std::max<uint64_t>(1, want / groups); }
 
 // Splits of `span` keys so that `groups` workgroups become `want`, in chunks
@@ -846,11 +938,19 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
     uint64_t span = b.max_kv;
     if (window) span = std::min<uint64_t>(span, (uint64_t)window + b.max_new + kKeyAlign - 1);
     p.tiles = (uint64_t)b.max_new * group > kRowsMax;
-    p.rows = !p.tiles || b.seqs > 1;      // a single sequence's rows all go the same way
+    p.rows = !p.tiles || (b.seqs > 1 && group <= kRowsMax);      // a single sequence's rows all go the same way
     p.slots = (uint32_t)std::min<uint64_t>((uint64_t)b.tokens * group / kTileRows + b.seqs, 0x7FFFFFFFu);
     p.rows_splits = p.tile_splits = 1;
-    if (p.rows)
-        split_keys(span, (uint64_t)b.seqs * c->kv_heads, kRowsGroups, kRowsMinChunk, p.rows_chunk, p.rows_splits);
+    p.rows_waves = 4;
+    if (p.rows) {
+        const uint64_t groups = (uint64_t)b.seqs * c->kv_heads;
+        if (groups <= kWideGroups && span <= kWideKeys) {
+            p.rows_waves = 8;
+            p.rows_chunk = (uint32_t)(span + 127) / 128 * 128;
+        } else {
+            split_keys(span, groups, kRowsGroups, kRowsMinChunk, p.rows_chunk, p.rows_splits);
+        }
+    }
     if (p.tiles)
         split_keys(span, (uint64_t)p.slots * c->kv_heads, kTileGroups, kTileMinChunk, p.tile_chunk, p.tile_splits);
     return p;
@@ -868,7 +968,10 @@ int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
         const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits;
         if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
         LaunchScope scope("sz_attn_rows", s);
-        hipLaunchKernelGGL((sz_attn_rows<DT, D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+        if (p.rows_waves == 8)
+            hipLaunchKernelGGL((sz_attn_rows<DT, D, 8>), dim3((uint32_t)groups), dim3(512), 0, s, a);
+        else
+            hipLaunchKernelGGL((sz_attn_rows<DT, D, 4>), dim3((uint32_t)groups), dim3(256), 0, s, a);
     }
     if (p.tiles) {
         const uint64_t groups = (uint64_t)a.c.heads * p.slots * p.tile_splits;
@@ -877,10 +980,11 @@ int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
         hipLaunchKernelGGL((sz_attn_tiles<DT, D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a, p.slots);
     }
     if (p.rows_splits > 1 || p.tile_splits > 1) {
-        const uint64_t groups = ((uint64_t)a.b.tokens * a.q_heads + 3) / 4;
+        const uint32_t per_seq = p.tile_splits > 1 ? 0 : std::min(a.b.max_new, kRowsMax / a.group);
+        const uint64_t groups = (per_seq ? (uint64_t)a.b.seqs * per_seq : (uint64_t)a.b.tokens) * a.q_heads;
         if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
         LaunchScope scope("sz_attn_join", s);
-        hipLaunchKernelGGL((sz_attn_join<D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+        hipLaunchKernelGGL((sz_attn_join<D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a, per_seq);
     }
     return hipGetLastError() == hipSuccess ? SZ_OK : SZ_E_HIP;
 }

@@ -19,7 +19,6 @@ and raises ``SplitZipError`` if the batch was found wrong.
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -143,50 +142,49 @@ def _rows(name, t, tokens, heads, cache):
     return t.data_ptr(), stride[0], stride[1]
 
 
-class _Launch:
-    """The stream of a call, with the cache's device current while it is
-    launched, as sz.encode's: memory that the call allocates is handed over to
-    a stream other than the current one."""
+def _run(name, call, cache, batch, args, stream, owned=()):
+    """Launches a call on `stream` (None: the current one) with the cache's
+    device current.  Memory that this layer took from the current stream's
+    pool (`owned`) is handed over to a stream other than that."""
+    if batch.device != cache.device:
+        raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
+    device = cache.device
+    if device.type != "cuda":
+        raise ValueError("the cache is on %s; its calls run on the GPU" % device)
+    side = None
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        handle = stream.cuda_stream
+        current = torch.cuda.current_stream(device)
+        if stream != current:
+            side = stream
+            if owned:
+                side.wait_stream(current)
+    if torch.cuda.current_device() == device.index:
+        rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status, handle)
+    if rc:
+        _native.check(name, rc)
+    if side is not None:
+        for t in owned:
+            t.record_stream(side)
 
-    def __init__(self, cache, batch, stream):
-        if batch.device != cache.device:
-            raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
-        if cache.device.type != "cuda":
-            raise ValueError("the cache is on %s; its calls run on the GPU" % cache.device)
-        current = torch.cuda.current_stream(cache.device)
-        self.side = None if stream is None or stream == current else stream
-        self.current = current
-        self.stream = (current if stream is None else stream).cuda_stream
-        self.guard = None if torch.cuda.current_device() == cache.device.index else torch.cuda.device(cache.device)
 
-    def run(self, name, call, *args, owned=()):
-        if self.side is not None and owned:
-            self.side.wait_stream(self.current)
-        if self.guard is None:
-            rc = call(*args, self.stream)
-        else:
-            with self.guard:
-                rc = call(*args, self.stream)
-        if rc:
-            _native.check(name, rc)
-        if self.side is not None:
-            for t in owned:
-                t.record_stream(self.side)
-
-    def raise_status(self, cache):
-        if self.side is not None:
-            self.side.synchronize()
-        cache.raise_status()
+def _raise_status(cache, stream):
+    if stream is not None:
+        stream.synchronize()
+    cache.raise_status()
 
 
 def cache_check(cache: PagedCache, batch: PageBatch, stream=None) -> None:
     """Raises ``SplitZipError`` unless the batch fits the cache and no page is
     written from two places (sz_cache_check); waits for the device."""
-    on = _Launch(cache, batch, stream)
     ws = torch.empty(_native.sz_cache_check_workspace_size(cache._ref), dtype=torch.uint8, device=cache.device)
-    on.run("sz_cache_check", _native.sz_cache_check, cache._ref, batch._ref(cache.page_tokens), ws.data_ptr(),
-           ws.numel(), cache._status, owned=(ws,))
-    on.raise_status(cache)
+    _run("sz_cache_check", _native.lib.sz_cache_check, cache, batch, (ws.data_ptr(), ws.numel()), stream, (ws,))
+    _raise_status(cache, stream)
 
 
 def cache_write(cache: PagedCache, batch: PageBatch, k: torch.Tensor, v: torch.Tensor, stream=None,
@@ -196,13 +194,10 @@ def cache_write(cache: PagedCache, batch: PageBatch, k: torch.Tensor, v: torch.T
     pages, FP8 caches quantised with a power-of-two scale for each row
     (sz_cache_write).  With ``check`` the batch is checked first
     (``cache_check``) and nothing is written if it is wrong."""
-    kp = _rows("k", k, batch.tokens, cache.kv_heads, cache)
-    vp = _rows("v", v, batch.tokens, cache.kv_heads, cache)
+    args = (*_rows("k", k, batch.tokens, cache.kv_heads, cache), *_rows("v", v, batch.tokens, cache.kv_heads, cache))
     if check:
         cache_check(cache, batch, stream)
-    on = _Launch(cache, batch, stream)
-    on.run("sz_cache_write", _native.sz_cache_write, cache._ref, batch._ref(cache.page_tokens), *kp, *vp,
-           cache._status)
+    _run("sz_cache_write", _native.lib.sz_cache_write, cache, batch, args, stream)
 
 
 def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check: bool = True):
@@ -211,17 +206,17 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
     read into.  Rows of tokens that belong to no sequence keep what they
     held."""
     owned = ()
-    on = _Launch(cache, batch, stream)
     if out is None:
-        shape = (batch.tokens, cache.kv_heads, cache.head_dim)
-        out = owned = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device),
-                       torch.empty(shape, dtype=torch.bfloat16, device=cache.device))
+        both = torch.empty((2, batch.tokens, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16,
+                           device=cache.device)
+        owned = (both,)
+        out = both[0], both[1]
     k, v = out
-    on.run("sz_cache_read", _native.sz_cache_read, cache._ref, batch._ref(cache.page_tokens),
-           *_rows("out[0]", k, batch.tokens, cache.kv_heads, cache),
-           *_rows("out[1]", v, batch.tokens, cache.kv_heads, cache), cache._status, owned=owned)
+    args = (*_rows("out[0]", k, batch.tokens, cache.kv_heads, cache),
+            *_rows("out[1]", v, batch.tokens, cache.kv_heads, cache))
+    _run("sz_cache_read", _native.lib.sz_cache_read, cache, batch, args, stream, owned)
     if check:
-        on.raise_status(cache)
+        _raise_status(cache, stream)
     return k, v
 
 
@@ -250,29 +245,28 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
         raise ValueError("q has %d heads, not a multiple of the cache's %d KV heads" % (q_heads, cache.kv_heads))
     if window < 0:
         raise ValueError("window counts from 0 (0: none)")
-    on = _Launch(cache, batch, stream)
     owned = []
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
         owned.append(out)
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != cache.device:
         raise ValueError("out is a contiguous bfloat16 tensor of q's shape on the cache's device")
-    want_lse = lse is not False and lse is not None
-    if want_lse and lse is True:
+    if lse is True:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device)
         owned.append(lse)
-    elif want_lse and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()
-                       or lse.device != cache.device):
+    elif lse is False:
+        lse = None
+    elif lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()
+                              or lse.device != cache.device):
         raise ValueError("lse is a contiguous float32 [tokens, q_heads] tensor on the cache's device")
     if ws is None:
         ws = attention_workspace(cache, batch, q_heads)
         owned.append(ws)
     elif not ws.is_contiguous() or ws.device != cache.device:
         raise ValueError("ws is a contiguous tensor on the cache's device")
-    on.run("sz_paged_attention", _native.sz_paged_attention, cache._ref, batch._ref(cache.page_tokens), qp, q_heads,
-           q_token, q_head, 1.0 / math.sqrt(cache.head_dim) if scale is None else scale, min(window, 1 << 30),
-           out.data_ptr(), lse.data_ptr() if want_lse else None, ws.data_ptr(), ws.numel() * ws.element_size(),
-           cache._status, owned=owned)
+    _run("sz_paged_attention", _native.lib.sz_paged_attention, cache, batch,
+         (qp, q_heads, q_token, q_head, cache.head_dim ** -0.5 if scale is None else scale, min(window, 1 << 30),
+          out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes), stream, owned)
     if check:
-        on.raise_status(cache)
-    return (out, lse) if want_lse else out
+        _raise_status(cache, stream)
+    return out if lse is None else (out, lse)
