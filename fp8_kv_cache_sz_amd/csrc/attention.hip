@@ -98,11 +98,10 @@ constexpr uint32_t kNotFinite = 0x80008000u;
 // counted values add up to; finite(w) is what is left for the tile's product.
 __device__ __forceinline__ uint32_t kinds(uint32_t w)
 {
-    const auto kind = [](uint32_t h) {
-        const uint32_t a = h & 0x7FFFu;
-        return a < 0x7F80u ? 0u : a > 0x7F80u ? 0x4680u : h & 0x8000u ? 0x4300u : 0x3F80u;
-    };
-    return kind(w & 0xFFFFu) | kind(w >> 16) << 16;
+    const uint32_t ends = (not_finite(w) & kNotFinite) >> 15;                       // 1 in each such half
+    const uint32_t nan = ends & (((w & 0x007F007Fu) + 0x007F007Fu) >> 7);           // mantissa not 0
+    const uint32_t minus = ends & ~nan & (w >> 15), plus = ends & ~nan & ~(w >> 15);
+    return nan * 0x4680u | minus * 0x4300u | plus * 0x3F80u;
 }
 __device__ __forceinline__ float from_kinds(float sum)
 {
@@ -175,7 +174,7 @@ struct KeyBlock {
     static constexpr int VW = D / 16 * ES / 4;           // dwords per lane and V row
     u32x4 k[2][KL];
     uint32_t v[8][VW];
-    uint32_t ks[2], vs[2];                               // scale bytes: K of the lane's key, V of its four rows
+    uint32_t ks[2], vs[2];                               // scale bytes: of the four keys around the lane's, of its V rows
 };
 
 template <int DT, int D>
@@ -189,8 +188,8 @@ __device__ __forceinline__ void load_keys(const AttnArgs &a, uint32_t head, cons
         const uint64_t r = row_index(a.c, page[b], 0, head, (uint32_t)(kb + 16 * b) & ((1u << a.c.lg_page) - 1));
         const uint8_t *p = a.c.data + r * (D * ES) + (m * (D * ES) + 16 * g);
 #pragma unroll
-        for (int i = 0; i < KeyBlock<DT, D>::KL; ++i) x.k[b][i] = *reinterpret_cast<const u32x4 *>(p + 64 * i);
-        if constexpr (DT != SZ_BF16) x.ks[b] = a.c.scales[r + m];
+        for (int i = 0; i < KeyBlock<DT, D>::KL; ++i) x.k[b][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + 64 * i));
+        if constexpr (DT != SZ_BF16) x.ks[b] = *reinterpret_cast<const uint32_t *>(a.c.scales + r + m / 4 * 4);
     }
 }
 
@@ -208,11 +207,11 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, uint32_t head, co
         for (int r = 0; r < 4; ++r) {
             const uint32_t off = r * (D * ES);
             if constexpr (KeyBlock<DT, D>::VW == 4) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(p + off);
+                const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + off));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x.v[4 * b + r][e] = w[e];
             } else if constexpr (KeyBlock<DT, D>::VW == 2) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(p + off);
+                const uint2 w = load_nt(reinterpret_cast<const uint2 *>(p + off));
                 x.v[4 * b + r][0] = w.x;
                 x.v[4 * b + r][1] = w.y;
             } else {
@@ -316,7 +315,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void sz_attn_rows(A
                 if constexpr (DT == SZ_BF16) {
                     w = cur.k[b][i];
                 } else {
-                    const uint32_t sc = cur.ks[b] << 23;
+                    const uint32_t sc = ((cur.ks[b] >> (8 * (n % 4))) & 0xFFu) << 23;
                     const uint32_t w0 = cur.k[b][i / 2][2 * (i % 2)], w1 = cur.k[b][i / 2][2 * (i % 2) + 1];
                     w = u32x4{fp8_pair_to_bf16<DT, false>(w0, sc), fp8_pair_to_bf16<DT, true>(w0, sc),
                               fp8_pair_to_bf16<DT, false>(w1, sc), fp8_pair_to_bf16<DT, true>(w1, sc)};
@@ -433,10 +432,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void sz_attn_rows(A
     while (kb < end) {
         for (; kb + STEP < end && kb >= all_lo && kb + 31 <= all_hi; kb += STEP)
             block(std::false_type{}, std::true_type{});
-        if (kb >= all_lo && kb + 31 <= all_hi)
-            block(std::false_type{}, std::false_type{});
-        else
-            block(std::true_type{}, kb + STEP < end);
+        block(std::true_type{}, kb + STEP < end);
         kb += STEP;
     }
 
@@ -911,7 +907,7 @@ struct AttnPlan {
 };
 
 constexpr uint64_t kRowsGroups = 2048;        // workgroups that sz_attn_rows wants
-constexpr uint32_t kRowsMinChunk = 512;
+constexpr uint32_t kRowsMinChunk = 1024;
 constexpr uint32_t kWideKeys = 2048;          // sz_attn_rows with 8 waves and no chunks up to here
 constexpr uint64_t kWideGroups = 256;
 constexpr uint64_t kTileGroups = 512;
