@@ -37,6 +37,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// A lambda whose captures are registers: a call would put them in memory.
+#define SZ_INLINE __attribute__((always_inline))
+
 constexpr uint32_t kAttnThreads = 256;
 constexpr uint32_t kRowsMax = 16;        // rows of sz_attn_rows
 constexpr uint32_t kTileRows = 128;      // rows of sz_attn_tiles
@@ -482,8 +485,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void sz_attn_rows(A
 //   S^T: lane (row = lane % 32, g = lane / 32) holds keys 32 b + 8 i + 4 g +
 //     0..3, b = 0, 1, i = 0..3.
 // ---------------------------------------------------------------------------
-// 16-byte pieces of a row are stored at piece ^ swizzle(row): K reads take
-// the same piece of 32 rows, V reads four pieces of 8 rows.
+// 16-byte pieces of a row are stored at piece ^ swizzle(row), so that 16 lanes
+// meet no bank twice: K reads take the same piece of 32 rows, V reads four
+// pieces of each of 8 rows, FP8 tiles' writes four pieces, D / 32 apart, of
+// each of 16 rows.
 template <int D>
 __device__ __forceinline__ uint32_t k_swizzle(uint32_t row)
 {
@@ -492,7 +497,7 @@ __device__ __forceinline__ uint32_t k_swizzle(uint32_t row)
 template <int D>
 __device__ __forceinline__ uint32_t v_swizzle(uint32_t row)
 {
-    return D == 128 ? (row & 3u) << 2 : (row & 2u) << 1;
+    return D == 128 ? (row & 3u) * 5 : ((row >> 1) & 1u) * 5;
 }
 
 template <int D>
@@ -502,89 +507,116 @@ struct TileLds {
     uint32_t wild;
 };
 
-template <int DT, int D>
-struct TileRegs {               // an FP8 tile on its way: 32 values of one K and one V row per lane (D = 128)
-    static constexpr int W = D / 64;
-    u32x4 k[W], v[W];
-    uint32_t ks, vs;
-};
+template <int D, int KV>
+__device__ __forceinline__ uint32_t tile_swizzle(uint32_t row)
+{
+    return KV == 0 ? k_swizzle<D>(row) : v_swizzle<D>(row);
+}
 
-// BF16: wave w fetches rows 16 w .. 16 w + 15 of the tile.
-template <int D>
-__device__ __forceinline__ void fetch_tile_bf16(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0,
-                                                uint32_t wave, uint16_t *k, uint16_t *v)
+// Memory of the workgroup, known as such.
+typedef __attribute__((address_space(3))) uint16_t *LdsPtr;
+
+// BF16: wave w fetches rows 16 w .. 16 w + 15 of the tile's K (KV = 0) or V.
+template <int D, int KV>
+__device__ __forceinline__ void fetch_bf16(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0,
+                                           uint32_t wave, LdsPtr to)
 {
     constexpr uint32_t PIECES = D / 8, RPI = 64 / PIECES;       // 16-byte pieces of a row, rows per instruction
     const uint32_t lane = lane_id();
     const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
-    const uint16_t *kp = reinterpret_cast<const uint16_t *>(a.c.data) + row_index(a.c, page, 0, head, row0) * D;
-    const uint16_t *vp = reinterpret_cast<const uint16_t *>(a.c.data) + row_index(a.c, page, 1, head, row0) * D;
+    uint16_t *p = reinterpret_cast<uint16_t *>(a.c.data) + row_index(a.c, page, KV, head, row0) * D;
+    // A buffer of these 16 rows: unlike a flat load into LDS, a buffer load
+    // leaves the waits of the LDS reads beside it exact.
+    const auto rows = __builtin_amdgcn_make_buffer_rsrc(p, 0, 16 * D * 2, 0x00027000);
 #pragma unroll
     for (uint32_t i = 0; i < 16 / RPI; ++i) {
         const uint32_t r = i * RPI + lane / PIECES;              // of this wave's 16
-        const uint32_t row = 16 * wave + r;
-        const uint32_t at = (16 * wave + i * RPI) * D;
         typedef __attribute__((address_space(3))) void *lds_ptr;
-        typedef const __attribute__((address_space(1))) void *global_ptr;
-        __builtin_amdgcn_global_load_lds((global_ptr)(kp + r * D + 8 * ((lane % PIECES) ^ k_swizzle<D>(row))),
-                                         (lds_ptr)(k + at), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((global_ptr)(vp + r * D + 8 * ((lane % PIECES) ^ v_swizzle<D>(row))),
-                                         (lds_ptr)(v + at), 16, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rows, (lds_ptr)(to + (16 * wave + i * RPI) * D), 16,
+            (r * D + 8 * ((lane % PIECES) ^ tile_swizzle<D, KV>(16 * wave + r))) * 2, 0, 0, 0);
     }
 }
 
-// FP8: thread t loads a quarter of row t / 4.
-template <int DT, int D>
-__device__ __forceinline__ void fetch_tile_fp8(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0,
-                                               TileRegs<DT, D> &x)
+// FP8: lane l of wave w loads a quarter of row 16 w + l / 4, to be placed later.
+template <int D>
+struct TileRegs {
+    static constexpr int W = D / 64;
+    u32x4 x[W];
+    uint32_t scale;
+};
+
+template <int D, int KV>
+__device__ __forceinline__ void fetch_fp8(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0,
+                                          TileRegs<D> &t)
 {
     const uint32_t r = lane_id() / 4, piece = lane_id() % 4;
     const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
-    const uint64_t kr = row_index(a.c, page, 0, head, row0) + r, vr = row_index(a.c, page, 1, head, row0) + r;
+    const uint64_t first = row_index(a.c, page, KV, head, row0);
+    const uint8_t *p = a.c.data + first * D + (r * D + piece * (D / 4));
 #pragma unroll
-    for (int i = 0; i < TileRegs<DT, D>::W; ++i) {
-        x.k[i] = *reinterpret_cast<const u32x4 *>(a.c.data + kr * D + piece * (D / 4) + 16 * i);
-        x.v[i] = *reinterpret_cast<const u32x4 *>(a.c.data + vr * D + piece * (D / 4) + 16 * i);
-    }
-    x.ks = a.c.scales[kr];
-    x.vs = a.c.scales[vr];
+    for (int i = 0; i < TileRegs<D>::W; ++i) t.x[i] = *reinterpret_cast<const u32x4 *>(p + 16 * i);
+    t.scale = *reinterpret_cast<const uint32_t *>(a.c.scales + first + r / 4 * 4);
 }
 
-template <int DT, int D>
-__device__ __forceinline__ void place_tile_fp8(const TileRegs<DT, D> &x, uint32_t wave, uint16_t *k, uint16_t *v)
+template <int DT, int D, int KV>
+__device__ __forceinline__ void place_fp8(const TileRegs<D> &t, uint32_t wave, uint16_t *to)
 {
     const uint32_t row = 16 * wave + lane_id() / 4, piece = lane_id() % 4;
-    const uint32_t ks = x.ks << 23, vs = x.vs << 23;
+    const uint32_t s = ((t.scale >> (8 * (row % 4))) & 0xFFu) << 23;
 #pragma unroll
-    for (int i = 0; i < TileRegs<DT, D>::W; ++i)
+    for (int i = 0; i < TileRegs<D>::W; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const uint32_t c = piece * (D / 32) + 2 * i + e;     // 16-byte piece of the BF16 row
-            const uint32_t k0 = x.k[i][2 * e], k1 = x.k[i][2 * e + 1], v0 = x.v[i][2 * e], v1 = x.v[i][2 * e + 1];
-            *reinterpret_cast<u32x4 *>(k + row * D + 8 * (c ^ k_swizzle<D>(row))) =
-                u32x4{fp8_pair_to_bf16<DT, false>(k0, ks), fp8_pair_to_bf16<DT, true>(k0, ks),
-                      fp8_pair_to_bf16<DT, false>(k1, ks), fp8_pair_to_bf16<DT, true>(k1, ks)};
-            *reinterpret_cast<u32x4 *>(v + row * D + 8 * (c ^ v_swizzle<D>(row))) =
-                u32x4{fp8_pair_to_bf16<DT, false>(v0, vs), fp8_pair_to_bf16<DT, true>(v0, vs),
-                      fp8_pair_to_bf16<DT, false>(v1, vs), fp8_pair_to_bf16<DT, true>(v1, vs)};
+            const uint32_t w0 = t.x[i][2 * e], w1 = t.x[i][2 * e + 1];
+            *reinterpret_cast<u32x4 *>(to + row * D + 8 * (c ^ tile_swizzle<D, KV>(row))) =
+                u32x4{fp8_pair_to_bf16<DT, false>(w0, s), fp8_pair_to_bf16<DT, true>(w0, s),
+                      fp8_pair_to_bf16<DT, false>(w1, s), fp8_pair_to_bf16<DT, true>(w1, s)};
         }
 }
 
-// V^T of 16 keys and 32 d as a product's first operand: keys base + 4 g + 0..3
-// and base + 8 + 4 g + 0..3 of d = 32 db + lane % 32.  Each 16 lanes of a
+// The places that a lane reads differ between the pieces of a row by an
+// exclusive or of constants, and between rows by constants: one register
+// holds them all.  opaque() keeps the compiler from holding each.
+__device__ __forceinline__ uint32_t opaque(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// K of 32 keys as the first operand: key 32 b + lane % 32, d = 16 i + 8 g + 0..7.
+template <int D>
+__device__ __forceinline__ uint32_t k_place()
+{
+    const uint32_t row = lane_id() % 32, g = lane_id() / 32;
+    return (row * D + 8 * (g ^ k_swizzle<D>(row))) * 2;
+}
+template <int D>
+__device__ __forceinline__ bf16x8 k_operand(LdsPtr k, uint32_t place, int b, int i)
+{
+    typedef __attribute__((address_space(3))) const u32x4 *lds_ptr;
+    return __builtin_bit_cast(bf16x8, *(lds_ptr)(k + ((place ^ (32 * i)) / 2 + 32 * b * D)));
+}
+
+// V^T of 16 keys and 32 d as the first operand: keys base + 4 g + 0..3 and
+// base + 8 + 4 g + 0..3 of d = 32 j + lane % 32.  Each 16 lanes of a
 // transposing read take 4 rows x 16 d.
 template <int D>
-__device__ __forceinline__ bf16x8 v_operand(const uint16_t *v, uint32_t base, uint32_t db)
+__device__ __forceinline__ uint32_t v_place()
+{
+    const uint32_t lane = lane_id(), i = lane % 16, g = lane / 32, half = lane / 16 % 2;
+    const uint32_t row = 4 * g + i / 4, col = 16 * half + 4 * (i % 4);
+    return (row * D + 8 * ((col / 8) ^ v_swizzle<D>(row)) + col % 8) * 2;
+}
+template <int D>
+__device__ __forceinline__ bf16x8 v_operand(LdsPtr v, uint32_t place, uint32_t base, int j)
 {
     typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
-    const uint32_t lane = lane_id(), i = lane % 16, g = lane / 32, half = lane / 16 % 2;
-    const uint32_t col = 32 * db + 16 * half + 4 * (i % 4);
-    const uint32_t r0 = base + 4 * g + i / 4, r1 = r0 + 8;
-    const s16x4 w0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_ptr)(v + r0 * D + 8 * ((col / 8) ^ v_swizzle<D>(r0)) + col % 8));
-    const s16x4 w1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_ptr)(v + r1 * D + 8 * ((col / 8) ^ v_swizzle<D>(r1)) + col % 8));
     typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const uint32_t at = (place ^ (64 * j)) / 2 + base * D;
+    const s16x4 w0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(v + at));
+    const s16x4 w1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(v + at + 8 * D));
     return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -633,15 +665,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
     if (!whole && begin >= end) return;                                        // no row's chunk: nobody reads it
     const int32_t all_lo = a.window > 0 ? max(0, p_last - a.window + 1) : 0;   // every row sees [all_lo, p_first]
 
-    bf16x8 q[D / 16];
+    bf16x8 q[D / 16];               // a row that is not there computes what the last one does, and stores nothing
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        u32x4 w = {0, 0, 0, 0};
-        if (mine)
-            w = *reinterpret_cast<const u32x4 *>(a.q + (uint64_t)(s.start + tok) * a.q_token +
-                                                 (uint64_t)q_head * a.q_head + 16 * i + 8 * g);
-        q[i] = __builtin_bit_cast(bf16x8, w);
-    }
+    for (int i = 0; i < D / 16; ++i)
+        q[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(a.q + (uint64_t)(s.start + tok) * a.q_token +
+                                                                           (uint64_t)q_head * a.q_head + 16 * i + 8 * g));
 
     f32x16 o[DB];
 #pragma unroll
@@ -651,77 +679,68 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
     float m = kNone, l = 0.f;
 
     // A wave fetches 16 rows of a tile: one page (or part of one).  The pages
-    // of its next 64 tiles, a lane each, in one load.  Rows behind the
-    // sequence's end come from its last page and are hidden.
-    uint32_t ahead = 0, at = 0;
-    const auto look_ahead = [&](int32_t from) {
+    // of 64 tiles, a lane each, in one load; V follows K by two tiles.  Rows
+    // behind the sequence's end come from its last page and are hidden.
+    uint32_t ahead = 0, before = 0;
+    const auto look_ahead = [&](uint32_t tile) SZ_INLINE {
+        before = ahead;
         ahead = page_of(a.c, a.b, seq,
-                        (uint32_t)min((int64_t)from + (int64_t)lane * kTileKeys + 16 * wave, (int64_t)s.len - 1));
-        at = 0;
+                        (uint32_t)min((int64_t)begin + ((int64_t)tile + lane) * kTileKeys + 16 * wave,
+                                      (int64_t)s.len - 1));
     };
-    TileRegs<DT, D> regs;
-    const auto fetch = [&](int32_t from, uint32_t into) {
-        if (at == 64) look_ahead(from);
-        const uint32_t page = __builtin_amdgcn_readlane(ahead, at++);
+    const uint32_t tiles = begin < end ? (uint32_t)(end - begin + (int32_t)kTileKeys - 1) / kTileKeys : 0;
+    TileRegs<D> kr, vr;
+    const auto fetch_k = [&](uint32_t t, LdsPtr to) SZ_INLINE {
+        if (t % 64 == 0) look_ahead(t);
+        const uint32_t page = __builtin_amdgcn_readlane(ahead, t % 64);
+        const int32_t key0 = begin + (int32_t)(t * kTileKeys + 16 * wave);
         if constexpr (DT == SZ_BF16)
-            fetch_tile_bf16<D>(a, head, page, from + 16 * (int32_t)wave, wave, lds.k[into], lds.v[into]);
+            fetch_bf16<D, 0>(a, head, page, key0, wave, to);
         else
-            fetch_tile_fp8<DT, D>(a, head, page, from + 16 * (int32_t)wave, regs);
+            fetch_fp8<D, 0>(a, head, page, key0, kr);
     };
-    if (begin < end) {
-        look_ahead(begin);
-        fetch(begin, 0);
-        if constexpr (DT != SZ_BF16) place_tile_fp8<DT, D>(regs, wave, lds.k[0], lds.v[0]);
-    }
-    uint32_t buf = 0;
-    for (int32_t kb = begin; kb < end; kb += kTileKeys, buf ^= 1) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                       // this wave's loads into LDS are done
-        __syncthreads();                                                       // this tile is in LDS, the other is free
-        const bool more = kb + (int32_t)kTileKeys < end;
-        if (more) fetch(kb + (int32_t)kTileKeys, buf ^ 1);
-        const uint16_t *kt = lds.k[buf];
-        uint16_t *vt = lds.v[buf];
+    const auto fetch_v = [&](uint32_t t, bool older, LdsPtr to) SZ_INLINE {
+        const uint32_t page = __builtin_amdgcn_readlane(older ? before : ahead, t % 64);
+        const int32_t key0 = begin + (int32_t)(t * kTileKeys + 16 * wave);
+        if constexpr (DT == SZ_BF16)
+            fetch_bf16<D, 1>(a, head, page, key0, wave, to);
+        else
+            fetch_fp8<D, 1>(a, head, page, key0, vr);
+    };
+    const auto place_k = [&](uint32_t t) SZ_INLINE {
+        if constexpr (DT != SZ_BF16) place_fp8<DT, D, 0>(kr, wave, lds.k[t % 2]);
+    };
+    const auto place_v = [&](uint32_t t) SZ_INLINE {
+        if constexpr (DT != SZ_BF16) place_fp8<DT, D, 1>(vr, wave, lds.v[t % 2]);
+    };
+    // Every wave's part of what was fetched is in LDS, and what was read is free.
+    const auto meet = [&]() SZ_INLINE {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    };
 
-        // scores
-        f32x16 st[2];
+    const uint32_t k_at = k_place<D>(), v_at = v_place<D>();
+    f32x16 st[2];
+    const auto scores = [&](LdsPtr k, int b) SZ_INLINE {                               // of 32 keys
+        const uint32_t place = opaque(k_at);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int r = 0; r < 16; ++r) st[b][r] = 0.f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) st[b][r] = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint32_t row = 32 * b + n;
-                const u32x4 w =
-                    *reinterpret_cast<const u32x4 *>(kt + row * D + 8 * ((uint32_t)(2 * i + g) ^ k_swizzle<D>(row)));
-                st[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), q[i], st[b], 0, 0, 0);
-            }
-        }
-
-        // Hidden keys, as in sz_attn_rows: -inf scores; V rows that no row of
-        // this tile sees become zeros in LDS; NaN and infinities in the others
-        // are counted further down.
-        const bool masked = kb < all_lo || kb + (int32_t)kTileKeys - 1 > p_first;
-        bool wild = false;
-        if (masked) {
-            if (threadIdx.x == 0) lds.wild = 0;
-            __syncthreads();
-            const uint32_t row = threadIdx.x / 4;
-            const int32_t key = kb + (int32_t)row;
-            const bool dead = key < any_lo || key > p_last;
-            uint32_t found = 0;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                u32x4 *p = reinterpret_cast<u32x4 *>(vt + row * D + (threadIdx.x % 4) * (D / 4) + 8 * i);
-                if (dead)
-                    *p = u32x4{0, 0, 0, 0};
-                else {
-                    const u32x4 w = *p;
-                    found |= not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3]);
-                }
-            }
-            if (found & kNotFinite) lds.wild = 1;
-            __syncthreads();
-            wild = lds.wild != 0;
+        for (int i = 0; i < D / 16; ++i)
+            st[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_operand<D>(k, place, b, i), q[i], st[b],
+                                                            0, 0, 0);
+    };
+    const auto masked = [&](uint32_t t) SZ_INLINE {
+        const int32_t kb = begin + (int32_t)(t * kTileKeys);
+        return kb < all_lo || kb + (int32_t)kTileKeys - 1 > p_first;
+    };
+    // Hides tile t's scores and raises the running maximum.  The sums of the
+    // tile before are not in o yet when it rises: o is scaled after them.
+    float late = 1.f;
+    bool scale_late = false;
+    const auto settle = [&](uint32_t t) SZ_INLINE {
+        if (masked(t)) {
+            const int32_t kb = begin + (int32_t)(t * kTileKeys);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -730,82 +749,185 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
                     if (k < lo || k > hi) st[b][r] = kNone;
                 }
         }
-
-        // running maximum
         float top = kNone;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, st[b][r]);
         top *= a.c2;
-        if (__any(top > m + kSlack)) {
+        scale_late = __any(top > m + kSlack);
+        if (scale_late) {
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             const float raised = fmaxf(m, top);
-            const float f = raised == kNone ? 1.f : exp2_fast(m - raised);
+            // not below the smallest normal: what was infinite stays so
+            late = raised == kNone ? 1.f : fmaxf(exp2_fast(m - raised), 1.17549435e-38f);
             m = raised;
-            l *= f;
-#pragma unroll
-            for (int j = 0; j < DB; ++j) o[j] *= f;
+            l *= late;
         }
-        const float base = m == kNone ? 0.f : m;
-        bf16x8 p[2][2];
+    };
+    bf16x8 p[2][2];                                                            // probabilities, the second operand
+    const auto values = [&](LdsPtr v, int b) SZ_INLINE {
+        const uint32_t place = opaque(v_at);
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t w[4];
+            for (int j = 0; j < DB; ++j)
+                o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    v_operand<D>(v, place, 32 * b + 16 * k, j), p[b][k], o[j], 0, 0, 0);
+    };
+    const auto scale_sums = [&]() SZ_INLINE {
+        if (scale_late)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p0 = exp2_fast(__builtin_fmaf(st[b][8 * t + 2 * e], a.c2, -base));
-                    const float p1 = exp2_fast(__builtin_fmaf(st[b][8 * t + 2 * e + 1], a.c2, -base));
-                    l += p0 + p1;
-                    w[e] = bf16_pair(p0, p1);
-                }
-                p[b][t] = __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+            for (int j = 0; j < DB; ++j) o[j] *= late;
+    };
+    // V of a tile that some row does not see all of: rows that none sees
+    // become zeros in LDS (0 times a NaN is one); NaN and infinities in the
+    // others are counted and taken out.
+    const auto clear_hidden = [&](uint32_t t) SZ_INLINE {
+        const int32_t kb = begin + (int32_t)(t * kTileKeys);
+        uint16_t *vt = lds.v[t % 2];
+        if (threadIdx.x == 0) lds.wild = 0;
+        __syncthreads();
+        const int32_t key = kb + (int32_t)threadIdx.x / 4;
+        const bool dead = key < any_lo || key > p_last;
+        u32x4 *mine4 = reinterpret_cast<u32x4 *>(vt + threadIdx.x / 4 * D + threadIdx.x % 4 * (D / 4));
+        uint32_t found = 0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            if (dead) {
+                mine4[i] = u32x4{0, 0, 0, 0};
+            } else {
+                const u32x4 w = mine4[i];
+                found |= not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3]);
             }
+        }
+        if (found & kNotFinite) lds.wild = 1;
+        __syncthreads();
+        if (lds.wild == 0) return;
+#pragma unroll 1
+        for (int j = 0; j < DB; ++j) {
+            f32x16 c;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) c[r] = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int32_t at = kb + 16 * k + 4 * (int32_t)g;
+                const u32x4 sw = {seen_pair(at, lo, hi), seen_pair(at + 2, lo, hi), seen_pair(at + 8, lo, hi),
+                                  seen_pair(at + 10, lo, hi)};
+                u32x4 w = __builtin_bit_cast(u32x4, v_operand<D>((LdsPtr)vt, v_at, 16 * k, j));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = kinds(w[e]);
+                c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
+                                                            __builtin_bit_cast(bf16x8, sw), c, 0, 0, 0);
+            }
+#pragma unroll
+            for (int jj = 0; jj < DB; ++jj)
+                if (jj == j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[jj][r] += from_kinds(c[r]);
+        }
+        __syncthreads();                                                       // every wave has counted
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const u32x4 w = mine4[i];
+            mine4[i] = u32x4{finite(w[0]), finite(w[1]), finite(w[2]), finite(w[3])};
+        }
+        __syncthreads();
+    };
 
-        if (__builtin_expect(wild, 0)) {
-#pragma unroll 1
-            for (int j = 0; j < DB; ++j) {
-                f32x16 c;
+    // Tile t's probabilities are worked out (vector unit) beside tile t - 1's
+    // values and tile t + 1's scores (matrix unit): V is needed one tile
+    // behind and K one ahead, and each is fetched the iteration before, into
+    // the half that the iteration before that has read.  The order is laid
+    // down here, one product to a slot with its share of the vector work (28
+    // cycles an element, 32 a product) and the LDS read of three slots on:
+    // values first, since the scores take the registers of the old ones.  The
+    // last iteration's scores are of whatever its half holds, and unused.
+    // (The four halves are named, and told apart by __restrict__, so that no
+    // read waits for the loads into the others.)
+    const auto beside = [&](uint32_t t, LdsPtr __restrict__ k_to, LdsPtr __restrict__ v_to,
+                            LdsPtr __restrict__ k_from, LdsPtr __restrict__ v_from) SZ_INLINE {
+        if (t + 2 < tiles) fetch_k(t + 2, k_to);
+        fetch_v(t, min(t + 2, tiles - 1) / 64 != t / 64, v_to);
+        constexpr int V_SLOTS = 4 * DB, K_SLOTS = D / 16, SLOTS = V_SLOTS + 2 * K_SLOTS, AHEAD = 3;
+        const uint32_t kp = opaque(k_at), vp = opaque(v_at);
+        const auto operand = [&](int slot) SZ_INLINE {
+            if (slot < V_SLOTS) return v_operand<D>(v_from, vp, 16 * (slot / DB), slot % DB);
+            return k_operand<D>(k_from, kp, (slot - V_SLOTS) / K_SLOTS, (slot - V_SLOTS) % K_SLOTS);
+        };
+        const float base = m == kNone ? 0.f : m;
+        uint32_t next[16];
+        float even = 0.f;
+        bf16x8 ring[AHEAD + 1];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) c[r] = 0.f;
-#pragma unroll 1
-                for (int t = 0; t < 4; ++t) {
-                    const int32_t key = kb + 16 * t + 4 * (int32_t)g;
-                    const u32x4 sw = {seen_pair(key, lo, hi), seen_pair(key + 2, lo, hi), seen_pair(key + 8, lo, hi),
-                                      seen_pair(key + 10, lo, hi)};
-                    u32x4 w = __builtin_bit_cast(u32x4, v_operand<D>(vt, 16 * t, j));
+        for (int i = 0; i < AHEAD; ++i) ring[i] = operand(i);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = kinds(w[e]);
-                    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
-                                                                __builtin_bit_cast(bf16x8, sw), c, 0, 0, 0);
+        for (int slot = 0; slot < SLOTS; ++slot) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (slot + AHEAD < SLOTS) ring[(slot + AHEAD) % (AHEAD + 1)] = operand(slot + AHEAD);
+            const bf16x8 x = ring[slot % (AHEAD + 1)];
+            if (slot < V_SLOTS) {
+                o[slot % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, p[slot / DB / 2][slot / DB % 2], o[slot % DB],
+                                                                       0, 0, 0);
+            } else {
+                const int b = (slot - V_SLOTS) / K_SLOTS, i = (slot - V_SLOTS) % K_SLOTS;
+                if (i == 0)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) st[b][r] = 0.f;
+                st[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[i], st[b], 0, 0, 0);
+            }
+            constexpr int SHARE = V_SLOTS + K_SLOTS;                           // slots with vector work
+#pragma unroll
+            for (int e = slot * 32 / SHARE; e < (slot + 1) * 32 / SHARE && e < 32; ++e) {
+                const float x1 = exp2_fast(__builtin_fmaf(st[e / 16][e % 16], a.c2, -base));
+                if (e % 2 == 0) {
+                    even = x1;
+                } else {
+                    l += even + x1;
+                    next[e / 2] = bf16_pair(even, x1);
+                    asm volatile("" : "+v"(l), "+v"(next[e / 2]));             // worked out here, not where they are used
                 }
-#pragma unroll
-                for (int jj = 0; jj < DB; ++jj)
-                    if (jj == j)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) o[jj][r] += from_kinds(c[r]);
             }
-            __syncthreads();                                                   // every wave has counted
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                u32x4 *x = reinterpret_cast<u32x4 *>(vt + threadIdx.x / 4 * D + threadIdx.x % 4 * (D / 4) + 8 * i);
-                const u32x4 w = *x;
-                *x = u32x4{finite(w[0]), finite(w[1]), finite(w[2]), finite(w[3])};
-            }
-            __syncthreads();
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int i = 0; i < 4; ++i)
+            p[i / 2][i % 2] = __builtin_bit_cast(
+                bf16x8, (u32x4{next[4 * i], next[4 * i + 1], next[4 * i + 2], next[4 * i + 3]}));
+    };
+    if (tiles > 0) {
+        fetch_k(0, (LdsPtr)lds.k[0]);
+        place_k(0);
+        if (tiles > 1) {
+            fetch_k(1, (LdsPtr)lds.k[1]);
+            place_k(1);
+        }
+        // "the tile before the first": no values, no probabilities
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+        for (int i = 0; i < D / 32; ++i)
+            reinterpret_cast<u32x4 *>(lds.v[1])[threadIdx.x + kAttnThreads * i] = u32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int j = 0; j < DB; ++j)
-                    o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_operand<D>(vt, 32 * b + 16 * t, j), p[b][t], o[j],
-                                                                    0, 0, 0);
-        if constexpr (DT != SZ_BF16)
-            if (more) place_tile_fp8<DT, D>(regs, wave, lds.k[buf ^ 1], lds.v[buf ^ 1]);
+        for (int b = 0; b < 2; ++b) p[b][0] = p[b][1] = __builtin_bit_cast(bf16x8, (u32x4{0, 0, 0, 0}));
+        meet();
+        scores((LdsPtr)lds.k[0], 0);
+        scores((LdsPtr)lds.k[0], 1);
+        settle(0);
+        scale_late = false;                                                    // o is still zero
+        uint32_t t = 0;
+        while (true) {
+            const uint32_t even = t % 2, odd = even ^ 1;
+            beside(t, (LdsPtr)lds.k[even], (LdsPtr)lds.v[even], (LdsPtr)lds.k[odd], (LdsPtr)lds.v[odd]);
+            scale_sums();
+            scale_late = false;
+            if (t + 1 < tiles) settle(t + 1);
+            if (t + 2 < tiles) place_k(t + 2);
+            place_v(t);
+            meet();
+            if (masked(t)) clear_hidden(t);
+            if (++t == tiles) break;
+        }
+        values((LdsPtr)lds.v[(tiles - 1) % 2], 0);
+        values((LdsPtr)lds.v[(tiles - 1) % 2], 1);
     }
 
     l += __shfl_xor(l, 32, 64);
