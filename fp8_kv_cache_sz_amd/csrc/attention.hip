@@ -42,7 +42,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kAttnThreads = 256;
 constexpr uint32_t kRowsMax = 16;        // rows of sz_attn_rows
-constexpr uint32_t kTileRows = 128;      // rows of sz_attn_tiles
 constexpr uint32_t kTileKeys = 64;
 constexpr uint32_t kKeyAlign = 64;       // chunks start at multiples of this
 constexpr float kSlack = 8.0f;
@@ -516,65 +515,66 @@ __device__ __forceinline__ uint32_t tile_swizzle(uint32_t row)
 // Memory of the workgroup, known as such.
 typedef __attribute__((address_space(3))) uint16_t *LdsPtr;
 
-// BF16: wave w fetches rows 16 w .. 16 w + 15 of the tile's K (KV = 0) or V.
-template <int D, int KV>
-__device__ __forceinline__ void fetch_bf16(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0,
-                                           uint32_t wave, LdsPtr to)
-{
-    constexpr uint32_t PIECES = D / 8, RPI = 64 / PIECES;       // 16-byte pieces of a row, rows per instruction
-    const uint32_t lane = lane_id();
-    const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
-    uint16_t *p = reinterpret_cast<uint16_t *>(a.c.data) + row_index(a.c, page, KV, head, row0) * D;
-    // A buffer of these 16 rows: unlike a flat load into LDS, a buffer load
-    // leaves the waits of the LDS reads beside it exact.
-    const auto rows = __builtin_amdgcn_make_buffer_rsrc(p, 0, 16 * D * 2, 0x00027000);
-#pragma unroll
-    for (uint32_t i = 0; i < 16 / RPI; ++i) {
-        const uint32_t r = i * RPI + lane / PIECES;              // of this wave's 16
+// A wave fetches ROWS = 64 / WAVES rows of a tile's K (KV = 0) and V: part of
+// one page.  BF16: PARTS loads straight to LDS, through a buffer of the rows
+// (unlike a flat load into LDS, a buffer load leaves the waits of the LDS
+// reads beside it exact).
+template <int D, int KV, int WAVES>
+struct FetchBf16 {
+    static constexpr uint32_t ROWS = kTileKeys / WAVES, PIECES = D / 8, RPI = 64 / PIECES, PARTS = ROWS / RPI;
+    __amdgpu_buffer_rsrc_t rows;
+    __device__ __forceinline__ FetchBf16(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0)
+    {
+        const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
+        uint16_t *p = reinterpret_cast<uint16_t *>(a.c.data) + row_index(a.c, page, KV, head, row0) * D;
+        rows = __builtin_amdgcn_make_buffer_rsrc(p, 0, ROWS * D * 2, 0x00027000);
+    }
+    __device__ __forceinline__ void part(uint32_t wave, uint32_t i, LdsPtr to) const
+    {
+        const uint32_t r = i * RPI + lane_id() / PIECES;
         typedef __attribute__((address_space(3))) void *lds_ptr;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rows, (lds_ptr)(to + (16 * wave + i * RPI) * D), 16,
-            (r * D + 8 * ((lane % PIECES) ^ tile_swizzle<D, KV>(16 * wave + r))) * 2, 0, 0, 0);
+            rows, (lds_ptr)(to + (ROWS * wave + i * RPI) * D), 16,
+            (r * D + 8 * ((lane_id() % PIECES) ^ tile_swizzle<D, KV>(ROWS * wave + r))) * 2, 0, 0, 0);
     }
-}
-
-// FP8: lane l of wave w loads a quarter of row 16 w + l / 4, to be placed later.
-template <int D>
-struct TileRegs {
-    static constexpr int W = D / 64;
-    u32x4 x[W];
-    uint32_t scale;
 };
 
-template <int D, int KV>
-__device__ __forceinline__ void fetch_fp8(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0,
-                                          TileRegs<D> &t)
-{
-    const uint32_t r = lane_id() / 4, piece = lane_id() % 4;
-    const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
-    const uint64_t first = row_index(a.c, page, KV, head, row0);
-    const uint8_t *p = a.c.data + first * D + (r * D + piece * (D / 4));
+// FP8: lane l of wave w loads D / WAVES bytes of row ROWS w + l / WAVES, and
+// places them as BF16 later, eight values (one LDS write) at a time.
+template <int DT, int D, int KV, int WAVES>
+struct FetchFp8 {
+    static constexpr uint32_t ROWS = kTileKeys / WAVES, PARTS = D / WAVES / 8;
+    uint32_t x[2 * PARTS], scale;
+    __device__ __forceinline__ void load(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0)
+    {
+        const uint32_t r = lane_id() / WAVES, piece = lane_id() % WAVES;
+        const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
+        const uint64_t first = row_index(a.c, page, KV, head, row0);
+        const uint8_t *p = a.c.data + first * D + (r * D + piece * (D / WAVES));
+        if constexpr (PARTS == 1) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(p);
+            x[0] = w.x;
+            x[1] = w.y;
+        } else {
 #pragma unroll
-    for (int i = 0; i < TileRegs<D>::W; ++i) t.x[i] = *reinterpret_cast<const u32x4 *>(p + 16 * i);
-    t.scale = *reinterpret_cast<const uint32_t *>(a.c.scales + first + r / 4 * 4);
-}
-
-template <int DT, int D, int KV>
-__device__ __forceinline__ void place_fp8(const TileRegs<D> &t, uint32_t wave, uint16_t *to)
-{
-    const uint32_t row = 16 * wave + lane_id() / 4, piece = lane_id() % 4;
-    const uint32_t s = ((t.scale >> (8 * (row % 4))) & 0xFFu) << 23;
+            for (uint32_t i = 0; i < PARTS / 2; ++i) {
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(p + 16 * i);
 #pragma unroll
-    for (int i = 0; i < TileRegs<D>::W; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t c = piece * (D / 32) + 2 * i + e;     // 16-byte piece of the BF16 row
-            const uint32_t w0 = t.x[i][2 * e], w1 = t.x[i][2 * e + 1];
-            *reinterpret_cast<u32x4 *>(to + row * D + 8 * (c ^ tile_swizzle<D, KV>(row))) =
-                u32x4{fp8_pair_to_bf16<DT, false>(w0, s), fp8_pair_to_bf16<DT, true>(w0, s),
-                      fp8_pair_to_bf16<DT, false>(w1, s), fp8_pair_to_bf16<DT, true>(w1, s)};
+                for (uint32_t e = 0; e < 4; ++e) x[4 * i + e] = w[e];
+            }
         }
-}
+        scale = *reinterpret_cast<const uint32_t *>(a.c.scales + first + r / 4 * 4);
+    }
+    __device__ __forceinline__ void place(uint32_t wave, uint32_t i, LdsPtr to) const
+    {
+        const uint32_t row = ROWS * wave + lane_id() / WAVES, c = lane_id() % WAVES * PARTS + i;
+        const uint32_t s = ((scale >> (8 * (row % 4))) & 0xFFu) << 23;
+        typedef __attribute__((address_space(3))) u32x4 *lds_ptr;
+        *(lds_ptr)(to + row * D + 8 * (c ^ tile_swizzle<D, KV>(row))) =
+            u32x4{fp8_pair_to_bf16<DT, false>(x[2 * i], s), fp8_pair_to_bf16<DT, true>(x[2 * i], s),
+                  fp8_pair_to_bf16<DT, false>(x[2 * i + 1], s), fp8_pair_to_bf16<DT, true>(x[2 * i + 1], s)};
+    }
+};
 
 // The places that a lane reads differ between the pieces of a row by an
 // exclusive or of constants, and between rows by constants: one register
@@ -620,17 +620,21 @@ __device__ __forceinline__ bf16x8 v_operand(LdsPtr v, uint32_t place, uint32_t b
     return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <int DT, int D>
-__global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uint32_t slots)
+template <int DT, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint32_t slots)
 {
     constexpr int DB = D / 32;
+    constexpr uint32_t kTileRows = 32 * WAVES, ROWS = kTileKeys / WAVES;
     __shared__ TileLds<D> lds;
 
     const uint32_t head = blockIdx.x % a.c.heads;
     const uint32_t slot = slots - 1 - blockIdx.x / a.c.heads % slots;          // later tiles see more keys: first
     const uint32_t split = blockIdx.x / a.c.heads / slots;
 
-    // Sequence i owns the slots from floor(starts[i] G / 128) + i on: at least as many as its rows fill.
+    // Sequence i owns the slots from floor(starts[i] G / rows) + i on: at
+    // least as many as its rows fill.  (One sequence after another: the heads
+    // of one XCD then read the same keys out of its L2.  The longest tiles of
+    // all sequences first measured 445 us where this takes 385.)
     const auto first_slot = [&](uint32_t i) {
         return (int64_t)(((uint64_t)(uint32_t)max(a.b.starts[i], 0) * a.group) / kTileRows) + i;
     };
@@ -678,41 +682,18 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
         for (int r = 0; r < 16; ++r) o[j][r] = 0.f;
     float m = kNone, l = 0.f;
 
-    // A wave fetches 16 rows of a tile: one page (or part of one).  The pages
-    // of 64 tiles, a lane each, in one load; V follows K by two tiles.  Rows
-    // behind the sequence's end come from its last page and are hidden.
+    // A wave's part of a tile is of one page.  The pages of 64 tiles, a lane
+    // each, in one load; V follows K by two tiles.  Rows behind the sequence's
+    // end come from its last page and are hidden.
     uint32_t ahead = 0, before = 0;
     const auto look_ahead = [&](uint32_t tile) SZ_INLINE {
         before = ahead;
         ahead = page_of(a.c, a.b, seq,
-                        (uint32_t)min((int64_t)begin + ((int64_t)tile + lane) * kTileKeys + 16 * wave,
+                        (uint32_t)min((int64_t)begin + ((int64_t)tile + lane) * kTileKeys + ROWS * wave,
                                       (int64_t)s.len - 1));
     };
     const uint32_t tiles = begin < end ? (uint32_t)(end - begin + (int32_t)kTileKeys - 1) / kTileKeys : 0;
-    TileRegs<D> kr, vr;
-    const auto fetch_k = [&](uint32_t t, LdsPtr to) SZ_INLINE {
-        if (t % 64 == 0) look_ahead(t);
-        const uint32_t page = __builtin_amdgcn_readlane(ahead, t % 64);
-        const int32_t key0 = begin + (int32_t)(t * kTileKeys + 16 * wave);
-        if constexpr (DT == SZ_BF16)
-            fetch_bf16<D, 0>(a, head, page, key0, wave, to);
-        else
-            fetch_fp8<D, 0>(a, head, page, key0, kr);
-    };
-    const auto fetch_v = [&](uint32_t t, bool older, LdsPtr to) SZ_INLINE {
-        const uint32_t page = __builtin_amdgcn_readlane(older ? before : ahead, t % 64);
-        const int32_t key0 = begin + (int32_t)(t * kTileKeys + 16 * wave);
-        if constexpr (DT == SZ_BF16)
-            fetch_bf16<D, 1>(a, head, page, key0, wave, to);
-        else
-            fetch_fp8<D, 1>(a, head, page, key0, vr);
-    };
-    const auto place_k = [&](uint32_t t) SZ_INLINE {
-        if constexpr (DT != SZ_BF16) place_fp8<DT, D, 0>(kr, wave, lds.k[t % 2]);
-    };
-    const auto place_v = [&](uint32_t t) SZ_INLINE {
-        if constexpr (DT != SZ_BF16) place_fp8<DT, D, 1>(vr, wave, lds.v[t % 2]);
-    };
+    const auto first_of = [&](uint32_t t) SZ_INLINE { return begin + (int32_t)(t * kTileKeys + ROWS * wave); };
     // Every wave's part of what was fetched is in LDS, and what was read is free.
     const auto meet = [&]() SZ_INLINE {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -738,7 +719,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
     // tile before are not in o yet when it rises: o is scaled after them.
     float late = 1.f;
     bool scale_late = false;
+    float top0 = kNone;                                                        // of the first 32 keys, not hidden
     const auto settle = [&](uint32_t t) SZ_INLINE {
+        float top = top0;
         if (masked(t)) {
             const int32_t kb = begin + (int32_t)(t * kTileKeys);
 #pragma unroll
@@ -748,13 +731,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
                     const int32_t k = kb + 32 * b + 8 * (r / 4) + 4 * (int32_t)g + r % 4;
                     if (k < lo || k > hi) st[b][r] = kNone;
                 }
+            top = kNone;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, st[0][r]);
         }
-        float top = kNone;
+        float top1 = kNone;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, st[b][r]);
-        top *= a.c2;
+        for (int r = 0; r < 16; ++r) top1 = fmaxf(top1, st[1][r]);
+        top = fmaxf(top, top1) * a.c2;
         scale_late = __any(top > m + kSlack);
         if (scale_late) {
             top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -786,14 +770,15 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
     const auto clear_hidden = [&](uint32_t t) SZ_INLINE {
         const int32_t kb = begin + (int32_t)(t * kTileKeys);
         uint16_t *vt = lds.v[t % 2];
+        constexpr int PIECES = D / WAVES / 8;                                  // 16 bytes each, of a lane
         if (threadIdx.x == 0) lds.wild = 0;
         __syncthreads();
-        const int32_t key = kb + (int32_t)threadIdx.x / 4;
+        const int32_t key = kb + (int32_t)(threadIdx.x / WAVES);
         const bool dead = key < any_lo || key > p_last;
-        u32x4 *mine4 = reinterpret_cast<u32x4 *>(vt + threadIdx.x / 4 * D + threadIdx.x % 4 * (D / 4));
+        u32x4 *mine4 = reinterpret_cast<u32x4 *>(vt + threadIdx.x / WAVES * D + threadIdx.x % WAVES * (D / WAVES));
         uint32_t found = 0;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
+        for (int i = 0; i < PIECES; ++i) {
             if (dead) {
                 mine4[i] = u32x4{0, 0, 0, 0};
             } else {
@@ -828,7 +813,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
         }
         __syncthreads();                                                       // every wave has counted
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
+        for (int i = 0; i < PIECES; ++i) {
             const u32x4 w = mine4[i];
             mine4[i] = u32x4{finite(w[0]), finite(w[1]), finite(w[2]), finite(w[3])};
         }
@@ -840,15 +825,20 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
     // behind and K one ahead, and each is fetched the iteration before, into
     // the half that the iteration before that has read.  The order is laid
     // down here, one product to a slot with its share of the vector work (28
-    // cycles an element, 32 a product) and the LDS read of three slots on:
-    // values first, since the scores take the registers of the old ones.  The
-    // last iteration's scores are of whatever its half holds, and unused.
+    // cycles an element, 32 a product), the LDS read of three slots on and,
+    // every other slot, a load of the tiles to come: values first, since the
+    // scores take the registers of the old ones.  FP8 tiles, loaded in the
+    // first slots, are converted in the last ones, which have no
+    // probabilities.  The last iterations' scores, and what they fetch beyond
+    // the last tile, are unused.
     // (The four halves are named, and told apart by __restrict__, so that no
     // read waits for the loads into the others.)
     const auto beside = [&](uint32_t t, LdsPtr __restrict__ k_to, LdsPtr __restrict__ v_to,
                             LdsPtr __restrict__ k_from, LdsPtr __restrict__ v_from) SZ_INLINE {
-        if (t + 2 < tiles) fetch_k(t + 2, k_to);
-        fetch_v(t, min(t + 2, tiles - 1) / 64 != t / 64, v_to);
+        const uint32_t tk = min(t + 2, tiles - 1);
+        if (tk == t + 2 && tk % 64 == 0) look_ahead(tk);
+        const uint32_t k_page = __builtin_amdgcn_readlane(ahead, tk % 64);
+        const uint32_t v_page = __builtin_amdgcn_readlane(tk / 64 == t / 64 ? ahead : before, t % 64);
         constexpr int V_SLOTS = 4 * DB, K_SLOTS = D / 16, SLOTS = V_SLOTS + 2 * K_SLOTS, AHEAD = 3;
         const uint32_t kp = opaque(k_at), vp = opaque(v_at);
         const auto operand = [&](int slot) SZ_INLINE {
@@ -856,9 +846,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
             return k_operand<D>(k_from, kp, (slot - V_SLOTS) / K_SLOTS, (slot - V_SLOTS) % K_SLOTS);
         };
         const float base = m == kNone ? 0.f : m;
+        __builtin_amdgcn_s_setprio(1);                                         // before a wave that settles or fetches
         uint32_t next[16];
         float even = 0.f;
         bf16x8 ring[AHEAD + 1];
+        using Bf16K = FetchBf16<D, 0, WAVES>;
+        using Fp8K = FetchFp8<DT, D, 0, WAVES>;
+        const Bf16K bk(a, head, k_page, first_of(tk));
+        const FetchBf16<D, 1, WAVES> bv(a, head, v_page, first_of(t));
+        Fp8K fk;
+        FetchFp8<DT, D, 1, WAVES> fv;
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) ring[i] = operand(i);
 #pragma unroll
@@ -876,6 +873,21 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
                     for (int r = 0; r < 16; ++r) st[b][r] = 0.f;
                 st[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[i], st[b], 0, 0, 0);
             }
+            if constexpr (DT == SZ_BF16) {
+                const int i = slot / 2;
+                if (slot % 2 == 0 && i < (int)Bf16K::PARTS) bk.part(wave, i, k_to);
+                if (slot % 2 == 1 && i < (int)Bf16K::PARTS) bv.part(wave, i, v_to);
+            } else {
+                if (slot == 0) fk.load(a, head, k_page, first_of(tk));
+                if (slot == 1) fv.load(a, head, v_page, first_of(t));
+                constexpr int PER = (2 * Fp8K::PARTS + K_SLOTS - 1) / K_SLOTS;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const int i = (slot - V_SLOTS - K_SLOTS) * PER + e;
+                    if (i >= 0 && i < (int)Fp8K::PARTS) fk.place(wave, i, k_to);
+                    if (i >= (int)Fp8K::PARTS && i < 2 * (int)Fp8K::PARTS) fv.place(wave, i - Fp8K::PARTS, v_to);
+                }
+            }
             constexpr int SHARE = V_SLOTS + K_SLOTS;                           // slots with vector work
 #pragma unroll
             for (int e = slot * 32 / SHARE; e < (slot + 1) * 32 / SHARE && e < 32; ++e) {
@@ -890,27 +902,43 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
             }
         }
         __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(0);
+        top0 = kNone;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top0 = fmaxf(top0, st[0][r]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             p[i / 2][i % 2] = __builtin_bit_cast(
                 bf16x8, (u32x4{next[4 * i], next[4 * i + 1], next[4 * i + 2], next[4 * i + 3]}));
     };
     if (tiles > 0) {
-        fetch_k(0, (LdsPtr)lds.k[0]);
-        place_k(0);
-        if (tiles > 1) {
-            fetch_k(1, (LdsPtr)lds.k[1]);
-            place_k(1);
+        look_ahead(0);
+#pragma unroll
+        for (uint32_t t = 0; t < 2; ++t) {                                     // K of the first two tiles
+            const uint32_t tk = min(t, tiles - 1);
+            const uint32_t page = __builtin_amdgcn_readlane(ahead, tk);
+            if constexpr (DT == SZ_BF16) {
+                const FetchBf16<D, 0, WAVES> bk(a, head, page, first_of(tk));
+#pragma unroll
+                for (uint32_t i = 0; i < bk.PARTS; ++i) bk.part(wave, i, (LdsPtr)lds.k[t]);
+            } else {
+                FetchFp8<DT, D, 0, WAVES> fk;
+                fk.load(a, head, page, first_of(tk));
+#pragma unroll
+                for (uint32_t i = 0; i < fk.PARTS; ++i) fk.place(wave, i, (LdsPtr)lds.k[t]);
+            }
         }
         // "the tile before the first": no values, no probabilities
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            reinterpret_cast<u32x4 *>(lds.v[1])[threadIdx.x + kAttnThreads * i] = u32x4{0, 0, 0, 0};
+        for (int i = 0; i < D / 8 / WAVES; ++i)
+            reinterpret_cast<u32x4 *>(lds.v[1])[threadIdx.x + 64 * WAVES * i] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int b = 0; b < 2; ++b) p[b][0] = p[b][1] = __builtin_bit_cast(bf16x8, (u32x4{0, 0, 0, 0}));
         meet();
         scores((LdsPtr)lds.k[0], 0);
         scores((LdsPtr)lds.k[0], 1);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top0 = fmaxf(top0, st[0][r]);
         settle(0);
         scale_late = false;                                                    // o is still zero
         uint32_t t = 0;
@@ -920,8 +948,6 @@ __global__ __launch_bounds__(kAttnThreads, 2) void sz_attn_tiles(AttnArgs a, uin
             scale_sums();
             scale_late = false;
             if (t + 1 < tiles) settle(t + 1);
-            if (t + 2 < tiles) place_k(t + 2);
-            place_v(t);
             meet();
             if (masked(t)) clear_hidden(t);
             if (++t == tiles) break;
@@ -1024,7 +1050,7 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_
 // ---------------------------------------------------------------------------
 struct AttnPlan {
     bool rows, tiles;                 // which kernels the batch can need
-    uint32_t rows_waves;
+    uint32_t rows_waves, tile_waves;
     uint32_t rows_chunk, rows_splits, tile_chunk, tile_splits, slots;
 };
 
@@ -1032,7 +1058,7 @@ constexpr uint64_t kRowsGroups = 2048;        // workgroups that sz_attn_rows wa
 constexpr uint32_t kRowsMinChunk = 1024;
 constexpr uint32_t kWideKeys = 2048;          // sz_attn_rows with 8 waves and no chunks up to here
 constexpr uint64_t kWideGroups = 256;
-constexpr uint64_t kTileGroups = 512;
+constexpr uint64_t kTileWaves = 2048;         // waves that sz_attn_tiles wants: two a SIMD
 constexpr uint32_t kTileMinChunk = 512;
 
 // Chunks of the batch's keys so that `groups` workgroups become `want`.
@@ -1049,6 +1075,16 @@ void split_keys(uint64_t span, uint64_t groups, uint64_t want, uint32_t least, u
     splits = (uint32_t)std::max<uint64_t>(1, (span + c - 1) / c);
 }
 
+// Waves of sz_attn_tiles, 32 rows each.  Eight share one conversion of each
+// FP8 tile where four need two: 606 against 635 us for 2,048 tokens over
+// 16,384, where the rows still fill the card.  BF16 tiles need none, and eight
+// waves at one barrier measured slower (408 against 400 us for six prompts).
+uint32_t tile_waves(uint32_t dtype, const PagedBatch &b, uint32_t kv_heads, uint32_t group)
+{
+    const uint64_t rows = (uint64_t)b.tokens * group;
+    return dtype != SZ_BF16 && rows >= 256ull * b.seqs && rows * kv_heads >= 256ull * kTileWaves / 8 ? 8 : 4;
+}
+
 AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint32_t window)
 {
     AttnPlan p{};
@@ -1057,7 +1093,8 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
     if (window) span = std::min<uint64_t>(span, (uint64_t)window + b.max_new + kKeyAlign - 1);
     p.tiles = (uint64_t)b.max_new * group > kRowsMax;
     p.rows = !p.tiles || (b.seqs > 1 && group <= kRowsMax);      // a single sequence's rows all go the same way
-    p.slots = (uint32_t)std::min<uint64_t>((uint64_t)b.tokens * group / kTileRows + b.seqs, 0x7FFFFFFFu);
+    p.tile_waves = tile_waves(c->dtype, b, c->kv_heads, group);
+    p.slots = (uint32_t)std::min<uint64_t>((uint64_t)b.tokens * group / (32 * p.tile_waves) + b.seqs, 0x7FFFFFFFu);
     p.rows_splits = p.tile_splits = 1;
     p.rows_waves = 4;
     if (p.rows) {
@@ -1070,7 +1107,7 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
         }
     }
     if (p.tiles)
-        split_keys(span, (uint64_t)p.slots * c->kv_heads, kTileGroups, kTileMinChunk, p.tile_chunk, p.tile_splits);
+        split_keys(span, (uint64_t)p.slots * c->kv_heads, kTileWaves / p.tile_waves, kTileMinChunk, p.tile_chunk, p.tile_splits);
     return p;
 }
 
@@ -1095,7 +1132,10 @@ int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
         const uint64_t groups = (uint64_t)a.c.heads * p.slots * p.tile_splits;
         if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
         LaunchScope scope("sz_attn_tiles", s);
-        hipLaunchKernelGGL((sz_attn_tiles<DT, D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a, p.slots);
+        if (p.tile_waves == 8)
+            hipLaunchKernelGGL((sz_attn_tiles<DT, D, 8>), dim3((uint32_t)groups), dim3(512), 0, s, a, p.slots);
+        else
+            hipLaunchKernelGGL((sz_attn_tiles<DT, D, 4>), dim3((uint32_t)groups), dim3(256), 0, s, a, p.slots);
     }
     if (p.rows_splits > 1 || p.tile_splits > 1) {
         const uint32_t per_seq = p.tile_splits > 1 ? 0 : std::min(a.b.max_new, kRowsMax / a.group);
@@ -1128,7 +1168,7 @@ extern "C" uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, con
         splits = std::max(splits, std::min(splits_wanted((uint64_t)b.seqs * cache->kv_heads, kRowsGroups),
                                            ((uint64_t)b.max_kv + kRowsMinChunk - 1) / kRowsMinChunk));
     if (p.tiles)
-        splits = std::max(splits, std::min(splits_wanted((uint64_t)p.slots * cache->kv_heads, kTileGroups),
+        splits = std::max(splits, std::min(splits_wanted((uint64_t)p.slots * cache->kv_heads, kTileWaves / p.tile_waves),
                                            ((uint64_t)b.max_kv + kTileMinChunk - 1) / kTileMinChunk));
     return std::max<uint64_t>(256, attn_ws_bytes((uint32_t)splits, (uint64_t)b.tokens * q_heads, cache->head_dim));
 }
