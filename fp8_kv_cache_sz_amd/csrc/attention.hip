@@ -56,6 +56,7 @@ struct AttnArgs {
     float *lse;               // [tokens][q_heads] or null
     float *part;              // [splits][tokens][q_heads][D], o before the division by l
     float2 *part_ml;          // [splits][tokens][q_heads] (m', l)
+    uint32_t *arrived;        // [seqs][kv heads] chunks done, 0 between calls; null: sz_attn_join joins
     float c2;                 // scale log2 e
     uint32_t group, q_heads;
     int32_t window;           // 0: none
@@ -155,6 +156,61 @@ __device__ __forceinline__ void store_stats(const AttnArgs &a, bool whole, uint3
         a.lse[r] = empty ? kNone : (m + __log2f(l)) * 0.69314718055994530942f;
 }
 
+// Chunks that sequence s has.  One is the whole result.
+__device__ __forceinline__ uint32_t chunks_of(const Sequence &s, int32_t window, uint32_t chunk)
+{
+    return max(1u, ((uint32_t)(s.len - min(first_key(s, window), s.len)) + chunk - 1) / chunk);
+}
+
+// Joining chunks:  M = max m'_s;  o = sum 2^(m'_s - M) o_s / sum 2^(m'_s - M)
+// l_s.  D/4 lanes hold a row.
+struct Joined {
+    float m = kNone, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(float2 ml, float4 v)
+    {
+        const float raised = fmaxf(m, ml.x);
+        const float base = raised == kNone ? 0.f : raised;
+        const float f = exp2_fast(m - base), g = exp2_fast(ml.x - base);
+        m = raised;
+        l = l * f + ml.y * g;
+        o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
+    }
+};
+
+// The visible chunks [s0, s1) of a token at position p.
+__device__ __forceinline__ void chunk_range(const Sequence &s, int32_t p, int32_t window, uint32_t chunk, uint32_t &s0,
+                                            uint32_t &s1)
+{
+    int32_t lo, hi;
+    visible(p, window, lo, hi);
+    const int32_t first = first_key(s, window);
+    s0 = hi < 0 ? 0 : (uint32_t)(lo - first) / chunk;
+    s1 = hi < 0 ? 0 : (uint32_t)(hi - first) / chunk + 1;
+}
+
+// Every parts-th chunk of row r from s0 + part on, four in flight.
+template <int D>
+__device__ __forceinline__ void join_chunks(const AttnArgs &a, uint64_t r, uint32_t s0, uint32_t s1, uint32_t part,
+                                            uint32_t parts, uint32_t lane, Joined &x)
+{
+    const uint64_t stride = (uint64_t)a.b.tokens * a.q_heads;
+    constexpr int AHEAD = 4;
+    for (uint32_t k = s0 + part; k < s1; k += AHEAD * parts) {
+        float2 ml[AHEAD];
+        float4 v[AHEAD];
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            const uint64_t at = min(k + e * parts, s1 - 1) * stride + r;
+            ml[e] = a.part_ml[at];
+            v[e] = *reinterpret_cast<const float4 *>(a.part + at * D + lane * 4);
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e)
+            if (k + e * parts < s1) x.add(ml[e], v[e]);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // sz_attn_rows: at most 16 rows.  A workgroup takes one chunk of one KV
 // head's keys; its four waves take 32-key blocks in turn, each with its own
@@ -224,12 +280,14 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, uint32_t head, co
     }
 }
 
-template <int DT, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void sz_attn_rows(AttnArgs a)
+template <int DT, int D>
+__global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
 {
     constexpr int VD = D / 16;                      // d values of a lane
+    constexpr int WAVES = kAttnThreads / 64;
     __shared__ float lds_o[WAVES][kRowsMax][D + 4];
     __shared__ float2 lds_ml[WAVES][kRowsMax];
+    __shared__ uint32_t lds_last;
 
     const uint32_t head = blockIdx.x % a.c.heads;
     const uint32_t seq = blockIdx.x / a.c.heads % a.b.seqs;
@@ -237,7 +295,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void sz_attn_rows(A
     const Sequence s = sequence(a.b, seq);
     const uint32_t rows = (uint32_t)s.n * a.group;
     if (s.n == 0 || (uint32_t)s.n > kRowsMax || rows > kRowsMax) return;
-    const bool whole = a.rows_splits == 1;
+    const uint32_t chunks = chunks_of(s, a.window, a.rows_chunk);
+    const bool whole = chunks == 1;
     const int64_t begin64 = (int64_t)first_key(s, a.window) + (int64_t)split * a.rows_chunk;
     if (split > 0 && begin64 >= s.len) return;
     const int32_t begin = (int32_t)begin64;
@@ -451,26 +510,70 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void sz_attn_rows(A
     __syncthreads();
     // 256 threads, each VD values of one row
     const uint32_t row = threadIdx.x / 16, d = threadIdx.x % 16 * VD;
-    if (row >= rows) return;
-    float top = kNone, sum = 0.f, acc[VD];
+    if (row < rows) {
+        float top = kNone, sum = 0.f, acc[VD];
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, lds_ml[w][row].x);
-    const float base = top == kNone ? 0.f : top;
+        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, lds_ml[w][row].x);
+        const float base = top == kNone ? 0.f : top;
 #pragma unroll
-    for (int j = 0; j < VD; ++j) acc[j] = 0.f;
-#pragma unroll 4
-    for (int w = 0; w < WAVES; ++w) {
-        const float2 ml = lds_ml[w][row];
-        const float f = exp2_fast(ml.x - base);
-        sum += ml.y * f;
+        for (int j = 0; j < VD; ++j) acc[j] = 0.f;
 #pragma unroll
-        for (int j = 0; j < VD; ++j) acc[j] += lds_o[w][row][d + j] * f;
+        for (int w = 0; w < WAVES; ++w) {
+            const float2 ml = lds_ml[w][row];
+            const float f = exp2_fast(ml.x - base);
+            sum += ml.y * f;
+#pragma unroll
+            for (int j = 0; j < VD; ++j) acc[j] += lds_o[w][row][d + j] * f;
+        }
+        const uint32_t rtok = row / a.group;
+        const bool empty = s.len - s.n + (int32_t)rtok < 0;
+        const uint32_t rhead = head * a.group + row % a.group;
+        store_row<D, VD>(a, whole, split, s.start + rtok, rhead, d, acc, empty ? 0.f : 1.f / sum);
+        if (d == 0) store_stats(a, whole, split, s.start + rtok, rhead, empty, top, sum);
     }
-    const uint32_t rtok = row / a.group;
-    const bool empty = s.len - s.n + (int32_t)rtok < 0;
-    const uint32_t rhead = head * a.group + row % a.group;
-    store_row<D, VD>(a, whole, split, s.start + rtok, rhead, d, acc, empty ? 0.f : 1.f / sum);
-    if (d == 0) store_stats(a, whole, split, s.start + rtok, rhead, empty, top, sum);
+    if (whole || a.arrived == nullptr) return;
+
+    // The last chunk's workgroup to get here joins them.  Each has its
+    // partials written back (the wait, the barrier and the release) before it
+    // counts itself; the last one's count wraps to 0 for the next call, and
+    // it reads past its caches (the acquire).  The order of the sums is that
+    // of the chunks, whichever comes last.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+        lds_last = atomicInc(a.arrived + (uint64_t)seq * a.c.heads + head, chunks - 1) == chunks - 1;
+    }
+    __syncthreads();
+    if (!lds_last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    constexpr uint32_t LANES = D / 4, GROUPS = kAttnThreads / LANES;
+    float4(*meet_o)[LANES] = reinterpret_cast<float4(*)[LANES]>(&lds_o[0][0][0]);
+    float2 *meet_ml = &lds_ml[0][0];
+    uint32_t parts = GROUPS;                        // groups of lanes to a row
+    while (parts > 1 && GROUPS / parts < rows) parts /= 2;
+    const uint32_t lanes_group = threadIdx.x / LANES, jlane = threadIdx.x % LANES, part = lanes_group % parts;
+    for (uint32_t r0 = 0; r0 < rows; r0 += GROUPS / parts) {
+        const uint32_t r = r0 + lanes_group / parts;
+        const uint32_t jtok = r / a.group, jhead = head * a.group + r % a.group;
+        const int32_t jpos = s.len - s.n + (int32_t)jtok;
+        Joined x;
+        if (r < rows) {
+            uint32_t s0, s1;
+            chunk_range(s, jpos, a.window, a.rows_chunk, s0, s1);
+            join_chunks<D>(a, (uint64_t)(s.start + jtok) * a.q_heads + jhead, s0, s1, part, parts, jlane, x);
+        }
+        __syncthreads();
+        meet_o[lanes_group][jlane] = x.o;
+        if (jlane == 0) meet_ml[lanes_group] = make_float2(x.m, x.l);
+        __syncthreads();
+        if (r < rows && part == 0) {
+            for (uint32_t k = 1; k < parts; ++k) x.add(meet_ml[lanes_group + k], meet_o[lanes_group + k][jlane]);
+            const float w[4] = {x.o.x, x.o.y, x.o.z, x.o.w};
+            store_row<D, 4>(a, true, 0, s.start + jtok, jhead, jlane * 4, w, jpos < 0 ? 0.f : 1.f / x.l);
+            if (jlane == 0) store_stats(a, true, 0, s.start + jtok, jhead, jpos < 0, x.m, x.l);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -661,12 +764,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
 
     // the keys of this tile of rows, and of its chunk
     const int32_t p_first = s.len - s.n + tok_first, p_last = s.len - s.n + tok_last;
-    const bool whole = a.tile_splits == 1;
+    const bool whole = a.tile_splits == 1 || chunks_of(s, a.window, a.tile_chunk) == 1;
     const int64_t chunk0 = (int64_t)first_key(s, a.window) + (int64_t)split * a.tile_chunk;
     const int32_t any_lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;  // some row sees [any_lo, p_last]
     const int32_t begin = (int32_t)max(chunk0, (int64_t)(any_lo & ~(int32_t)(kTileKeys - 1)));
     const int32_t end = (int32_t)min((int64_t)p_last + 1, chunk0 + a.tile_chunk);
-    if (!whole && begin >= end) return;                                        // no row's chunk: nobody reads it
+    if (whole ? split > 0 : begin >= end) return;                              // no row's chunk: nobody reads it
     const int32_t all_lo = a.window > 0 ? max(0, p_last - a.window + 1) : 0;   // every row sees [all_lo, p_first]
 
     bf16x8 q[D / 16];               // a row that is not there computes what the last one does, and stores nothing
@@ -972,12 +1075,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
 
 // ---------------------------------------------------------------------------
 // sz_attn_join: a workgroup joins the chunks of one (token, head) row that
-// hold visible keys:  M = max m'_s;  o = sum 2^(m'_s - M) o_s / sum
-// 2^(m'_s - M) l_s.  D/4 lanes take a partial in 16-byte loads, so 8 (D = 64:
-// 16) partials are read at once, each such group of lanes keeping a running
-// maximum over every 8th (16th) chunk; the groups meet in LDS, in order.
-// With per_seq > 0 only sequences of sz_attn_rows were split: the grid is
-// their tokens, at most per_seq each; else it is all tokens.
+// hold visible keys.  8 (D = 64: 16) groups of lanes take every 8th (16th)
+// chunk each and meet in LDS, in order.  With per_seq > 0 only sequences of
+// sz_attn_rows were split: the grid is their tokens, at most per_seq each;
+// else it is all tokens.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_t per_seq)
@@ -1000,49 +1101,23 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_
         if ((int32_t)t < s.start || (int32_t)t >= s.start + s.n) return;
     }
     const bool few = (uint64_t)s.n * a.group <= a.rows_limit;
-    if ((few ? a.rows_splits : a.tile_splits) == 1) return;                    // already whole
     const uint32_t chunk = few ? a.rows_chunk : a.tile_chunk;
-    int32_t lo, hi;
-    visible(s.len - s.n + ((int32_t)t - s.start), a.window, lo, hi);
-    const bool empty = hi < 0;
-    const int32_t first = first_key(s, a.window);
-    const uint32_t s0 = empty ? 0 : (uint32_t)(lo - first) / chunk, s1 = empty ? 0 : (uint32_t)(hi - first) / chunk + 1;
-
+    if ((few ? a.rows_splits : a.tile_splits) == 1 || chunks_of(s, a.window, chunk) == 1) return;      // already whole
+    const int32_t p = s.len - s.n + ((int32_t)t - s.start);
+    uint32_t s0, s1;
+    chunk_range(s, p, a.window, chunk, s0, s1);
     const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-    const uint64_t r = (uint64_t)t * a.q_heads + head, stride = (uint64_t)a.b.tokens * a.q_heads;
-    float m = kNone, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto add = [&](float2 ml, float4 v) {
-        const float raised = fmaxf(m, ml.x);
-        const float base = raised == kNone ? 0.f : raised;
-        const float f = exp2_fast(m - base), g = exp2_fast(ml.x - base);
-        m = raised;
-        l = l * f + ml.y * g;
-        o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
-    };
-    constexpr int AHEAD = 4;
-    for (uint32_t k = s0 + group; k < s1; k += AHEAD * GROUPS) {
-        float2 ml[AHEAD];
-        float4 v[AHEAD];
-#pragma unroll
-        for (int e = 0; e < AHEAD; ++e) {
-            const uint64_t at = min(k + e * GROUPS, s1 - 1) * stride + r;
-            ml[e] = a.part_ml[at];
-            v[e] = *reinterpret_cast<const float4 *>(a.part + at * D + lane * 4);
-        }
-#pragma unroll
-        for (int e = 0; e < AHEAD; ++e)
-            if (k + e * GROUPS < s1) add(ml[e], v[e]);
-    }
-    lds_o[group][lane] = o;
-    if (lane == 0) lds_ml[group] = make_float2(m, l);
+    Joined x;
+    join_chunks<D>(a, (uint64_t)t * a.q_heads + head, s0, s1, group, GROUPS, lane, x);
+    lds_o[group][lane] = x.o;
+    if (lane == 0) lds_ml[group] = make_float2(x.m, x.l);
     __syncthreads();
     if (group != 0) return;
 #pragma unroll
-    for (uint32_t g = 1; g < GROUPS; ++g) add(lds_ml[g], lds_o[g][lane]);
-    const float w[4] = {o.x, o.y, o.z, o.w};
-    store_row<D, 4>(a, true, 0, t, head, lane * 4, w, empty ? 0.f : 1.f / l);
-    if (lane == 0) store_stats(a, true, 0, t, head, empty, m, l);
+    for (uint32_t g = 1; g < GROUPS; ++g) x.add(lds_ml[g], lds_o[g][lane]);
+    const float w[4] = {x.o.x, x.o.y, x.o.z, x.o.w};
+    store_row<D, 4>(a, true, 0, t, head, lane * 4, w, p < 0 ? 0.f : 1.f / x.l);
+    if (lane == 0) store_stats(a, true, 0, t, head, p < 0, x.m, x.l);
 }
 
 // ---------------------------------------------------------------------------
@@ -1050,29 +1125,44 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_
 // ---------------------------------------------------------------------------
 struct AttnPlan {
     bool rows, tiles;                 // which kernels the batch can need
-    uint32_t rows_waves, tile_waves;
+    bool fused;                       // sz_attn_rows joins its chunks itself
+    uint32_t tile_waves;
     uint32_t rows_chunk, rows_splits, tile_chunk, tile_splits, slots;
 };
 
 constexpr uint64_t kRowsGroups = 2048;        // workgroups that sz_attn_rows wants
-constexpr uint32_t kRowsMinChunk = 1024;
-constexpr uint32_t kWideKeys = 2048;          // sz_attn_rows with 8 waves and no chunks up to here
-constexpr uint64_t kWideGroups = 256;
 constexpr uint64_t kTileWaves = 2048;         // waves that sz_attn_tiles wants: two a SIMD
-constexpr uint32_t kTileMinChunk = 512;
+constexpr uint32_t kMinChunk = 128;           // keys: a block for each wave, two tiles
+constexpr uint32_t kMaxLeast = 1024;
+constexpr uint64_t kArrivals = SZ_ATTENTION_COUNTERS / 4;      // counters at the workspace's start
+constexpr uint64_t kJoinChunks = 64;
+// Up to so many workgroups join their chunks themselves.  It saves a launch
+// (one sequence of 1,001 tokens: 9.7 us where two launches take 12.8), but
+// each workgroup's release writes back its XCD's L2: with 256 workgroups a 64K
+// context took 43 us where sz_attn_join makes it 29, with 1,200 a step of 64
+// sequences 188 where it is 127.
+constexpr uint64_t kFusedGroups = 128;
+static_assert(kFusedGroups <= kArrivals);
 
-// Chunks of the batch's keys so that `groups` workgroups become `want`.
-uint64_t splits_wanted(uint64_t groups, uint64_t want) { return std::max<uint64_t>(1, want / groups); }
+uint64_t round_up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
-// Splits of `span` keys so that `groups` workgroups become `want`, in chunks
-// of at least `least` keys.
-void split_keys(uint64_t span, uint64_t groups, uint64_t want, uint32_t least, uint32_t &chunk, uint32_t &splits)
+// Splits of `span` keys so that `groups` workgroups become `want`.  A chunk
+// is not made shorter than a 64th of the keys (joining grows with their
+// number) unless that is over kMaxLeast.
+void split_keys(uint64_t span, uint64_t groups, uint64_t want, uint32_t &chunk, uint32_t &splits)
 {
-    const uint64_t n = splits_wanted(groups, want);
-    uint64_t c = std::max<uint64_t>(least, (span + n - 1) / n);
-    c = (c + 127) / 128 * 128;
+    const uint64_t n = std::max<uint64_t>(1, want / std::max<uint64_t>(1, groups));
+    const uint64_t least = std::min<uint64_t>(kMaxLeast, round_up((span + kJoinChunks - 1) / kJoinChunks, kMinChunk));
+    const uint64_t c = round_up(std::max<uint64_t>({kMinChunk, least, (span + n - 1) / n}), kMinChunk);
     chunk = (uint32_t)c;
     splits = (uint32_t)std::max<uint64_t>(1, (span + c - 1) / c);
+}
+
+// No span up to this one gives more chunks than:
+uint64_t most_splits(uint64_t span, uint64_t groups, uint64_t want)
+{
+    const uint64_t n = std::max<uint64_t>(1, want / std::max<uint64_t>(1, groups));
+    return std::min<uint64_t>(n, (span + kMinChunk - 1) / kMinChunk);
 }
 
 // Waves of sz_attn_tiles, 32 rows each.  Eight share one conversion of each
@@ -1092,28 +1182,25 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
     uint64_t span = b.max_kv;
     if (window) span = std::min<uint64_t>(span, (uint64_t)window + b.max_new + kKeyAlign - 1);
     p.tiles = (uint64_t)b.max_new * group > kRowsMax;
-    p.rows = !p.tiles || (b.seqs > 1 && group <= kRowsMax);      // a single sequence's rows all go the same way
+    // Sequences of few rows beside others: none if there is one sequence (its
+    // rows all go the same way) or every sequence has max_new tokens.
+    p.rows = !p.tiles || (b.seqs > 1 && group <= kRowsMax && b.tokens != (uint64_t)b.seqs * b.max_new);
     p.tile_waves = tile_waves(c->dtype, b, c->kv_heads, group);
     p.slots = (uint32_t)std::min<uint64_t>((uint64_t)b.tokens * group / (32 * p.tile_waves) + b.seqs, 0x7FFFFFFFu);
     p.rows_splits = p.tile_splits = 1;
-    p.rows_waves = 4;
-    if (p.rows) {
-        const uint64_t groups = (uint64_t)b.seqs * c->kv_heads;
-        if (groups <= kWideGroups && span <= kWideKeys) {
-            p.rows_waves = 8;
-            p.rows_chunk = (uint32_t)(span + 127) / 128 * 128;
-        } else {
-            split_keys(span, groups, kRowsGroups, kRowsMinChunk, p.rows_chunk, p.rows_splits);
-        }
-    }
+    p.rows_chunk = p.tile_chunk = kMinChunk;
+    const uint64_t groups = (uint64_t)b.seqs * c->kv_heads;
+    if (p.rows) split_keys(span, groups, kRowsGroups, p.rows_chunk, p.rows_splits);
     if (p.tiles)
-        split_keys(span, (uint64_t)p.slots * c->kv_heads, kTileWaves / p.tile_waves, kTileMinChunk, p.tile_chunk, p.tile_splits);
+        split_keys(span, (uint64_t)p.slots * c->kv_heads, kTileWaves / p.tile_waves, p.tile_chunk, p.tile_splits);
+    p.fused = p.rows_splits > 1 && p.tile_splits == 1 && groups * p.rows_splits <= kFusedGroups;
     return p;
 }
 
-uint64_t attn_ws_bytes(uint32_t splits, uint64_t rows, uint32_t head_dim)
+// Workspace: kArrivals counters, then the partials of the chunks.
+uint64_t attn_ws_bytes(uint64_t splits, uint64_t rows, uint32_t head_dim)
 {
-    return splits == 1 ? 0 : up256(splits * rows * head_dim * 4) + up256(splits * rows * 8);
+    return 4 * kArrivals + (splits == 1 ? 0 : up256(splits * rows * head_dim * 4) + up256(splits * rows * 8));
 }
 
 template <int DT, int D>
@@ -1123,10 +1210,7 @@ int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
         const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits;
         if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
         LaunchScope scope("sz_attn_rows", s);
-        if (p.rows_waves == 8)
-            hipLaunchKernelGGL((sz_attn_rows<DT, D, 8>), dim3((uint32_t)groups), dim3(512), 0, s, a);
-        else
-            hipLaunchKernelGGL((sz_attn_rows<DT, D, 4>), dim3((uint32_t)groups), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((sz_attn_rows<DT, D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
     }
     if (p.tiles) {
         const uint64_t groups = (uint64_t)a.c.heads * p.slots * p.tile_splits;
@@ -1137,7 +1221,7 @@ int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
         else
             hipLaunchKernelGGL((sz_attn_tiles<DT, D, 4>), dim3((uint32_t)groups), dim3(256), 0, s, a, p.slots);
     }
-    if (p.rows_splits > 1 || p.tile_splits > 1) {
+    if ((p.rows_splits > 1 && !p.fused) || p.tile_splits > 1) {
         const uint32_t per_seq = p.tile_splits > 1 ? 0 : std::min(a.b.max_new, kRowsMax / a.group);
         const uint64_t groups = (per_seq ? (uint64_t)a.b.seqs * per_seq : (uint64_t)a.b.tokens) * a.q_heads;
         if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
@@ -1160,17 +1244,14 @@ extern "C" uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, con
     b.tokens = batch->tokens;
     b.max_new = std::min(batch->max_new, batch->tokens);
     b.max_kv = batch->max_kv;
-    if (b.seqs == 0 || b.tokens == 0) return 256;
+    if (b.seqs == 0 || b.tokens == 0) return attn_ws_bytes(1, 0, 0);
     // the most chunks that any window gives
     const AttnPlan p = attn_plan(cache, b, q_heads / cache->kv_heads, 0);
     uint64_t splits = 1;
-    if (p.rows)
-        splits = std::max(splits, std::min(splits_wanted((uint64_t)b.seqs * cache->kv_heads, kRowsGroups),
-                                           ((uint64_t)b.max_kv + kRowsMinChunk - 1) / kRowsMinChunk));
+    if (p.rows) splits = std::max(splits, most_splits(b.max_kv, (uint64_t)b.seqs * cache->kv_heads, kRowsGroups));
     if (p.tiles)
-        splits = std::max(splits, std::min(splits_wanted((uint64_t)p.slots * cache->kv_heads, kTileWaves / p.tile_waves),
-                                           ((uint64_t)b.max_kv + kTileMinChunk - 1) / kTileMinChunk));
-    return std::max<uint64_t>(256, attn_ws_bytes((uint32_t)splits, (uint64_t)b.tokens * q_heads, cache->head_dim));
+        splits = std::max(splits, most_splits(b.max_kv, (uint64_t)p.slots * cache->kv_heads, kTileWaves / p.tile_waves));
+    return attn_ws_bytes(splits, (uint64_t)b.tokens * q_heads, cache->head_dim);
 }
 
 extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void *d_q, uint32_t q_heads,
@@ -1191,15 +1272,17 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     const AttnPlan p = attn_plan(cache, a.b, a.group, window);
     const uint32_t splits = std::max(p.rows_splits, p.tile_splits);
     const uint64_t rows = (uint64_t)a.b.tokens * q_heads;
-    if (splits > 1 && !d_ws) return SZ_E_ARG;
+    if (!d_ws) return SZ_E_ARG;
     if (ws_bytes < attn_ws_bytes(splits, rows, cache->head_dim)) return SZ_E_WORKSPACE;
     a.q = static_cast<const uint16_t *>(d_q);
     a.q_token = q_token_stride;
     a.q_head = q_head_stride;
     a.out = static_cast<uint16_t *>(d_out);
     a.lse = d_lse;
-    a.part = static_cast<float *>(d_ws);
-    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(d_ws) + up256(splits * rows * cache->head_dim * 4));
+    a.arrived = p.fused ? static_cast<uint32_t *>(d_ws) : nullptr;
+    a.part = static_cast<float *>(d_ws) + kArrivals;
+    a.part_ml = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(a.part) +
+                                           up256(splits * rows * cache->head_dim * 4));
     a.c2 = scale * 1.44269504088896340736f;
     a.q_heads = q_heads;
     a.window = (int32_t)window;

@@ -26,6 +26,7 @@ from . import _native
 from ._native import SZ_BF16, SZ_FP8_E4M3, SZ_FP8_E5M2, SplitZipError
 
 E4M3 = SZ_FP8_E4M3
+ARRIVALS = 4096         # bytes of counters at the start of an attention workspace
 
 _ELEMENT = {SZ_BF16: torch.bfloat16, SZ_FP8_E5M2: torch.float8_e5m2, SZ_FP8_E4M3: torch.float8_e4m3fn}
 
@@ -136,38 +137,36 @@ def _rows(name, t, tokens, heads, cache):
         raise ValueError("%s is [%d, %d, %d], got %s" % (name, tokens, heads, cache.head_dim, tuple(t.shape)))
     if t.device != cache.device:
         raise ValueError("%s is on %s, the cache on %s" % (name, t.device, cache.device))
-    stride = t.stride()
-    if stride[2] != 1 and t.numel():
+    token, head, last = t.stride()
+    if last != 1 and tokens:
         raise ValueError("%s needs contiguous rows (a last stride of 1)" % name)
-    return t.data_ptr(), stride[0], stride[1]
+    return t.data_ptr(), token, head
 
 
 def _run(name, call, cache, batch, args, stream, owned=()):
     """Launches a call on `stream` (None: the current one) with the cache's
     device current.  Memory that this layer took from the current stream's
     pool (`owned`) is handed over to a stream other than that."""
-    if batch.device != cache.device:
-        raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
     device = cache.device
+    if batch.device != device:
+        raise ValueError("the batch is on %s, the cache on %s" % (batch.device, device))
+    index = device.index
     if device.type != "cuda":
         raise ValueError("the cache is on %s; its calls run on the GPU" % device)
-    side = None
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        handle = stream.cuda_stream
-        current = torch.cuda.current_stream(device)
-        if stream != current:
-            side = stream
-            if owned:
-                side.wait_stream(current)
-    if torch.cuda.current_device() == device.index:
-        rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status, handle)
-    else:
-        with torch.cuda.device(device):
-            rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status, handle)
-    if rc:
-        _native.check(name, rc)
+    if stream is None and torch.cuda.current_device() == index:
+        # the common case, without a Stream object: small calls are as short as their launch
+        rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status,
+                  torch._C._cuda_getCurrentRawStream(index))
+        if rc:
+            _native.check(name, rc)
+        return
+    current = torch.cuda.current_stream(device)
+    side = None if stream is None or stream == current else stream
+    if side is not None and owned:
+        side.wait_stream(current)
+    with torch.cuda.device(device):
+        rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status, (side or current).cuda_stream)
+    _native.check(name, rc)
     if side is not None:
         for t in owned:
             t.record_stream(side)
@@ -205,15 +204,17 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
     ``[tokens, kv_heads, head_dim]`` (sz_cache_read).  ``out``: such a pair to
     read into.  Rows of tokens that belong to no sequence keep what they
     held."""
+    tokens, heads, dim = batch.tokens, cache.kv_heads, cache.head_dim
     owned = ()
     if out is None:
-        both = torch.empty((2, batch.tokens, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16,
-                           device=cache.device)
+        both = torch.empty((2, tokens, heads, dim), dtype=torch.bfloat16, device=cache.device)
         owned = (both,)
-        out = both[0], both[1]
-    k, v = out
-    args = (*_rows("out[0]", k, batch.tokens, cache.kv_heads, cache),
-            *_rows("out[1]", v, batch.tokens, cache.kv_heads, cache))
+        k, v = both.unbind(0)
+        at, row = both.data_ptr(), heads * dim
+        args = (at, row, dim, at + tokens * row * 2, row, dim)
+    else:
+        k, v = out
+        args = (*_rows("out[0]", k, tokens, heads, cache), *_rows("out[1]", v, tokens, heads, cache))
     _run("sz_cache_read", _native.lib.sz_cache_read, cache, batch, args, stream, owned)
     if check:
         _raise_status(cache, stream)
@@ -221,11 +222,14 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
 
 
 def attention_workspace(cache: PagedCache, batch: PageBatch, q_heads: int) -> torch.Tensor:
-    """A workspace for ``paged_attention`` of this batch's bounds, with any window."""
+    """A workspace for ``paged_attention`` of this batch's bounds, with any
+    window.  Its first ``ARRIVALS`` bytes are zero, as every call leaves them."""
     if q_heads <= 0 or q_heads % cache.kv_heads:
         raise ValueError("q_heads is a multiple of the cache's %d KV heads, got %d" % (cache.kv_heads, q_heads))
     n = _native.sz_paged_attention_workspace_size(cache._ref, batch._ref(cache.page_tokens), q_heads)
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    ws[:ARRIVALS].zero_()
+    return ws
 
 
 def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale: float | None = None,
@@ -247,12 +251,12 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
         raise ValueError("window counts from 0 (0: none)")
     owned = []
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         owned.append(out)
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != cache.device:
         raise ValueError("out is a contiguous bfloat16 tensor of q's shape on the cache's device")
     if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device)
+        lse = q.new_empty((batch.tokens, q_heads), dtype=torch.float32)
         owned.append(lse)
     elif lse is False:
         lse = None
@@ -263,7 +267,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
         ws = attention_workspace(cache, batch, q_heads)
         owned.append(ws)
     elif not ws.is_contiguous() or ws.device != cache.device:
-        raise ValueError("ws is a contiguous tensor on the cache's device")
+        raise ValueError("ws is a contiguous tensor on the cache's device (attention_workspace)")
     _run("sz_paged_attention", _native.lib.sz_paged_attention, cache, batch,
          (qp, q_heads, q_token, q_head, cache.head_dim ** -0.5 if scale is None else scale, min(window, 1 << 30),
           out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes), stream, owned)

@@ -395,8 +395,12 @@ int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uin
  * and max_kv in its last bits, through the split of the keys.  scale must be
  * finite and above 0.  d_ws: ws_bytes >=
  * sz_paged_attention_workspace_size(cache, batch, q_heads) (0 for heads that
- * do not divide; host fields of cache and batch only).  Returns SZ_OK,
- * SZ_E_DTYPE, SZ_E_ARG, SZ_E_ALIGN, SZ_E_WORKSPACE or SZ_E_HIP. */
+ * do not divide; host fields of cache and batch only).  Its first
+ * SZ_ATTENTION_COUNTERS bytes are counters of chunks done: the caller clears
+ * them once, and every call finds and leaves them 0, whatever shapes the
+ * calls that share the workspace have.  Returns SZ_OK, SZ_E_DTYPE, SZ_E_ARG,
+ * SZ_E_ALIGN, SZ_E_WORKSPACE or SZ_E_HIP. */
+enum { SZ_ATTENTION_COUNTERS = 4096 };
 uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, const sz_batch *batch, uint32_t q_heads);
 int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void *d_q, uint32_t q_heads,
                        uint64_t q_token_stride, uint64_t q_head_stride, float scale, uint32_t window, void *d_out,
