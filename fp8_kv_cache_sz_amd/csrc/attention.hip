@@ -4,14 +4,16 @@
 // h / G), over the visible keys j, max(0, p - window + 1) <= j <= p:
 //   s_j = scale q . K_j      m = max s_j      l = sum exp(s_j - m)
 //   o   = sum exp(s_j - m) V_j / l            lse = m + ln l
-// computed in one pass over the keys with a running m and l (in powers of
-// two: exp(s - m) = 2^(c s - m'), c = scale log2 e).  m' need not be the
-// maximum itself, only near enough that no power overflows: it is raised,
+// computed in one pass over the keys with a running m and l, in powers of two:
+// exp(s - m) = 2^(c (x - m')), x = q . K_j, c = scale log2 e.  m' need not be
+// the maximum itself, only near enough that no power overflows: it is raised,
 // and the sums scaled, only when a score exceeds it by more than 2^kSlack,
-// which is rare after the first keys.  Scores, m, l and o are 32 bits; the
-// probabilities are rounded to BF16 (relative 2^-9 each, errors of either
-// sign) because the matrix instructions take BF16, and K and V enter as the
-// exact BF16 values that sz_cache_read returns.
+// which is rare after the first keys.  Scores, m', l and o are 32 bits, and K
+// and V enter as the exact BF16 values that sz_cache_read returns.  The matrix
+// instructions take BF16 probabilities: sz_attn_rows, which waits for memory,
+// gives them what the rounding left as a second product; sz_attn_tiles, bound
+// by those products, rounds (at most 2^-8 of each, of either sign, as much as
+// the result's own rounding).
 //
 // Rows are (token, head of the KV head's group), so one K/V row read serves
 // the G query heads of its KV head.  Both kernels compute S^T = K Q^T, whose
@@ -57,7 +59,7 @@ struct AttnArgs {
     float *part;              // [splits][tokens][q_heads][D], o before the division by l
     float2 *part_ml;          // [splits][tokens][q_heads] (m', l)
     uint32_t *arrived;        // [seqs][kv heads] chunks done, 0 between calls; null: sz_attn_join joins
-    float c2;                 // scale log2 e
+    float scale, c2;          // c2: scale log2 e
     uint32_t group, q_heads;
     int32_t window;           // 0: none
     uint32_t rows_limit;      // sequences of up to so many rows are sz_attn_rows's
@@ -80,6 +82,38 @@ __device__ __forceinline__ void visible(int32_t p, int32_t window, int32_t &lo, 
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A row's running reference.  The powers are 2^(c x - base) with base = c m'
+// rounded: one fused multiply each.  delta = c m' - base is what the rounding
+// left; it keeps the reference exact where it changes.  Where |c m'| is over
+// kFar the rounding could be a power of its own, so there (far, of the whole
+// wave: rare) the scores are made differences x - m' first, and base = -delta.
+constexpr float kFar = 1048576.f;
+struct Reference {
+    float top = kNone, delta = 0.f;                    // m' and delta
+    __device__ __forceinline__ bool below(float x, float c) const { return (x - top) * c > kSlack; }
+    // Raises m' to x at least; what the sums so far are to be scaled by.
+    __device__ __forceinline__ float raise(float x, float c)
+    {
+        const float raised = fmaxf(top, x), base = raised * c;
+        const float rest = fabsf(base) <= kFar ? __builtin_fmaf(raised, c, -base) : 0.f;
+        const float f = raised == kNone ? 1.f : exp2_fast(__builtin_fmaf(top - raised, c, rest - delta));
+        top = raised;
+        delta = rest;
+        return f;
+    }
+    __device__ __forceinline__ bool is_far(float c) const { return top != kNone && !(fabsf(top * c) <= kFar); }
+    __device__ __forceinline__ float origin() const { return top == kNone ? 0.f : top; }       // of far differences
+    __device__ __forceinline__ float base(float c, bool far) const
+    {
+        return top == kNone ? 0.f : far ? -delta : __builtin_fmaf(top, c, -delta);
+    }
+};
+// 2^(c (x - top)) for sums that were made with m' = x
+__device__ __forceinline__ float rebased(float x, float top, float c)
+{
+    return exp2_fast((x - (top == kNone ? 0.f : top)) * c);
+}
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
@@ -153,7 +187,7 @@ __device__ __forceinline__ void store_stats(const AttnArgs &a, bool whole, uint3
     if (!whole)
         a.part_ml[(uint64_t)split * a.b.tokens * a.q_heads + r] = make_float2(m, l);
     else if (a.lse)
-        a.lse[r] = empty ? kNone : (m + __log2f(l)) * 0.69314718055994530942f;
+        a.lse[r] = empty ? kNone : __builtin_fmaf(__log2f(l), 0.69314718055994530942f, m * a.scale);
 }
 
 // Chunks that sequence s has.  One is the whole result.
@@ -162,16 +196,15 @@ __device__ __forceinline__ uint32_t chunks_of(const Sequence &s, int32_t window,
     return max(1u, ((uint32_t)(s.len - min(first_key(s, window), s.len)) + chunk - 1) / chunk);
 }
 
-// Joining chunks:  M = max m'_s;  o = sum 2^(m'_s - M) o_s / sum 2^(m'_s - M)
-// l_s.  D/4 lanes hold a row.
+// Joining chunks:  M = max m'_s;  f_s = 2^(c (m'_s - M));  o = sum f_s o_s /
+// sum f_s l_s.  D/4 lanes hold a row.
 struct Joined {
     float m = kNone, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    __device__ __forceinline__ void add(float2 ml, float4 v)
+    __device__ __forceinline__ void add(float2 ml, float4 v, float c)
     {
         const float raised = fmaxf(m, ml.x);
-        const float base = raised == kNone ? 0.f : raised;
-        const float f = exp2_fast(m - base), g = exp2_fast(ml.x - base);
+        const float f = rebased(m, raised, c), g = rebased(ml.x, raised, c);
         m = raised;
         l = l * f + ml.y * g;
         o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
@@ -207,7 +240,7 @@ __device__ __forceinline__ void join_chunks(const AttnArgs &a, uint64_t r, uint3
         }
 #pragma unroll
         for (int e = 0; e < AHEAD; ++e)
-            if (k + e * parts < s1) x.add(ml[e], v[e]);
+            if (k + e * parts < s1) x.add(ml[e], v[e], a.c2);
     }
 }
 
@@ -328,7 +361,9 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
     f32x4 o[VD];
 #pragma unroll
     for (int j = 0; j < VD; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = kNone, l = 0.f;
+    Reference ref;
+    bool far = false;
+    float l = 0.f;
 
     const int32_t all_lo = a.window > 0 ? max(0, s.len - a.window) : 0;      // every row sees [all_lo, all_hi]
     const int32_t all_hi = s.len - s.n;
@@ -433,18 +468,19 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
         float top = kNone;
 #pragma unroll
         for (int r = 0; r < 8; ++r) top = fmaxf(top, st[r / 4][r % 4]);
-        top *= a.c2;
-        if (__any(top > m + kSlack)) {
+        if (__any(ref.below(top, a.c2))) {
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float raised = fmaxf(m, top);
-            const float f = raised == kNone ? 1.f : exp2_fast(m - raised);
-            m = raised;
+            const float f = ref.raise(top, a.c2);
+            far = __any(ref.is_far(a.c2));
             l *= f;
 #pragma unroll
             for (int j = 0; j < VD; ++j) o[j] *= f;
         }
-        const float base = m == kNone ? 0.f : m;
+        if (far)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) st[r / 4][r % 4] -= ref.origin();
+        const float base = ref.base(a.c2, far);
         float p[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
@@ -452,7 +488,14 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
             l += p[r];
         }
         const u32x4 pw = {bf16_pair(p[0], p[1]), bf16_pair(p[2], p[3]), bf16_pair(p[4], p[5]), bf16_pair(p[6], p[7])};
-        const bf16x8 pb = __builtin_bit_cast(bf16x8, pw);
+        // and what BF16 left of them: the products are cheap beside the reads
+        // (0 to 1 % of the time), and the result is as exact as its own rounding
+        u32x4 rw;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            rw[e] = bf16_pair(p[2 * e] - __builtin_bit_cast(float, pw[e] << 16),
+                              p[2 * e + 1] - __builtin_bit_cast(float, pw[e] & 0xFFFF0000u));
+        const bf16x8 pb = __builtin_bit_cast(bf16x8, pw), pr = __builtin_bit_cast(bf16x8, rw);
 
         if (MASKED && wild) {
             const int32_t key = kb + 4 * (int32_t)g;
@@ -481,6 +524,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
             const u32x4 w = {perm(v[1][j / 2], v[0][j / 2], sel), perm(v[3][j / 2], v[2][j / 2], sel),
                              perm(v[5][j / 2], v[4][j / 2], sel), perm(v[7][j / 2], v[6][j / 2], sel)};
             o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pb, o[j], 0, 0, 0);
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pr, o[j], 0, 0, 0);
         }
         if (more) {
             if (MASKED) {
@@ -500,7 +544,11 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
     // the waves' sums meet in LDS
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    if (g == 0) lds_ml[wave][n] = make_float2(m, l);
+    const float plain = exp2_fast(-ref.delta);      // to sums with m' itself as the reference
+    l *= plain;
+#pragma unroll
+    for (int j = 0; j < VD; ++j) o[j] *= plain;
+    if (g == 0) lds_ml[wave][n] = make_float2(ref.top, l);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -514,13 +562,12 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
         float top = kNone, sum = 0.f, acc[VD];
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) top = fmaxf(top, lds_ml[w][row].x);
-        const float base = top == kNone ? 0.f : top;
 #pragma unroll
         for (int j = 0; j < VD; ++j) acc[j] = 0.f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const float2 ml = lds_ml[w][row];
-            const float f = exp2_fast(ml.x - base);
+            const float f = rebased(ml.x, top, a.c2);
             sum += ml.y * f;
 #pragma unroll
             for (int j = 0; j < VD; ++j) acc[j] += lds_o[w][row][d + j] * f;
@@ -568,7 +615,7 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
         if (jlane == 0) meet_ml[lanes_group] = make_float2(x.m, x.l);
         __syncthreads();
         if (r < rows && part == 0) {
-            for (uint32_t k = 1; k < parts; ++k) x.add(meet_ml[lanes_group + k], meet_o[lanes_group + k][jlane]);
+            for (uint32_t k = 1; k < parts; ++k) x.add(meet_ml[lanes_group + k], meet_o[lanes_group + k][jlane], a.c2);
             const float w[4] = {x.o.x, x.o.y, x.o.z, x.o.w};
             store_row<D, 4>(a, true, 0, s.start + jtok, jhead, jlane * 4, w, jpos < 0 ? 0.f : 1.f / x.l);
             if (jlane == 0) store_stats(a, true, 0, s.start + jtok, jhead, jpos < 0, x.m, x.l);
@@ -783,7 +830,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
     for (int j = 0; j < DB; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[j][r] = 0.f;
-    float m = kNone, l = 0.f;
+    Reference ref;
+    bool far = false;
+    float l = 0.f;
 
     // A wave's part of a tile is of one page.  The pages of 64 tiles, a lane
     // each, in one load; V follows K by two tiles.  Rows behind the sequence's
@@ -841,16 +890,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
         float top1 = kNone;
 #pragma unroll
         for (int r = 0; r < 16; ++r) top1 = fmaxf(top1, st[1][r]);
-        top = fmaxf(top, top1) * a.c2;
-        scale_late = __any(top > m + kSlack);
+        top = fmaxf(top, top1);
+        scale_late = __any(ref.below(top, a.c2));
         if (scale_late) {
             top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float raised = fmaxf(m, top);
-            // not below the smallest normal: what was infinite stays so
-            late = raised == kNone ? 1.f : fmaxf(exp2_fast(m - raised), 1.17549435e-38f);
-            m = raised;
+            late = fmaxf(ref.raise(top, a.c2), 1.17549435e-38f);               // what was infinite stays so
+            far = __any(ref.is_far(a.c2));
             l *= late;
         }
+        if (far)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) st[b][r] -= ref.origin();
     };
     bf16x8 p[2][2];                                                            // probabilities, the second operand
     const auto values = [&](LdsPtr v, int b) SZ_INLINE {
@@ -948,7 +1000,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
             if (slot < V_SLOTS) return v_operand<D>(v_from, vp, 16 * (slot / DB), slot % DB);
             return k_operand<D>(k_from, kp, (slot - V_SLOTS) / K_SLOTS, (slot - V_SLOTS) % K_SLOTS);
         };
-        const float base = m == kNone ? 0.f : m;
+        const float base = ref.base(a.c2, far);
         __builtin_amdgcn_s_setprio(1);                                         // before a wave that settles or fetches
         uint32_t next[16];
         float even = 0.f;
@@ -1062,15 +1114,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
     l += __shfl_xor(l, 32, 64);
     if (!mine) return;
     const bool empty = pos < 0;
-    const float inv = empty ? 0.f : 1.f / l;
+    const float plain = exp2_fast(-ref.delta);                                 // to sums with m' itself as the reference
+    l *= plain;
+    const float inv = whole ? empty ? 0.f : plain / l : plain;
 #pragma unroll
     for (int j = 0; j < DB; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float w[4] = {o[j][4 * i], o[j][4 * i + 1], o[j][4 * i + 2], o[j][4 * i + 3]};
-            store_row<D, 4>(a, whole, split, s.start + tok, q_head, 32 * j + 8 * i + 4 * g, w, inv);
+            const float w[4] = {o[j][4 * i] * inv, o[j][4 * i + 1] * inv, o[j][4 * i + 2] * inv, o[j][4 * i + 3] * inv};
+            store_row<D, 4>(a, whole, split, s.start + tok, q_head, 32 * j + 8 * i + 4 * g, w, 1.f);
         }
-    if (g == 0) store_stats(a, whole, split, s.start + tok, q_head, empty, m, l);
+    if (g == 0) store_stats(a, whole, split, s.start + tok, q_head, empty, ref.top, l);
 }
 
 // ---------------------------------------------------------------------------
@@ -1114,7 +1168,7 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_
     __syncthreads();
     if (group != 0) return;
 #pragma unroll
-    for (uint32_t g = 1; g < GROUPS; ++g) x.add(lds_ml[g], lds_o[g][lane]);
+    for (uint32_t g = 1; g < GROUPS; ++g) x.add(lds_ml[g], lds_o[g][lane], a.c2);
     const float w[4] = {x.o.x, x.o.y, x.o.z, x.o.w};
     store_row<D, 4>(a, true, 0, t, head, lane * 4, w, p < 0 ? 0.f : 1.f / x.l);
     if (lane == 0) store_stats(a, true, 0, t, head, p < 0, x.m, x.l);
@@ -1267,7 +1321,7 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     if ((rc = check_rows(d_q, q_token_stride, q_head_stride, a.b.tokens, q_heads)) != SZ_OK) return rc;
     if (a.b.tokens && !d_out) return SZ_E_ARG;
     if (!aligned16(d_out) || !aligned16(d_ws) || (reinterpret_cast<uintptr_t>(d_lse) & 3u)) return SZ_E_ALIGN;
-    if (a.b.tokens == 0 || a.b.seqs == 0 || a.b.max_new == 0) return SZ_OK;
+    if (a.b.tokens == 0 || a.b.seqs == 0) return SZ_OK;
     a.group = q_heads / a.c.heads;
     const AttnPlan p = attn_plan(cache, a.b, a.group, window);
     const uint32_t splits = std::max(p.rows_splits, p.tile_splits);
@@ -1283,6 +1337,7 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     a.part = static_cast<float *>(d_ws) + kArrivals;
     a.part_ml = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(a.part) +
                                            up256(splits * rows * cache->head_dim * 4));
+    a.scale = scale;
     a.c2 = scale * 1.44269504088896340736f;
     a.q_heads = q_heads;
     a.window = (int32_t)window;

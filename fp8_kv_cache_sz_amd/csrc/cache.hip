@@ -109,24 +109,48 @@ __global__ __launch_bounds__(kMoveThreads) void sz_cache_move(PagedCache c, Page
     if (t0 >= b.tokens) return;
     const uint32_t lane = lane_id();
 
-    // The place of token t0 + lane as a row of pair 0, or none.
+    // The place of token t0 + lane as a row of pair 0, or none.  Loads that
+    // wait for one another are most of a wave's time, so the starts and
+    // lengths of the 64 sequences from t0's on come in one (up to 63
+    // sequences: the first), and each token counts its own from there.
     constexpr uint64_t NONE = ~0ull;
     uint64_t mine = NONE;
-    const int32_t first = wave_last_not_above(b.seqs + 1, t0, [&](uint32_t j) { return (int64_t)b.starts[j]; });
-    if (lane < kMoveTokens && t0 + lane < b.tokens && first < (int32_t)b.seqs) {
+    uint32_t base = 0;
+    for (uint32_t span = b.seqs + 1; span > 64;) {
+        const uint32_t step = (span + 63) / 64, at = lane * step;
+        const uint32_t hits = (uint32_t)__popcll(__ballot(at < span && (int64_t)b.starts[base + min(at, span - 1)] <= t0));
+        const uint32_t skip = hits > 0 ? (hits - 1) * step : 0;
+        base += skip;
+        span = min(step, span - skip);
+    }
+    const bool there = base + lane < b.seqs;
+    const int32_t start = base + lane <= b.seqs ? b.starts[base + lane] : INT32_MAX;
+    const int32_t len = there ? b.lens[base + lane] : 0;
+    uint32_t count = 0;                              // of the starts up to this lane's token
+#pragma unroll
+    for (uint32_t j = 0; j < kMoveTokens; ++j) {
+        const uint64_t passed = __ballot(start <= (int32_t)(t0 + j));
+        if (lane == j) count = (uint32_t)__popcll(passed);
+    }
+    const int32_t my_start = __shfl(start, (int)max(count, 1u) - 1, 64), my_next = __shfl(start, (int)min(count, 63u), 64);
+    const int32_t my_len = __shfl(len, (int)max(count, 1u) - 1, 64);
+    if (lane < kMoveTokens && t0 + lane < b.tokens && count > 0) {
         const uint32_t t = t0 + lane;
-        uint32_t i = (uint32_t)max(first, 0);
-        while (i < b.seqs && (int64_t)b.starts[i + 1] <= (int64_t)t) ++i;
-        if (i < b.seqs) {
-            const Sequence s = sequence(b, i);
-            const int32_t pos = s.len - s.n + ((int32_t)t - s.start);
-            if ((int32_t)t >= s.start && (int32_t)t < s.start + s.n && pos >= 0) {
-                const uint32_t page = (uint32_t)b.table[(uint64_t)i * b.width + ((uint32_t)pos >> c.lg_page)];
-                if (page < c.pages)
-                    mine = row_index(c, page, 0, 0, (uint32_t)pos & ((1u << c.lg_page) - 1));
-                else
-                    flag_batch(b);
-            }
+        uint32_t i = base + count - 1;
+        Sequence s{0, 0, 0};
+        if (count < 64) {
+            if (i < b.seqs) s = checked(b, my_start, my_next, my_len);
+        } else {                                     // 64 sequences on, or more
+            while (i < b.seqs && b.starts[i + 1] <= (int32_t)t) ++i;
+            if (i < b.seqs) s = sequence(b, i);
+        }
+        const int32_t pos = s.len - s.n + ((int32_t)t - s.start);
+        if ((int32_t)t >= s.start && (int32_t)t < s.start + s.n && pos >= 0) {
+            const uint32_t page = (uint32_t)b.table[(uint64_t)i * b.width + ((uint32_t)pos >> c.lg_page)];
+            if (page < c.pages)
+                mine = row_index(c, page, 0, 0, (uint32_t)pos & ((1u << c.lg_page) - 1));
+            else
+                flag_batch(b);
         }
     }
     const uint32_t sub = lane / LPR, off = (lane % LPR) * 8;
@@ -184,7 +208,7 @@ int move(const sz_cache *cache, const sz_batch *batch, void *d_k, uint64_t k_tok
     if (rc != SZ_OK) return rc;
     if ((rc = check_rows(d_k, k_token, k_head, b.tokens, c.heads)) != SZ_OK) return rc;
     if ((rc = check_rows(d_v, v_token, v_head, b.tokens, c.heads)) != SZ_OK) return rc;
-    if (b.tokens == 0 || b.seqs == 0 || b.max_kv == 0) return SZ_OK;
+    if (b.tokens == 0 || b.seqs == 0) return SZ_OK;
     const Rows x{{static_cast<uint16_t *>(d_k), static_cast<uint16_t *>(d_v)}, {k_token, v_token}, {k_head, v_head}};
     hipStream_t s = static_cast<hipStream_t>(stream);
     const uint64_t tiles = ((uint64_t)b.tokens + kMoveTokens - 1) / kMoveTokens;

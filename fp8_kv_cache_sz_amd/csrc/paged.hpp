@@ -89,23 +89,21 @@ __device__ __forceinline__ void flag_batch(const PagedBatch &b) { *b.status = SZ
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// The sequence's lengths, checked against the host's bounds; a sequence that
+// A sequence's lengths, checked against the host's bounds; a sequence that
 // contradicts them has no tokens.
-__device__ __forceinline__ Sequence sequence(const PagedBatch &b, uint32_t i)
+__device__ __forceinline__ Sequence checked(const PagedBatch &b, int32_t start, int32_t next, int32_t len)
 {
-    Sequence s;
-    s.start = b.starts[i];
-    s.n = b.starts[i + 1];
-    s.len = b.lens[i];
-    const bool good = s.start >= 0 && s.n >= s.start && s.n <= (int32_t)b.tokens &&
-                      s.n - s.start <= (int32_t)b.max_new && s.len >= 0 && s.len <= (int32_t)b.max_kv;
+    const bool good = start >= 0 && next >= start && next <= (int32_t)b.tokens && next - start <= (int32_t)b.max_new &&
+                      len >= 0 && len <= (int32_t)b.max_kv;
     if (!good) {
         flag_batch(b);
-        s = Sequence{0, 0, 0};
-    } else {
-        s.n -= s.start;
+        return Sequence{0, 0, 0};
     }
-    return s;
+    return Sequence{start, next - start, len};
+}
+__device__ __forceinline__ Sequence sequence(const PagedBatch &b, uint32_t i)
+{
+    return checked(b, b.starts[i], b.starts[i + 1], b.lens[i]);
 }
 
 // Largest i in [0, count) with key(i) <= x for ascending keys, or -1; one

@@ -215,6 +215,9 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
     else:
         k, v = out
         args = (*_rows("out[0]", k, tokens, heads, cache), *_rows("out[1]", v, tokens, heads, cache))
+        for token, head in (args[1:3], args[4:6]):
+            if (heads > 1 and head < dim) or (tokens > 1 and token < dim):
+                raise ValueError("out has rows that share memory")
     _run("sz_cache_read", _native.lib.sz_cache_read, cache, batch, args, stream, owned)
     if check:
         _raise_status(cache, stream)

@@ -390,7 +390,8 @@ int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uin
  * [tokens][q_heads][head_dim], contiguous.  d_lse: float [tokens][q_heads]
  * or NULL.  A token that sees no key gets 0 and -inf.  Keys that a token does
  * not see do not reach its result, NaN and infinities included.  Sums,
- * scores and lse are 32-bit; probabilities are rounded to BF16.  The result
+ * scores and lse are 32-bit; with more than 16 rows (new tokens times query
+ * heads of a KV head) in a sequence its probabilities are rounded to BF16.  The result
  * does not depend on what runs beside it, bit for bit; it depends on max_new
  * and max_kv in its last bits, through the split of the keys.  scale must be
  * finite and above 0.  d_ws: ws_bytes >=
