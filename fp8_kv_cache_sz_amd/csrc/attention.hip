@@ -28,6 +28,7 @@
 // (m, l, o) sz_attn_join joins, always in the order of the chunks.
 #include "paged.hpp"
 
+#include <cmath>
 #include <type_traits>
 
 namespace sz {
@@ -83,6 +84,10 @@ __device__ __forceinline__ void visible(int32_t p, int32_t window, int32_t &lo, 
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A factor of sums, 2^x.  Never 0, so that an infinite sum stays infinite: at
+// 2^-149 it is as much below the powers themselves, which end at 2^-126.
+__device__ __forceinline__ float scaling(float x) { return fmaxf(exp2_fast(x), 0x1p-149f); }
+
 // A row's running reference.  The powers are 2^(c x - base) with base = c m'
 // rounded: one fused multiply each.  delta = c m' - base is what the rounding
 // left; it keeps the reference exact where it changes.  Where |c m'| is over
@@ -97,7 +102,7 @@ struct Reference {
     {
         const float raised = fmaxf(top, x), base = raised * c;
         const float rest = fabsf(base) <= kFar ? __builtin_fmaf(raised, c, -base) : 0.f;
-        const float f = raised == kNone ? 1.f : exp2_fast(__builtin_fmaf(top - raised, c, rest - delta));
+        const float f = raised == kNone ? 1.f : scaling(__builtin_fmaf(top - raised, c, rest - delta));
         top = raised;
         delta = rest;
         return f;
@@ -112,7 +117,7 @@ struct Reference {
 // 2^(c (x - top)) for sums that were made with m' = x
 __device__ __forceinline__ float rebased(float x, float top, float c)
 {
-    return exp2_fast((x - (top == kNone ? 0.f : top)) * c);
+    return scaling((x - (top == kNone ? 0.f : top)) * c);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
@@ -487,14 +492,23 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
             p[r] = exp2_fast(__builtin_fmaf(st[r / 4][r % 4], a.c2, -base));
             l += p[r];
         }
-        const u32x4 pw = {bf16_pair(p[0], p[1]), bf16_pair(p[2], p[3]), bf16_pair(p[4], p[5]), bf16_pair(p[6], p[7])};
-        // and what BF16 left of them: the products are cheap beside the reads
-        // (0 to 1 % of the time), and the result is as exact as its own rounding
-        u32x4 rw;
+        // Their upper 16 bits, and the rest in a second product: products are
+        // cheap beside the reads (0 to 1 % of the time), and the result is as
+        // exact as its own rounding.  Where every row sees every key the rest
+        // is 2^-133 at least (BF16's smallest): 0 times an infinite value is a NaN.
+        u32x4 pw, rw;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            rw[e] = bf16_pair(p[2 * e] - __builtin_bit_cast(float, pw[e] << 16),
-                              p[2 * e + 1] - __builtin_bit_cast(float, pw[e] & 0xFFFF0000u));
+        for (int e = 0; e < 4; ++e) {
+            float rest[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float x = p[2 * e + h];
+                rest[h] = x - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xFFFF0000u);
+                if constexpr (!MASKED) rest[h] = fmaxf(rest[h], 0x1p-133f);
+            }
+            pw[e] = perm(__builtin_bit_cast(uint32_t, p[2 * e + 1]), __builtin_bit_cast(uint32_t, p[2 * e]), 0x07060302u);
+            rw[e] = bf16_pair(rest[0], rest[1]);
+        }
         const bf16x8 pb = __builtin_bit_cast(bf16x8, pw), pr = __builtin_bit_cast(bf16x8, rw);
 
         if (MASKED && wild) {
@@ -894,7 +908,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
         scale_late = __any(ref.below(top, a.c2));
         if (scale_late) {
             top = fmaxf(top, __shfl_xor(top, 32, 64));
-            late = fmaxf(ref.raise(top, a.c2), 1.17549435e-38f);               // what was infinite stays so
+            late = ref.raise(top, a.c2);
             far = __any(ref.is_far(a.c2));
             l *= late;
         }
@@ -1184,6 +1198,7 @@ struct AttnPlan {
     uint32_t rows_chunk, rows_splits, tile_chunk, tile_splits, slots;
 };
 
+constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;                // of a launch
 constexpr uint64_t kRowsGroups = 2048;        // workgroups that sz_attn_rows wants
 constexpr uint64_t kTileWaves = 2048;         // waves that sz_attn_tiles wants: two a SIMD
 constexpr uint32_t kMinChunk = 128;           // keys: a block for each wave, two tiles
@@ -1257,28 +1272,44 @@ uint64_t attn_ws_bytes(uint64_t splits, uint64_t rows, uint32_t head_dim)
     return 4 * kArrivals + (splits == 1 ? 0 : up256(splits * rows * head_dim * 4) + up256(splits * rows * 8));
 }
 
+// sz_attn_join's tokens per sequence (0: all tokens of the batch), and its workgroups.
+uint32_t join_per_seq(const PagedBatch &b, const AttnPlan &p, uint32_t group)
+{
+    return p.tile_splits > 1 ? 0 : std::min(b.max_new, kRowsMax / group);
+}
+uint64_t join_groups(const PagedBatch &b, const AttnPlan &p, uint32_t group, uint32_t q_heads)
+{
+    if ((p.rows_splits == 1 || p.fused) && p.tile_splits == 1) return 0;
+    const uint32_t per_seq = join_per_seq(b, p, group);
+    return (per_seq ? (uint64_t)b.seqs * per_seq : (uint64_t)b.tokens) * q_heads;
+}
+
+// Whether the launches stay within a launch's threads.
+bool launchable(const PagedCache &c, const PagedBatch &b, const AttnPlan &p, uint32_t group, uint32_t q_heads)
+{
+    return (!p.rows || (uint64_t)c.heads * b.seqs * p.rows_splits * kAttnThreads <= kMaxThreads) &&
+           (!p.tiles || (uint64_t)c.heads * p.slots * p.tile_splits * 64 * p.tile_waves <= kMaxThreads) &&
+           join_groups(b, p, group, q_heads) * kAttnThreads <= kMaxThreads;
+}
+
 template <int DT, int D>
 int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
 {
     if (p.rows) {
         const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits;
-        if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
         LaunchScope scope("sz_attn_rows", s);
         hipLaunchKernelGGL((sz_attn_rows<DT, D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
     }
     if (p.tiles) {
         const uint64_t groups = (uint64_t)a.c.heads * p.slots * p.tile_splits;
-        if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
         LaunchScope scope("sz_attn_tiles", s);
         if (p.tile_waves == 8)
             hipLaunchKernelGGL((sz_attn_tiles<DT, D, 8>), dim3((uint32_t)groups), dim3(512), 0, s, a, p.slots);
         else
             hipLaunchKernelGGL((sz_attn_tiles<DT, D, 4>), dim3((uint32_t)groups), dim3(256), 0, s, a, p.slots);
     }
-    if ((p.rows_splits > 1 && !p.fused) || p.tile_splits > 1) {
-        const uint32_t per_seq = p.tile_splits > 1 ? 0 : std::min(a.b.max_new, kRowsMax / a.group);
-        const uint64_t groups = (per_seq ? (uint64_t)a.b.seqs * per_seq : (uint64_t)a.b.tokens) * a.q_heads;
-        if (groups > 0x7FFFFFFFull) return SZ_E_ARG;
+    if (const uint64_t groups = join_groups(a.b, p, a.group, a.q_heads)) {
+        const uint32_t per_seq = join_per_seq(a.b, p, a.group);
         LaunchScope scope("sz_attn_join", s);
         hipLaunchKernelGGL((sz_attn_join<D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a, per_seq);
     }
@@ -1317,13 +1348,15 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     int rc = check_paged(cache, batch, d_status, a.c, a.b);
     if (rc != SZ_OK) return rc;
     if (q_heads == 0 || q_heads > 0xFFFFu || q_heads % a.c.heads) return SZ_E_ARG;
-    if (!(scale > 0.f) || !(scale <= 3.4e38f) || window > 0x7FFFFFFFu) return SZ_E_ARG;
+    a.c2 = scale * 1.44269504088896340736f;
+    if (!(scale > 0.f) || !std::isfinite(a.c2) || window > 0x7FFFFFFFu) return SZ_E_ARG;
     if ((rc = check_rows(d_q, q_token_stride, q_head_stride, a.b.tokens, q_heads)) != SZ_OK) return rc;
     if (a.b.tokens && !d_out) return SZ_E_ARG;
     if (!aligned16(d_out) || !aligned16(d_ws) || (reinterpret_cast<uintptr_t>(d_lse) & 3u)) return SZ_E_ALIGN;
     if (a.b.tokens == 0 || a.b.seqs == 0) return SZ_OK;
     a.group = q_heads / a.c.heads;
     const AttnPlan p = attn_plan(cache, a.b, a.group, window);
+    if (!launchable(a.c, a.b, p, a.group, q_heads)) return SZ_E_ARG;
     const uint32_t splits = std::max(p.rows_splits, p.tile_splits);
     const uint64_t rows = (uint64_t)a.b.tokens * q_heads;
     if (!d_ws) return SZ_E_ARG;
@@ -1338,7 +1371,6 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     a.part_ml = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(a.part) +
                                            up256(splits * rows * cache->head_dim * 4));
     a.scale = scale;
-    a.c2 = scale * 1.44269504088896340736f;
     a.q_heads = q_heads;
     a.window = (int32_t)window;
     a.rows_limit = p.rows ? kRowsMax : 0;

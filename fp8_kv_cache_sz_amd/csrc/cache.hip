@@ -141,8 +141,11 @@ __global__ __launch_bounds__(kMoveThreads) void sz_cache_move(PagedCache c, Page
         if (count < 64) {
             if (i < b.seqs) s = checked(b, my_start, my_next, my_len);
         } else {                                     // 64 sequences on, or more
-            while (i < b.seqs && b.starts[i + 1] <= (int32_t)t) ++i;
-            if (i < b.seqs) s = sequence(b, i);
+            for (uint32_t past = b.seqs; past - i > 1;) {
+                const uint32_t mid = i + (past - i) / 2;
+                (b.starts[mid] <= (int32_t)t ? i : past) = mid;
+            }
+            s = sequence(b, i);
         }
         const int32_t pos = s.len - s.n + ((int32_t)t - s.start);
         if ((int32_t)t >= s.start && (int32_t)t < s.start + s.n && pos >= 0) {
@@ -213,7 +216,7 @@ int move(const sz_cache *cache, const sz_batch *batch, void *d_k, uint64_t k_tok
     hipStream_t s = static_cast<hipStream_t>(stream);
     const uint64_t tiles = ((uint64_t)b.tokens + kMoveTokens - 1) / kMoveTokens;
     const uint64_t groups = (tiles * 2 * c.heads + 3) / 4;
-    if (groups > 0x3FFFFFFFull) return SZ_E_ARG;
+    if (groups * kMoveThreads > 0xFFFFFFFFull) return SZ_E_ARG;      // a launch's threads
     LaunchScope scope(WRITE ? "sz_cache_write" : "sz_cache_read", s);
     const dim3 grid((uint32_t)groups), block(kMoveThreads);
 #define SZ_MOVE(DT)                                                                                         \

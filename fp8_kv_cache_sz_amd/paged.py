@@ -140,6 +140,8 @@ def _rows(name, t, tokens, heads, cache):
     token, head, last = t.stride()
     if last != 1 and tokens:
         raise ValueError("%s needs contiguous rows (a last stride of 1)" % name)
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s requires a gradient, and the paged cache has none to give (torch.no_grad)" % name)
     return t.data_ptr(), token, head
 
 
@@ -160,6 +162,8 @@ def _run(name, call, cache, batch, args, stream, owned=()):
         if rc:
             _native.check(name, rc)
         return
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream is on %s, the cache on %s" % (stream.device, device))
     current = torch.cuda.current_stream(device)
     side = None if stream is None or stream == current else stream
     if side is not None and owned:
@@ -216,8 +220,11 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
         k, v = out
         args = (*_rows("out[0]", k, tokens, heads, cache), *_rows("out[1]", v, tokens, heads, cache))
         for token, head in (args[1:3], args[4:6]):
-            if (heads > 1 and head < dim) or (tokens > 1 and token < dim):
+            (near, count), (far, more) = sorted([(token, tokens), (head, heads)])
+            if (count > 1 and near < dim) or (more > 1 and far < (count - 1) * near + dim):
                 raise ValueError("out has rows that share memory")
+        if tokens and args[0] == args[3]:
+            raise ValueError("out's two tensors are one")
     _run("sz_cache_read", _native.lib.sz_cache_read, cache, batch, args, stream, owned)
     if check:
         _raise_status(cache, stream)

@@ -305,7 +305,9 @@ int sz_decode_noalloc(const void *d_in, uint64_t in_bytes, int dtype, void *d_ou
  * host's upper bounds of a sequence's new tokens and of kv_lens (max_kv <=
  * table_width * page_tokens): the host does not see the lengths, so launch
  * shapes follow from these, and tight bounds are faster ones.  Up to 2^30
- * tokens in a batch and in a sequence.
+ * tokens in a batch and in a sequence, and what one launch of 2^32 threads
+ * covers: 2^28 tokens times kv_heads moved, 2^23 sequences times kv_heads or
+ * 2^29 tokens times q_heads attended to are always inside; SZ_E_ARG beyond.
  *
  * The calls only enqueue, allocate nothing, issue no memset and can be
  * captured into a HIP graph, with lengths and tables that change between
@@ -394,7 +396,8 @@ int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uin
  * heads of a KV head) in a sequence its probabilities are rounded to BF16.  The result
  * does not depend on what runs beside it, bit for bit; it depends on max_new
  * and max_kv in its last bits, through the split of the keys.  scale must be
- * finite and above 0.  d_ws: ws_bytes >=
+ * above 0, scale * log2 e finite.  A probability below 2^-126 may count as 0,
+ * and 0 times an infinite value is a NaN.  d_ws: ws_bytes >=
  * sz_paged_attention_workspace_size(cache, batch, q_heads) (0 for heads that
  * do not divide; host fields of cache and batch only).  Its first
  * SZ_ATTENTION_COUNTERS bytes are counters of chunks done: the caller clears

@@ -52,6 +52,7 @@ SHAPES = {
     "one": ([1], [1]),
     "page_edge": ([16, 17, 15, 32], [1, 2, 15, 17]),
     "mixed": ([5, 0, 300, 64, 33], [5, 0, 1, 64, 20]),
+    "empties": ([3] + [0] * 130 + [5] + [0] * 70 + [2, 9], [3] + [0] * 130 + [4] + [0] * 70 + [2, 1]),
     "many": ([(7 * i) % 41 + 1 for i in range(150)], [1 + (i % 2 if (7 * i) % 41 else 0) for i in range(150)]),
 }
 
@@ -307,6 +308,38 @@ def test_attention_infinite_values_seen_by_some(rows, kinds):
         for d in (7, 9):
             a, b = got[t][:, d].float(), expect[:, d].float()
             assert bool(((a == b) | (a.isnan() & b.isnan())).all()), (t, d, a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("later", [0.0, 40.0], ids=["level", "outweighed"])
+def test_attention_infinite_values_seen_by_all(dtype, new, later):
+    """Infinities and NaN in V far before the new tokens: the sums of them,
+    also where a later key outweighs theirs by e^400."""
+    H, G, D, P, n = 1, 2, 128, 16, 700
+    table, kv, starts, T, pages = ref.layout([n], [new], P, seed=4)
+    data, scales = filled(dtype, pages, H, P, D, 3)
+    q = (torch.randn(1, 1, D, generator=gen(8)) + 0.01 * torch.randn(T, H * G, D, generator=gen(9))).to(torch.bfloat16)
+
+    def put(which, p, values):
+        pg, r = int(table[0, p // P]), p % P
+        for d, x in values:
+            data[pg, which, 0, r, d] = x
+        return pg, r
+    put(1, 100, [(7, math.inf), (9, -math.inf), (11, math.inf), (13, math.nan)])
+    put(1, 301, [(7, math.inf), (11, -math.inf), (15, -math.inf)])
+    pg, r = put(0, 600, list(enumerate((q[0, 0].double() * later).tolist())) if later else [])
+    if later and scales is not None:
+        scales[pg, 0, 0, r] = 127
+    out, lse = sz().paged_attention(q.cuda(), on_gpu(dtype, data, scales),
+                                    batch_of(table, kv, starts, T, max_new=new, max_kv=n), lse=True)
+    want, want_l, tol, tol_l = ref.attention(q, data, scales, table, kv, starts, P, D ** -0.5, 0)
+    assert bool(torch.isfinite(want_l).all()) and bool(want[..., 7].isinf().all())
+    assert not ref.close(lse, want_l, tol_l)
+    special = [7, 9, 11, 13, 15]
+    assert not ref.close(out[..., special], want[..., special], tol[..., special])
+    rest = [d for d in range(D) if d not in special]
+    assert not ref.close(out[..., rest], want[..., rest], tol[..., rest])
 
 
 def test_attention_scores_out_of_range():

@@ -277,3 +277,17 @@ def test_instrumentation_names_the_launches():
         m.profile_enable(False)
     assert {"sz_cache_check_clear", "sz_cache_check_walk", "sz_cache_write", "sz_cache_read", "sz_attn_rows",
             "sz_attn_tiles", "sz_attn_join"} == set(got)
+
+
+def test_streams_of_another_device_are_refused():
+    import types
+    cache = sz().paged_cache(2, 16, 1, 64)
+    index = torch.zeros(1, dtype=torch.int32, device="cuda")
+    batch = sz().PageBatch(index.view(1, 1), index + 1, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1)
+    x = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    other = types.SimpleNamespace(device=torch.device("cuda", cache.device.index + 1), cuda_stream=0)
+    for call in (lambda: sz().cache_write(cache, batch, x, x, stream=other),
+                 lambda: sz().cache_read(cache, batch, stream=other),
+                 lambda: sz().paged_attention(x, cache, batch, stream=other)):
+        with pytest.raises(ValueError, match="stream is on"):
+            call()

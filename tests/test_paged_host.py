@@ -199,3 +199,51 @@ def test_reference_rounding_by_hand():
     assert q[2, 0] == 2.0 ** -7 and q[3, 1] == 256.0 and bool(q[3, :3].isnan()[[0, 2]].all()) and q[4, 0] == 256.0
     q, s = ref.quantise(x[3:4], ref.E5M2)
     assert s.tolist() == [127 - 14] and q.float()[0, 0] == math.inf and q.float()[0, 1] == 32768.0
+
+
+def test_launches_that_no_grid_holds_are_refused():
+    nat = _native()
+    wide = cache_of(nat, kv_heads=1024)
+    many = batch_of(nat, tokens=1 << 30, max_new=1 << 30)
+    assert calls(nat, wide, many, q_heads=1024, token=1 << 17) == [ARG] * 3
+    # 2^24 workgroups of 256 threads are one launch too many, in either kernel
+    for kw in (dict(max_new=1), dict(max_new=100)):
+        b = batch_of(nat, seqs=1 << 24, table_width=16, max_kv=128, tokens=1 << 20, **kw)
+        assert calls(nat, cache_of(nat, kv_heads=1), b, q_heads=1)[2] == ARG
+
+
+def test_scale_is_finite_in_powers_of_two():
+    nat = _native()
+    c, b = cache_of(nat), batch_of(nat)
+    for scale in (3e38, 2.4e38, float("inf"), float("nan"), 0.0, -1.0):
+        assert calls(nat, c, b, scale=scale)[2] == ARG, scale
+    # the largest that is passes this check and fails the next
+    assert calls(nat, c, b, scale=2.3e38, ws_bytes=0)[2] == WORKSPACE
+
+
+def test_python_layer_refuses_shared_rows_and_gradients():
+    import fp8_kv_cache_sz_amd as sz
+    H, D, P = 2, 64, 16
+    cache = sz.paged_cache(4, P, H, D, device="cpu")
+    batch = sz.PageBatch(torch.zeros(2, 2, dtype=torch.int32), torch.tensor([3, 4], dtype=torch.int32),
+                         torch.tensor([0, 1, 2], dtype=torch.int32), 2)
+    x = torch.zeros(2, H, D, dtype=torch.bfloat16)
+    store = torch.zeros(8 * D, dtype=torch.bfloat16)
+    view = lambda token, head: store.as_strided((2, H, D), (token, head, 1))
+    # the fourth: the second token starts inside the first's last row
+    for bad in (view(D, D), view(0, D), view(D, 0), view(2 * D, D + 8), view(D, 2 * D - 8)):
+        with pytest.raises(ValueError, match="share memory"):
+            sz.cache_read(cache, batch, out=(bad, x), check=False)
+    with pytest.raises(ValueError, match="are one"):
+        sz.cache_read(cache, batch, out=(x, x), check=False)
+    for good in (view(2 * D, D), view(D, 2 * D)):          # these fail only at the device
+        with pytest.raises(ValueError, match="run on the GPU"):
+            sz.cache_read(cache, batch, out=(good, x), check=False)
+    g = x.clone().requires_grad_()
+    for call in (lambda: sz.cache_write(cache, batch, g, x, check=False),
+                 lambda: sz.cache_write(cache, batch, x, g, check=False),
+                 lambda: sz.paged_attention(g, cache, batch, ws=store, check=False)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="run on the GPU"):
+            call()
