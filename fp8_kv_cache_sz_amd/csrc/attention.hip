@@ -1199,9 +1199,22 @@ struct AttnPlan {
 };
 
 constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;                // of a launch
-constexpr uint64_t kRowsGroups = 2048;        // workgroups that sz_attn_rows wants
-constexpr uint64_t kTileWaves = 2048;         // waves that sz_attn_tiles wants: two a SIMD
-constexpr uint32_t kMinChunk = 128;           // keys: a block for each wave, two tiles
+// Workgroups that sz_attn_rows wants: enough to fill the card (768 run at a
+// time, and some chunks are behind their sequence's end), and up to kRowsEven
+// while their chunks have kRowsLong keys, to even out lengths.  Against 2,048
+// whatever the chunk's length: 128 sequences of up to 500 E4M3 tokens 24 us
+// (31), 4 of up to 8,192 21 us (26), 100 of 8,192 in BF16 555 us (574), 64 of
+// 8,192 in E4M3 202 us (196).  Against 768: 8 of up to 8,192 25 us (29);
+// against chunks of 2,048: 32 of up to 8,192 71 us (79).
+constexpr uint64_t kRowsFill = 1024;
+constexpr uint64_t kRowsEven = 3328;
+constexpr uint64_t kRowsLong = 1024;
+// Waves that sz_attn_tiles wants: two a SIMD.  With half, drafts of 16
+// sequences take 16.8 us instead of 15.7; with twice as many nothing changes.
+constexpr uint64_t kTileWaves = 2048;
+constexpr uint32_t kMinChunk = 128;           // keys: a block for each wave, two tiles (256: drafts 16.7 us, not 15.7)
+// Chunks of a long context have 1,024 keys at least: 64K tokens take 29.7 us,
+// with 512 keys 32.2.
 constexpr uint32_t kMaxLeast = 1024;
 constexpr uint64_t kArrivals = SZ_ATTENTION_COUNTERS / 4;      // counters at the workspace's start
 constexpr uint64_t kJoinChunks = 64;
@@ -1215,12 +1228,18 @@ static_assert(kFusedGroups <= kArrivals);
 
 uint64_t round_up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
-// Splits of `span` keys so that `groups` workgroups become `want`.  A chunk
-// is not made shorter than a 64th of the keys (joining grows with their
-// number) unless that is over kMaxLeast.
-void split_keys(uint64_t span, uint64_t groups, uint64_t want, uint32_t &chunk, uint32_t &splits)
+uint64_t rows_wanted(uint64_t span, uint64_t groups)
 {
-    const uint64_t n = std::max<uint64_t>(1, want / std::max<uint64_t>(1, groups));
+    return std::max(kRowsFill / groups, std::min(kRowsEven / groups, span / kRowsLong));
+}
+uint64_t tiles_wanted(uint64_t groups, uint32_t waves) { return kTileWaves / waves / groups; }
+
+// Splits of `span` keys into `want` chunks.  A chunk is not made shorter than
+// a 64th of the keys (joining grows with their number) unless that is over
+// kMaxLeast.
+void split_keys(uint64_t span, uint64_t want, uint32_t &chunk, uint32_t &splits)
+{
+    const uint64_t n = std::max<uint64_t>(1, want);
     const uint64_t least = std::min<uint64_t>(kMaxLeast, round_up((span + kJoinChunks - 1) / kJoinChunks, kMinChunk));
     const uint64_t c = round_up(std::max<uint64_t>({kMinChunk, least, (span + n - 1) / n}), kMinChunk);
     chunk = (uint32_t)c;
@@ -1228,10 +1247,9 @@ void split_keys(uint64_t span, uint64_t groups, uint64_t want, uint32_t &chunk, 
 }
 
 // No span up to this one gives more chunks than:
-uint64_t most_splits(uint64_t span, uint64_t groups, uint64_t want)
+uint64_t most_splits(uint64_t span, uint64_t want)
 {
-    const uint64_t n = std::max<uint64_t>(1, want / std::max<uint64_t>(1, groups));
-    return std::min<uint64_t>(n, (span + kMinChunk - 1) / kMinChunk);
+    return std::min<uint64_t>(std::max<uint64_t>(1, want), (span + kMinChunk - 1) / kMinChunk);
 }
 
 // Waves of sz_attn_tiles, 32 rows each.  Eight share one conversion of each
@@ -1259,9 +1277,9 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
     p.rows_splits = p.tile_splits = 1;
     p.rows_chunk = p.tile_chunk = kMinChunk;
     const uint64_t groups = (uint64_t)b.seqs * c->kv_heads;
-    if (p.rows) split_keys(span, groups, kRowsGroups, p.rows_chunk, p.rows_splits);
+    if (p.rows) split_keys(span, rows_wanted(span, groups), p.rows_chunk, p.rows_splits);
     if (p.tiles)
-        split_keys(span, (uint64_t)p.slots * c->kv_heads, kTileWaves / p.tile_waves, p.tile_chunk, p.tile_splits);
+        split_keys(span, tiles_wanted((uint64_t)p.slots * c->kv_heads, p.tile_waves), p.tile_chunk, p.tile_splits);
     p.fused = p.rows_splits > 1 && p.tile_splits == 1 && groups * p.rows_splits <= kFusedGroups;
     return p;
 }
@@ -1333,9 +1351,10 @@ extern "C" uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, con
     // the most chunks that any window gives
     const AttnPlan p = attn_plan(cache, b, q_heads / cache->kv_heads, 0);
     uint64_t splits = 1;
-    if (p.rows) splits = std::max(splits, most_splits(b.max_kv, (uint64_t)b.seqs * cache->kv_heads, kRowsGroups));
+    if (p.rows)
+        splits = std::max(splits, most_splits(b.max_kv, rows_wanted(b.max_kv, (uint64_t)b.seqs * cache->kv_heads)));
     if (p.tiles)
-        splits = std::max(splits, most_splits(b.max_kv, (uint64_t)p.slots * cache->kv_heads, kTileWaves / p.tile_waves));
+        splits = std::max(splits, most_splits(b.max_kv, tiles_wanted((uint64_t)p.slots * cache->kv_heads, p.tile_waves)));
     return attn_ws_bytes(splits, (uint64_t)b.tokens * q_heads, cache->head_dim);
 }
 
