@@ -1142,20 +1142,25 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
 }
 
 // ---------------------------------------------------------------------------
-// sz_attn_join: a workgroup joins the chunks of one (token, head) row that
-// hold visible keys.  8 (D = 64: 16) groups of lanes take every 8th (16th)
-// chunk each and meet in LDS, in order.  With per_seq > 0 only sequences of
-// sz_attn_rows were split: the grid is their tokens, at most per_seq each;
-// else it is all tokens.
+// sz_attn_join: a workgroup joins the chunks of some heads' rows of one token.
+// `parts` groups of D/4 lanes take a row, every parts-th of its chunks each,
+// four in flight, and meet in LDS, in order.  With per_seq > 0 only sequences
+// of sz_attn_rows were split: the grid is their tokens, at most per_seq each;
+// else it is all tokens.  Bound by reading the partials: 512 tokens of 32
+// heads of 128 in 4 chunks (34 MB) took 29 us with a workgroup to a row, and
+// take 9.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_t per_seq)
+constexpr uint32_t kJoinGroups = kAttnThreads / (D / 4);
+
+template <int D>
+__global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_t per_seq, uint32_t parts)
 {
-    constexpr uint32_t LANES = D / 4, GROUPS = kAttnThreads / LANES;
+    constexpr uint32_t LANES = D / 4, GROUPS = kJoinGroups<D>;
     __shared__ float4 lds_o[GROUPS][LANES];
     __shared__ float2 lds_ml[GROUPS];
-    const uint32_t head = blockIdx.x % a.q_heads;
-    uint32_t t = blockIdx.x / a.q_heads;
+    const uint32_t rows = GROUPS / parts, blocks = (a.q_heads + rows - 1) / rows;
+    uint32_t t = blockIdx.x / blocks;
     Sequence s;
     if (per_seq > 0) {
         s = sequence(a.b, t / per_seq);
@@ -1174,15 +1179,18 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_
     const int32_t p = s.len - s.n + ((int32_t)t - s.start);
     uint32_t s0, s1;
     chunk_range(s, p, a.window, chunk, s0, s1);
-    const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES, part = group % parts;
+    const uint32_t head = blockIdx.x % blocks * rows + group / parts;
     Joined x;
-    join_chunks<D>(a, (uint64_t)t * a.q_heads + head, s0, s1, group, GROUPS, lane, x);
-    lds_o[group][lane] = x.o;
-    if (lane == 0) lds_ml[group] = make_float2(x.m, x.l);
-    __syncthreads();
-    if (group != 0) return;
-#pragma unroll
-    for (uint32_t g = 1; g < GROUPS; ++g) x.add(lds_ml[g], lds_o[g][lane], a.c2);
+    if (head < a.q_heads) join_chunks<D>(a, (uint64_t)t * a.q_heads + head, s0, s1, part, parts, lane, x);
+    if (parts > 1) {
+        lds_o[group][lane] = x.o;
+        if (lane == 0) lds_ml[group] = make_float2(x.m, x.l);
+        __syncthreads();
+        if (part == 0)
+            for (uint32_t g = 1; g < parts; ++g) x.add(lds_ml[group + g], lds_o[group + g][lane], a.c2);
+    }
+    if (head >= a.q_heads || part != 0) return;
     const float w[4] = {x.o.x, x.o.y, x.o.z, x.o.w};
     store_row<D, 4>(a, true, 0, t, head, lane * 4, w, p < 0 ? 0.f : 1.f / x.l);
     if (lane == 0) store_stats(a, true, 0, t, head, p < 0, x.m, x.l);
@@ -1232,7 +1240,17 @@ uint64_t rows_wanted(uint64_t span, uint64_t groups)
 {
     return std::max(kRowsFill / groups, std::min(kRowsEven / groups, span / kRowsLong));
 }
-uint64_t tiles_wanted(uint64_t groups, uint32_t waves) { return kTileWaves / waves / groups; }
+// A chunk's partials cost their way out and back, rows D 8 bytes; its keys are
+// the time that the others do not take.  span / n + rows D n / kPartialKeys is
+// least at n = sqrt(kPartialKeys span / (rows D)).  512 tokens by themselves
+// then stay whole, 20 us (26 in four chunks), 700 take 24.5 (29.7); with half
+// of kPartialKeys 64 tokens in each of 8 sequences of up to 1,064 take 33.5 us
+// (31), with a quarter 64 tokens behind 16,384 take 55.6 (48.3).
+constexpr double kPartialKeys = 12500;
+uint64_t tiles_wanted(uint64_t span, uint64_t groups, uint32_t waves, uint64_t values)
+{
+    return std::min<uint64_t>(kTileWaves / waves / groups, (uint64_t)std::sqrt(kPartialKeys * (double)span / (double)values));
+}
 
 // Splits of `span` keys into `want` chunks.  A chunk is not made shorter than
 // a 64th of the keys (joining grows with their number) unless that is over
@@ -1277,9 +1295,11 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
     p.rows_splits = p.tile_splits = 1;
     p.rows_chunk = p.tile_chunk = kMinChunk;
     const uint64_t groups = (uint64_t)b.seqs * c->kv_heads;
+    const uint64_t values = (uint64_t)b.tokens * group * c->kv_heads * c->head_dim;
     if (p.rows) split_keys(span, rows_wanted(span, groups), p.rows_chunk, p.rows_splits);
     if (p.tiles)
-        split_keys(span, tiles_wanted((uint64_t)p.slots * c->kv_heads, p.tile_waves), p.tile_chunk, p.tile_splits);
+        split_keys(span, tiles_wanted(span, (uint64_t)p.slots * c->kv_heads, p.tile_waves, values), p.tile_chunk,
+                   p.tile_splits);
     p.fused = p.rows_splits > 1 && p.tile_splits == 1 && groups * p.rows_splits <= kFusedGroups;
     return p;
 }
@@ -1290,28 +1310,35 @@ uint64_t attn_ws_bytes(uint64_t splits, uint64_t rows, uint32_t head_dim)
     return 4 * kArrivals + (splits == 1 ? 0 : up256(splits * rows * head_dim * 4) + up256(splits * rows * 8));
 }
 
-// sz_attn_join's tokens per sequence (0: all tokens of the batch), and its workgroups.
-uint32_t join_per_seq(const PagedBatch &b, const AttnPlan &p, uint32_t group)
+// sz_attn_join's tokens per sequence (0: all tokens of the batch), groups of
+// lanes to a row (four chunks each, as far as a workgroup goes) and workgroups.
+struct JoinPlan {
+    uint32_t per_seq, parts;
+    uint64_t groups;
+};
+JoinPlan join_plan(const PagedBatch &b, const AttnPlan &p, uint32_t group, uint32_t q_heads, uint32_t head_dim)
 {
-    return p.tile_splits > 1 ? 0 : std::min(b.max_new, kRowsMax / group);
-}
-uint64_t join_groups(const PagedBatch &b, const AttnPlan &p, uint32_t group, uint32_t q_heads)
-{
-    if ((p.rows_splits == 1 || p.fused) && p.tile_splits == 1) return 0;
-    const uint32_t per_seq = join_per_seq(b, p, group);
-    return (per_seq ? (uint64_t)b.seqs * per_seq : (uint64_t)b.tokens) * q_heads;
+    JoinPlan j{};
+    const uint32_t rows_splits = p.fused ? 1 : p.rows_splits, splits = std::max(rows_splits, p.tile_splits);
+    if (splits == 1) return j;
+    const uint32_t most = kAttnThreads / (head_dim / 4);
+    j.per_seq = p.tile_splits > 1 ? 0 : std::min(b.max_new, kRowsMax / group);
+    for (j.parts = 1; j.parts < most && 4 * j.parts < splits;) j.parts *= 2;
+    const uint32_t rows = most / j.parts;
+    j.groups = (j.per_seq ? (uint64_t)b.seqs * j.per_seq : (uint64_t)b.tokens) * ((q_heads + rows - 1) / rows);
+    return j;
 }
 
 // Whether the launches stay within a launch's threads.
-bool launchable(const PagedCache &c, const PagedBatch &b, const AttnPlan &p, uint32_t group, uint32_t q_heads)
+bool launchable(const PagedCache &c, const PagedBatch &b, const AttnPlan &p, const JoinPlan &j)
 {
     return (!p.rows || (uint64_t)c.heads * b.seqs * p.rows_splits * kAttnThreads <= kMaxThreads) &&
            (!p.tiles || (uint64_t)c.heads * p.slots * p.tile_splits * 64 * p.tile_waves <= kMaxThreads) &&
-           join_groups(b, p, group, q_heads) * kAttnThreads <= kMaxThreads;
+           j.groups * kAttnThreads <= kMaxThreads;
 }
 
 template <int DT, int D>
-int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
+int launch_attention(const AttnArgs &a, const AttnPlan &p, const JoinPlan &j, hipStream_t s)
 {
     if (p.rows) {
         const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits;
@@ -1326,10 +1353,10 @@ int launch_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s)
         else
             hipLaunchKernelGGL((sz_attn_tiles<DT, D, 4>), dim3((uint32_t)groups), dim3(256), 0, s, a, p.slots);
     }
-    if (const uint64_t groups = join_groups(a.b, p, a.group, a.q_heads)) {
-        const uint32_t per_seq = join_per_seq(a.b, p, a.group);
+    if (j.groups) {
         LaunchScope scope("sz_attn_join", s);
-        hipLaunchKernelGGL((sz_attn_join<D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a, per_seq);
+        hipLaunchKernelGGL((sz_attn_join<D>), dim3((uint32_t)j.groups), dim3(kAttnThreads), 0, s, a, j.per_seq,
+                           j.parts);
     }
     return hipGetLastError() == hipSuccess ? SZ_OK : SZ_E_HIP;
 }
@@ -1354,7 +1381,8 @@ extern "C" uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, con
     if (p.rows)
         splits = std::max(splits, most_splits(b.max_kv, rows_wanted(b.max_kv, (uint64_t)b.seqs * cache->kv_heads)));
     if (p.tiles)
-        splits = std::max(splits, most_splits(b.max_kv, tiles_wanted((uint64_t)p.slots * cache->kv_heads, p.tile_waves)));
+        splits = std::max(splits, most_splits(b.max_kv, tiles_wanted(b.max_kv, (uint64_t)p.slots * cache->kv_heads, p.tile_waves,
+                                                                     (uint64_t)b.tokens * q_heads * cache->head_dim)));
     return attn_ws_bytes(splits, (uint64_t)b.tokens * q_heads, cache->head_dim);
 }
 
@@ -1375,7 +1403,8 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     if (a.b.tokens == 0 || a.b.seqs == 0) return SZ_OK;
     a.group = q_heads / a.c.heads;
     const AttnPlan p = attn_plan(cache, a.b, a.group, window);
-    if (!launchable(a.c, a.b, p, a.group, q_heads)) return SZ_E_ARG;
+    const JoinPlan j = join_plan(a.b, p, a.group, q_heads, cache->head_dim);
+    if (!launchable(a.c, a.b, p, j)) return SZ_E_ARG;
     const uint32_t splits = std::max(p.rows_splits, p.tile_splits);
     const uint64_t rows = (uint64_t)a.b.tokens * q_heads;
     if (!d_ws) return SZ_E_ARG;
@@ -1400,9 +1429,9 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool wide = cache->head_dim == 128;
     switch (cache->dtype) {
-    case SZ_BF16: return wide ? launch_attention<SZ_BF16, 128>(a, p, s) : launch_attention<SZ_BF16, 64>(a, p, s);
+    case SZ_BF16: return wide ? launch_attention<SZ_BF16, 128>(a, p, j, s) : launch_attention<SZ_BF16, 64>(a, p, j, s);
     case SZ_FP8_E5M2:
-        return wide ? launch_attention<SZ_FP8_E5M2, 128>(a, p, s) : launch_attention<SZ_FP8_E5M2, 64>(a, p, s);
-    default: return wide ? launch_attention<SZ_FP8_E4M3, 128>(a, p, s) : launch_attention<SZ_FP8_E4M3, 64>(a, p, s);
+        return wide ? launch_attention<SZ_FP8_E5M2, 128>(a, p, j, s) : launch_attention<SZ_FP8_E5M2, 64>(a, p, j, s);
+    default: return wide ? launch_attention<SZ_FP8_E4M3, 128>(a, p, j, s) : launch_attention<SZ_FP8_E4M3, 64>(a, p, j, s);
     }
 }

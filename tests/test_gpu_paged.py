@@ -204,6 +204,28 @@ def test_attention(case, tight):
     assert not ref.close(lse, want_l, tol_l)
 
 
+# Keys in 4 to 36 chunks that a launch of their own joins: a group of lanes to
+# a row and several, more rows to a workgroup than heads, heads left over, rows
+# of both kernels.
+JOINED = [
+    (BF16, [1500], [20], 3, 5, 64, 32, 0),
+    (E4M3, [420], [33], 1, 7, 128, 16, 0),
+    (E4M3, [420], [33], 1, 7, 128, 16, 150),
+    (E5M2, [1000, 200, 40, 9], [6, 1, 40, 1], 1, 9, 128, 16, 0),
+    (BF16, [700, 100], [40, 17], 2, 3, 128, 64, 0),
+    (BF16, [9000, 8000, 17], [2, 1, 2], 2, 7, 64, 64, 0),
+    (E5M2, [9000, 100, 4500], [1, 1, 1], 2, 11, 128, 256, 0),
+]
+
+
+@pytest.mark.parametrize("case", JOINED, ids=lambda c: "%s-%s-%s" % (ref.NAMES[c[0]], c[1], c[2]))
+def test_attention_joined(case):
+    print("joined", case, flush=True)
+    out, lse, want, want_l, tol, tol_l = run_attention(*case)
+    assert not ref.close(out, want, tol)
+    assert not ref.close(lse, want_l, tol_l)
+
+
 # Larger than a laid-out test needs, but the smallest that fills the tile
 # kernel's eight-wave form (FP8, 256 rows a workgroup over all of the card).
 def test_attention_many_rows_fp8():
