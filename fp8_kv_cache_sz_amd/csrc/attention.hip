@@ -20,8 +20,8 @@
 // result layout gives each lane one row's scores (maxima and sums stay in
 // the lane) and is, keys renumbered, the operand layout of O^T = V^T P^T: P
 // never leaves its registers.
-//   sz_attn_rows  sequences with at most 16 rows per KV head (single tokens,
-//                 drafts): bound by reading K and V.
+//   sz_attn_rows  sequences with at most 16 (or 32) rows per KV head (single
+//                 tokens, drafts): bound by reading K and V.
 //   sz_attn_tiles the others: 128 rows a workgroup, bound by the matrix and
 //                 vector units.
 // Where there are few rows the keys are split into chunks whose partial
@@ -44,7 +44,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define SZ_INLINE __attribute__((always_inline))
 
 constexpr uint32_t kAttnThreads = 256;
-constexpr uint32_t kRowsMax = 16;        // rows of sz_attn_rows
+constexpr uint32_t kRowsMax = 16;        // rows of sz_attn_rows, or twice as many: its products have 16
 constexpr uint32_t kTileKeys = 64;
 constexpr uint32_t kKeyAlign = 64;       // chunks start at multiples of this
 constexpr float kSlack = 8.0f;
@@ -250,11 +250,11 @@ __device__ __forceinline__ void join_chunks(const AttnArgs &a, uint64_t r, uint3
 }
 
 // ---------------------------------------------------------------------------
-// sz_attn_rows: at most 16 rows.  A workgroup takes one chunk of one KV
+// sz_attn_rows: at most 16 NB rows.  A workgroup takes one chunk of one KV
 // head's keys; its four waves take 32-key blocks in turn, each with its own
 // (m', l, o) and no barrier, and meet in LDS at the end.  K and V go straight
 // to registers in 16-byte loads, the next block's issued before the current
-// one is used.  Per 32 keys a wave runs 2 D/32 + D/16 16x16x32 products.
+// one is used.  Per 32 keys a wave runs NB (2 D/32 + 2 D/16) 16x16x32 products.
 //   K, 16 keys at a time: lane (key = lane % 16, g = lane / 16) holds d =
 //     32 s + 8 g + 0..7 of step s (FP8: a 16-byte load covers two steps, d =
 //     64 i + 16 g + 8 h + 0..7; q is loaded in the same order).
@@ -262,6 +262,15 @@ __device__ __forceinline__ void join_chunks(const AttnArgs &a, uint64_t r, uint3
 //   V: lane (c = lane % 16, g) loads D/16 values of rows 16 b + 4 g + 0..3 at
 //     d = c D/16; byte permutes turn its 8 rows x D/16 values into D/16
 //     operands of 8 keys each.
+// Bound by reading K and V.  Measured (MI355X, 8 KV heads of 128, four query
+// heads each, contexts of 8,192): 100 sequences in BF16 551 us, 6.1 TB/s; 64
+// in E4M3 196 us, 5.5 TB/s (with three waves a SIMD, half of BF16's bytes
+// in flight, and converting); 64 of up to 8,192 124 us, 4.9 TB/s, for the
+// chunks that end late.  One context of 64K (4 heads, BF16) 24 us and 4 to
+// join, 4.8 TB/s: 256 workgroups of 1,024 keys.  The order of the loads and
+// the waits that count them carry this: where a wait in the loop was for all
+// loads in flight, 32 rows took 89 us instead of 83, and one spilled register
+// in it costs 8 %.
 // ---------------------------------------------------------------------------
 template <int DT, int D>
 struct KeyBlock {
@@ -318,21 +327,23 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, uint32_t head, co
     }
 }
 
-template <int DT, int D>
-__global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
+template <int DT, int D, int NB>
+__global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void sz_attn_rows(AttnArgs a)
 {
+    constexpr uint32_t ROWS = 16 * NB;
     constexpr int VD = D / 16;                      // d values of a lane
     constexpr int WAVES = kAttnThreads / 64;
-    __shared__ float lds_o[WAVES][kRowsMax][D + 4];
-    __shared__ float2 lds_ml[WAVES][kRowsMax];
+    __shared__ float lds_o[WAVES][ROWS][D + 4];
+    __shared__ float2 lds_ml[WAVES][ROWS];
     __shared__ uint32_t lds_last;
 
     const uint32_t head = blockIdx.x % a.c.heads;
     const uint32_t seq = blockIdx.x / a.c.heads % a.b.seqs;
     const uint32_t split = blockIdx.x / a.c.heads / a.b.seqs;
     const Sequence s = sequence(a.b, seq);
-    const uint32_t rows = (uint32_t)s.n * a.group;
-    if (s.n == 0 || (uint32_t)s.n > kRowsMax || rows > kRowsMax) return;
+    const uint64_t all_rows = (uint64_t)s.n * a.group;
+    if (all_rows == 0 || all_rows > min(a.rows_limit, ROWS)) return;
+    const uint32_t rows = (uint32_t)all_rows;
     const uint32_t chunks = chunks_of(s, a.window, a.rows_chunk);
     const bool whole = chunks == 1;
     const int64_t begin64 = (int64_t)first_key(s, a.window) + (int64_t)split * a.rows_chunk;
@@ -342,33 +353,31 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
 
     const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / 64);
     const uint32_t n = lane % 16, g = lane / 16;
-    const uint32_t tok = n / a.group;
-    const int32_t pos = s.len - s.n + (int32_t)tok;
-    int32_t lo, hi;
-    visible(pos, a.window, lo, hi);
-    if (n >= rows) {                                // a row that is not there sees what the last one sees
-        visible(s.len - 1, a.window, lo, hi);
+    // Row 16 b + n; one that is not there computes what the last one does.
+    int32_t lo[NB], hi[NB];
+    bf16x8 q[NB][D / 32];                           // the products' second operand, in K's order of d
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint32_t r = min(16 * b + n, rows - 1), tok = r / a.group;
+        visible(s.len - s.n + (int32_t)tok, a.window, lo[b], hi[b]);
+        const uint16_t *p = a.q + (uint64_t)(s.start + tok) * a.q_token + (uint64_t)(head * a.group + r % a.group) * a.q_head;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            q[b][i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(
+                                                     p + (DT == SZ_BF16 ? 32 * i + 8 * g
+                                                                        : 64 * (i / 2) + 16 * g + 8 * (i % 2))));
     }
 
-    // q as the products' second operand, in K's order of d
-    bf16x8 q[D / 32];
+    f32x4 o[NB][VD];
+    Reference ref[NB];
+    float l[NB];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        u32x4 w = {0, 0, 0, 0};
-        if (n < rows) {
-            const uint32_t d = DT == SZ_BF16 ? 32 * i + 8 * g : 64 * (i / 2) + 16 * g + 8 * (i % 2);
-            w = *reinterpret_cast<const u32x4 *>(a.q + (uint64_t)(s.start + tok) * a.q_token +
-                                                 (uint64_t)(head * a.group + n % a.group) * a.q_head + d);
-        }
-        q[i] = __builtin_bit_cast(bf16x8, w);
+    for (int b = 0; b < NB; ++b) {
+        l[b] = 0.f;
+#pragma unroll
+        for (int j = 0; j < VD; ++j) o[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-
-    f32x4 o[VD];
-#pragma unroll
-    for (int j = 0; j < VD; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    Reference ref;
     bool far = false;
-    float l = 0.f;
 
     const int32_t all_lo = a.window > 0 ? max(0, s.len - a.window) : 0;      // every row sees [all_lo, all_hi]
     const int32_t all_hi = s.len - s.n;
@@ -391,12 +400,23 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
         page[1] = __builtin_amdgcn_readlane(ahead, at + 1);
         at += 2;
     };
+    // q is here before the first keys are asked for (or no keys are): waits in
+    // the loop count the loads behind the ones they wait for.
+    const auto have_q = [&]() SZ_INLINE {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) asm volatile("" : "+v"(q[b][i]));
+    };
     if (kb < end) {
         look_ahead(kb);
         next_pages();
+        have_q();
         load_keys<DT, D>(a, head, page, kb, cur);
         __builtin_amdgcn_sched_barrier(0);       // keys always before values: a wait for keys leaves values in flight
         load_values<DT, D>(a, head, page, kb, cur);
+    } else {
+        have_q();
     }
     // One block.  MASKED: some row does not see some key of it; a path of its
     // own, so that the common one has the registers to itself.  more: another
@@ -406,22 +426,26 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
         constexpr bool MASKED = decltype(masked_path)::value;
 
         // scores
-        f32x4 st[2];
+        f32x4 st[NB][2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            st[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) st[b][k] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 u32x4 w;
                 if constexpr (DT == SZ_BF16) {
-                    w = cur.k[b][i];
+                    w = cur.k[k][i];
                 } else {
-                    const uint32_t sc = ((cur.ks[b] >> (8 * (n % 4))) & 0xFFu) << 23;
-                    const uint32_t w0 = cur.k[b][i / 2][2 * (i % 2)], w1 = cur.k[b][i / 2][2 * (i % 2) + 1];
+                    const uint32_t sc = ((cur.ks[k] >> (8 * (n % 4))) & 0xFFu) << 23;
+                    const uint32_t w0 = cur.k[k][i / 2][2 * (i % 2)], w1 = cur.k[k][i / 2][2 * (i % 2) + 1];
                     w = u32x4{fp8_pair_to_bf16<DT, false>(w0, sc), fp8_pair_to_bf16<DT, true>(w0, sc),
                               fp8_pair_to_bf16<DT, false>(w1, sc), fp8_pair_to_bf16<DT, true>(w1, sc)};
                 }
-                st[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[i], st[b], 0, 0, 0);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    st[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[b][i], st[b][k],
+                                                                       0, 0, 0);
             }
         }
         if (more) {
@@ -430,22 +454,26 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
             if (!MASKED) load_keys<DT, D>(a, head, page, kb + STEP, cur);
         }
 
-        // V rows as BF16
+        // V rows as BF16.  FP8 values of the common path take their registers
+        // half at a time, the second half's after the first one's products.
+        constexpr bool HALVES = DT != SZ_BF16 && !MASKED;
         uint32_t v[8][VD / 2];
+        const auto convert = [&](int first, int last) SZ_INLINE {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            if constexpr (DT == SZ_BF16) {
+            for (int r = 0; r < 8; ++r) {
+                if constexpr (DT == SZ_BF16) {
 #pragma unroll
-                for (int e = 0; e < VD / 2; ++e) v[r][e] = cur.v[r][e];
-            } else {
-                const uint32_t sc = ((cur.vs[r / 4] >> (8 * (r % 4))) & 0xFFu) << 23;
+                    for (int e = first; e < last; ++e) v[r][e] = cur.v[r][e];
+                } else {
+                    const uint32_t sc = ((cur.vs[r / 4] >> (8 * (r % 4))) & 0xFFu) << 23;
 #pragma unroll
-                for (int e = 0; e < VD / 4; ++e) {
-                    v[r][2 * e] = fp8_pair_to_bf16<DT, false>(cur.v[r][e], sc);
-                    v[r][2 * e + 1] = fp8_pair_to_bf16<DT, true>(cur.v[r][e], sc);
+                    for (int e = first; e < last; ++e)
+                        v[r][e] = e % 2 ? fp8_pair_to_bf16<DT, true>(cur.v[r][e / 2], sc)
+                                        : fp8_pair_to_bf16<DT, false>(cur.v[r][e / 2], sc);
                 }
             }
-        }
+        };
+        convert(0, HALVES ? VD / 4 : VD / 2);
 
         // Hidden keys: their scores are -inf whatever K holds; V rows that no
         // row sees (behind the end, before the window) become zeros, since 0
@@ -458,7 +486,9 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 const int32_t key = kb + 16 * (r / 4) + 4 * (int32_t)g + r % 4;
-                if (key < lo || key > hi) st[r / 4][r % 4] = kNone;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    if (key < lo[b] || key > hi[b]) st[b][r / 4][r % 4] = kNone;
                 const bool dead = key < any_lo || key >= s.len;
 #pragma unroll
                 for (int e = 0; e < VD / 2; ++e) {
@@ -469,52 +499,65 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
             wild = __any((found & kNotFinite) != 0);
         }
 
-        // running maximum, raised only when some row needs it
-        float top = kNone;
+        // running maxima, raised only when some row needs it
 #pragma unroll
-        for (int r = 0; r < 8; ++r) top = fmaxf(top, st[r / 4][r % 4]);
-        if (__any(ref.below(top, a.c2))) {
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float f = ref.raise(top, a.c2);
-            far = __any(ref.is_far(a.c2));
-            l *= f;
+        for (int b = 0; b < NB; ++b) {
+            float top = kNone;
 #pragma unroll
-            for (int j = 0; j < VD; ++j) o[j] *= f;
-        }
-        if (far)
+            for (int r = 0; r < 8; ++r) top = fmaxf(top, st[b][r / 4][r % 4]);
+            if (__any(ref[b].below(top, a.c2))) {
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                const float f = ref[b].raise(top, a.c2);
+                far = __any(ref[0].is_far(a.c2) || ref[NB - 1].is_far(a.c2));
+                l[b] *= f;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) st[r / 4][r % 4] -= ref.origin();
-        const float base = ref.base(a.c2, far);
-        float p[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            p[r] = exp2_fast(__builtin_fmaf(st[r / 4][r % 4], a.c2, -base));
-            l += p[r];
-        }
-        // Their upper 16 bits, and the rest in a second product: products are
-        // cheap beside the reads (0 to 1 % of the time), and the result is as
-        // exact as its own rounding.  Where every row sees every key the rest
-        // is 2^-133 at least (BF16's smallest): 0 times an infinite value is a NaN.
-        u32x4 pw, rw;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float rest[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float x = p[2 * e + h];
-                rest[h] = x - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xFFFF0000u);
-                if constexpr (!MASKED) rest[h] = fmaxf(rest[h], 0x1p-133f);
+                for (int j = 0; j < VD; ++j) o[b][j] *= f;
             }
-            pw[e] = perm(__builtin_bit_cast(uint32_t, p[2 * e + 1]), __builtin_bit_cast(uint32_t, p[2 * e]), 0x07060302u);
-            rw[e] = bf16_pair(rest[0], rest[1]);
         }
-        const bf16x8 pb = __builtin_bit_cast(bf16x8, pw), pr = __builtin_bit_cast(bf16x8, rw);
+        bf16x8 pb[NB], pr[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (far)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) st[b][r / 4][r % 4] -= ref[b].origin();
+            const float base = ref[b].base(a.c2, far);
+            float p[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                p[r] = exp2_fast(__builtin_fmaf(st[b][r / 4][r % 4], a.c2, -base));
+                l[b] += p[r];
+            }
+            // Their upper 16 bits, and the rest in a second product: products
+            // are cheap beside the reads (0 to 1 % of the time), and the result
+            // is as exact as its own rounding.  Where every row sees every key
+            // the rest is 2^-133 at least (BF16's smallest): 0 times an
+            // infinite value is a NaN.
+            u32x4 pw, rw;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float rest[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float x = p[2 * e + h];
+                    rest[h] = x - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xFFFF0000u);
+                    if constexpr (!MASKED) rest[h] = fmaxf(rest[h], 0x1p-133f);
+                }
+                pw[e] = perm(__builtin_bit_cast(uint32_t, p[2 * e + 1]), __builtin_bit_cast(uint32_t, p[2 * e]),
+                             0x07060302u);
+                rw[e] = bf16_pair(rest[0], rest[1]);
+            }
+            pb[b] = __builtin_bit_cast(bf16x8, pw);
+            pr[b] = __builtin_bit_cast(bf16x8, rw);
+        }
 
         if (MASKED && wild) {
             const int32_t key = kb + 4 * (int32_t)g;
-            const u32x4 sw = {seen_pair(key, lo, hi), seen_pair(key + 2, lo, hi), seen_pair(key + 16, lo, hi),
-                              seen_pair(key + 18, lo, hi)};
+            u32x4 sw[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                sw[b] = u32x4{seen_pair(key, lo[b], hi[b]), seen_pair(key + 2, lo[b], hi[b]),
+                              seen_pair(key + 16, lo[b], hi[b]), seen_pair(key + 18, lo[b], hi[b])};
             uint32_t even = 0x05040100u;
             asm volatile("" : "+s"(even));       // these permutes are not shared with the ones below, which would
 #pragma unroll                                   // keep all of them in registers
@@ -522,10 +565,14 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
                 const uint32_t sel = even + (j % 2 ? 0x02020202u : 0u);
                 const u32x4 w = {kinds(perm(v[1][j / 2], v[0][j / 2], sel)), kinds(perm(v[3][j / 2], v[2][j / 2], sel)),
                                  kinds(perm(v[5][j / 2], v[4][j / 2], sel)), kinds(perm(v[7][j / 2], v[6][j / 2], sel))};
-                const f32x4 c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, sw), f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) o[j][r] += from_kinds(c[r]);
+                for (int b = 0; b < NB; ++b) {
+                    const f32x4 c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, sw[b]), f32x4{0.f, 0.f, 0.f, 0.f}, 0,
+                        0, 0);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[b][j][r] += from_kinds(c[r]);
+                }
             }
 #pragma unroll
             for (int r = 0; r < 8; ++r)
@@ -534,11 +581,23 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
         }
 #pragma unroll
         for (int j = 0; j < VD; ++j) {
+            if (HALVES && j == VD / 2) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+#pragma unroll
+                    for (int e = VD / 8; e < VD / 4; ++e) asm volatile("" : "+v"(cur.v[r][e]));
+                convert(VD / 4, VD / 2);
+            }
             const uint32_t sel = j % 2 ? 0x07060302u : 0x05040100u;
             const u32x4 w = {perm(v[1][j / 2], v[0][j / 2], sel), perm(v[3][j / 2], v[2][j / 2], sel),
                              perm(v[5][j / 2], v[4][j / 2], sel), perm(v[7][j / 2], v[6][j / 2], sel)};
-            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pb, o[j], 0, 0, 0);
-            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pr, o[j], 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                o[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pb[b], o[b][j], 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                o[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), pr[b], o[b][j], 0, 0, 0);
         }
         if (more) {
             if (MASKED) {
@@ -556,23 +615,24 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
     }
 
     // the waves' sums meet in LDS
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    const float plain = exp2_fast(-ref.delta);      // to sums with m' itself as the reference
-    l *= plain;
 #pragma unroll
-    for (int j = 0; j < VD; ++j) o[j] *= plain;
-    if (g == 0) lds_ml[wave][n] = make_float2(ref.top, l);
+    for (int b = 0; b < NB; ++b) {
+        l[b] += __shfl_xor(l[b], 16, 64);
+        l[b] += __shfl_xor(l[b], 32, 64);
+        const float plain = exp2_fast(-ref[b].delta);   // to sums with m' itself as the reference
+        if (g == 0) lds_ml[wave][16 * b + n] = make_float2(ref[b].top, l[b] * plain);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int j = 0; j < VD; j += 4)
-            *reinterpret_cast<float4 *>(&lds_o[wave][n][(4 * g + r) * VD + j]) =
-                make_float4(o[j][r], o[j + 1][r], o[j + 2][r], o[j + 3][r]);
+            for (int j = 0; j < VD; j += 4)
+                *reinterpret_cast<float4 *>(&lds_o[wave][16 * b + n][(4 * g + r) * VD + j]) =
+                    make_float4(o[b][j][r] * plain, o[b][j + 1][r] * plain, o[b][j + 2][r] * plain,
+                                o[b][j + 3][r] * plain);
+    }
     __syncthreads();
-    // 256 threads, each VD values of one row
-    const uint32_t row = threadIdx.x / 16, d = threadIdx.x % 16 * VD;
-    if (row < rows) {
+    // 256 threads, each VD values of one row of 16
+    const uint32_t d = threadIdx.x % 16 * VD;
+    for (uint32_t row = threadIdx.x / 16; row < rows; row += 16) {
         float top = kNone, sum = 0.f, acc[VD];
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) top = fmaxf(top, lds_ml[w][row].x);
@@ -586,9 +646,8 @@ __global__ __launch_bounds__(kAttnThreads, 3) void sz_attn_rows(AttnArgs a)
 #pragma unroll
             for (int j = 0; j < VD; ++j) acc[j] += lds_o[w][row][d + j] * f;
         }
-        const uint32_t rtok = row / a.group;
+        const uint32_t rtok = row / a.group, rhead = head * a.group + row % a.group;
         const bool empty = s.len - s.n + (int32_t)rtok < 0;
-        const uint32_t rhead = head * a.group + row % a.group;
         store_row<D, VD>(a, whole, split, s.start + rtok, rhead, d, acc, empty ? 0.f : 1.f / sum);
         if (d == 0) store_stats(a, whole, split, s.start + rtok, rhead, empty, top, sum);
     }
@@ -1203,6 +1262,7 @@ struct AttnPlan {
     bool rows, tiles;                 // which kernels the batch can need
     bool fused;                       // sz_attn_rows joins its chunks itself
     uint32_t tile_waves;
+    uint32_t rows_limit;              // of sz_attn_rows
     uint32_t rows_chunk, rows_splits, tile_chunk, tile_splits, slots;
 };
 
@@ -1280,16 +1340,28 @@ uint32_t tile_waves(uint32_t dtype, const PagedBatch &b, uint32_t kv_heads, uint
     return dtype != SZ_BF16 && rows >= 256ull * b.seqs && rows * kv_heads >= 256ull * kTileWaves / 8 ? 8 : 4;
 }
 
+// Whether sz_attn_rows takes 17 to 32 rows, as two of its products.  FP8: 64
+// sequences of up to 4,000 tokens, 32 rows, 83 us where sz_attn_tiles takes
+// 136, 15 of up to 15,246, 26 rows, 49 (82); BF16 with D = 64: 72 (84).  With
+// BF16 and D = 128 its registers leave two waves a SIMD, and it is no faster:
+// 15 of up to 15,241, 32 rows, 76 us (77), 20 rows over 1,005 tokens 17 (16).
+// 33 to 64 rows in two such workgroups gained little or nothing (FP8 58 for
+// 65 us and 38 for 38, BF16 90 for 60).
+constexpr bool row_pairs(uint32_t dtype, uint32_t head_dim) { return dtype != SZ_BF16 || head_dim == 64; }
+
 AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint32_t window)
 {
     AttnPlan p{};
     // chunks start at a multiple of kKeyAlign: up to kKeyAlign - 1 keys more than the visible ones
     uint64_t span = b.max_kv;
     if (window) span = std::min<uint64_t>(span, (uint64_t)window + b.max_new + kKeyAlign - 1);
-    p.tiles = (uint64_t)b.max_new * group > kRowsMax;
+    p.rows_limit = (uint64_t)b.max_new * group <= kRowsMax || !row_pairs(c->dtype, c->head_dim) ? kRowsMax : 2 * kRowsMax;
+    p.tiles = (uint64_t)b.max_new * group > p.rows_limit;
+    if (p.tiles) p.rows_limit = kRowsMax;
     // Sequences of few rows beside others: none if there is one sequence (its
     // rows all go the same way) or every sequence has max_new tokens.
     p.rows = !p.tiles || (b.seqs > 1 && group <= kRowsMax && b.tokens != (uint64_t)b.seqs * b.max_new);
+    if (!p.rows) p.rows_limit = 0;
     p.tile_waves = tile_waves(c->dtype, b, c->kv_heads, group);
     p.slots = (uint32_t)std::min<uint64_t>((uint64_t)b.tokens * group / (32 * p.tile_waves) + b.seqs, 0x7FFFFFFFu);
     p.rows_splits = p.tile_splits = 1;
@@ -1297,9 +1369,15 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
     const uint64_t groups = (uint64_t)b.seqs * c->kv_heads;
     const uint64_t values = (uint64_t)b.tokens * group * c->kv_heads * c->head_dim;
     if (p.rows) split_keys(span, rows_wanted(span, groups), p.rows_chunk, p.rows_splits);
-    if (p.tiles)
-        split_keys(span, tiles_wanted(span, (uint64_t)p.slots * c->kv_heads, p.tile_waves, values), p.tile_chunk,
-                   p.tile_splits);
+    if (p.tiles) {
+        // With a window a tile of rows sees less than its sequence's tokens
+        // together: no chunks where that would not be split (a window of 14
+        // over 488 new tokens 24 us in chunks, 14 without).
+        const uint64_t tiles = (uint64_t)p.slots * c->kv_heads, tokens = 32 * p.tile_waves / group + 2;
+        const uint64_t seen = window ? std::min(span, window + tokens + kTileKeys) : span;
+        const bool split = tiles_wanted(seen, tiles, p.tile_waves, values) > 1;
+        split_keys(span, split ? tiles_wanted(span, tiles, p.tile_waves, values) : 1, p.tile_chunk, p.tile_splits);
+    }
     p.fused = p.rows_splits > 1 && p.tile_splits == 1 && groups * p.rows_splits <= kFusedGroups;
     return p;
 }
@@ -1322,7 +1400,7 @@ JoinPlan join_plan(const PagedBatch &b, const AttnPlan &p, uint32_t group, uint3
     const uint32_t rows_splits = p.fused ? 1 : p.rows_splits, splits = std::max(rows_splits, p.tile_splits);
     if (splits == 1) return j;
     const uint32_t most = kAttnThreads / (head_dim / 4);
-    j.per_seq = p.tile_splits > 1 ? 0 : std::min(b.max_new, kRowsMax / group);
+    j.per_seq = p.tile_splits > 1 ? 0 : std::min(b.max_new, p.rows_limit / group);
     for (j.parts = 1; j.parts < most && 4 * j.parts < splits;) j.parts *= 2;
     const uint32_t rows = most / j.parts;
     j.groups = (j.per_seq ? (uint64_t)b.seqs * j.per_seq : (uint64_t)b.tokens) * ((q_heads + rows - 1) / rows);
@@ -1343,15 +1421,18 @@ int launch_attention(const AttnArgs &a, const AttnPlan &p, const JoinPlan &j, hi
     if (p.rows) {
         const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits;
         LaunchScope scope("sz_attn_rows", s);
-        hipLaunchKernelGGL((sz_attn_rows<DT, D>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+        if (p.rows_limit <= kRowsMax)
+            hipLaunchKernelGGL((sz_attn_rows<DT, D, 1>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+        else if constexpr (row_pairs(DT, D))
+            hipLaunchKernelGGL((sz_attn_rows<DT, D, 2>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
     }
     if (p.tiles) {
         const uint64_t groups = (uint64_t)a.c.heads * p.slots * p.tile_splits;
         LaunchScope scope("sz_attn_tiles", s);
-        if (p.tile_waves == 8)
-            hipLaunchKernelGGL((sz_attn_tiles<DT, D, 8>), dim3((uint32_t)groups), dim3(512), 0, s, a, p.slots);
-        else
+        if (p.tile_waves == 4)
             hipLaunchKernelGGL((sz_attn_tiles<DT, D, 4>), dim3((uint32_t)groups), dim3(256), 0, s, a, p.slots);
+        else if constexpr (DT != SZ_BF16)
+            hipLaunchKernelGGL((sz_attn_tiles<DT, D, 8>), dim3((uint32_t)groups), dim3(512), 0, s, a, p.slots);
     }
     if (j.groups) {
         LaunchScope scope("sz_attn_join", s);
@@ -1421,7 +1502,7 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     a.scale = scale;
     a.q_heads = q_heads;
     a.window = (int32_t)window;
-    a.rows_limit = p.rows ? kRowsMax : 0;
+    a.rows_limit = p.rows_limit;
     a.rows_chunk = p.rows_chunk;
     a.rows_splits = p.rows_splits;
     a.tile_chunk = p.tile_chunk;

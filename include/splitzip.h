@@ -393,9 +393,10 @@ int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uin
  * or NULL.  A token that sees no key gets 0 and -inf.  Keys that a token does
  * not see do not reach its result, NaN and infinities included.  Sums,
  * scores and lse are 32-bit; with more than 16 rows (new tokens times query
- * heads of a KV head) in a sequence its probabilities are rounded to BF16.  The result
- * does not depend on what runs beside it, bit for bit; it depends on max_new
- * and max_kv in its last bits, through the split of the keys.  scale must be
+ * heads of a KV head) in a sequence its probabilities may be rounded to BF16.
+ * The result does not depend on what runs beside it, bit for bit; it depends
+ * on max_new and max_kv in its last bits, through the split of the keys and
+ * the choice of the kernel.  scale must be
  * above 0, scale * log2 e finite.  A probability below 2^-126 may count as 0,
  * and 0 times an infinite value is a NaN.  d_ws: ws_bytes >=
  * sz_paged_attention_workspace_size(cache, batch, q_heads) (0 for heads that

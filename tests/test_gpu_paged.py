@@ -158,6 +158,13 @@ ATTENTION = [
     (E4M3, [1500], [129], 1, 7, 128, 16, 100),
     (BF16, [400, 129], [300, 129], 2, 2, 64, 16, 33),
     (E5M2, [260], [260], 1, 1, 64, 256, 1),
+    # 17 to 32 rows: two blocks of rows, or tiles
+    (BF16, [300, 90, 40], [5, 4, 6], 2, 5, 64, 16, 0),
+    (E5M2, [300, 90, 17], [17, 1, 17], 2, 1, 128, 32, 0),
+    (E4M3, [900, 33, 200], [4, 2, 3], 1, 8, 128, 16, 40),
+    (E4M3, [1300, 31], [8, 1], 2, 4, 64, 64, 0),
+    (E5M2, [130, 20], [1, 1], 1, 32, 64, 16, 0),
+    (BF16, [10, 700], [20, 25], 1, 1, 64, 16, 7),
     # both kinds of sequence in one call, and sequences without new tokens or without any
     (BF16, [900, 300, 0, 64, 1], [1, 100, 0, 0, 1], 2, 4, 128, 16, 0),
     (E4M3, [20, 1000, 500], [20, 1, 2], 2, 8, 128, 32, 50),
@@ -275,6 +282,7 @@ def spoil_hidden(value):
 @pytest.mark.parametrize("case", [
     (BF16, [200, 40], [5, 3], 2, 3, 128, 16, 0),
     (E5M2, [200, 40], [5, 3], 2, 3, 64, 32, 0),
+    (E5M2, [200, 40], [9, 6], 2, 3, 128, 32, 0),
     (BF16, [200, 70], [90, 70], 2, 2, 128, 16, 0),
     (E5M2, [200, 70], [90, 70], 1, 2, 128, 64, 0),
     (BF16, [200, 70], [90, 70], 1, 2, 64, 16, 37),
@@ -333,7 +341,7 @@ def test_attention_infinite_values_seen_by_some(rows, kinds):
 
 
 @pytest.mark.parametrize("dtype", [BF16, E5M2])
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 14, 40])
 @pytest.mark.parametrize("later", [0.0, 40.0], ids=["level", "outweighed"])
 def test_attention_infinite_values_seen_by_all(dtype, new, later):
     """Infinities and NaN in V far before the new tokens: the sums of them,
