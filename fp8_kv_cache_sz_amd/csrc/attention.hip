@@ -161,6 +161,31 @@ __device__ __forceinline__ uint32_t seen_pair(int32_t key, int32_t lo, int32_t h
     return (key >= lo && key <= hi ? 0x3F80u : 0u) | (key + 1 >= lo && key + 1 <= hi ? 0x3F800000u : 0u);
 }
 
+// Partials that another workgroup of the same launch joins pass through the
+// memory that all XCDs see: the relaxed atomic accesses of the device's scope
+// write through an XCD's L2 and do not read what it holds, so a workgroup
+// that has waited for its stores need not write that L2 back (a release
+// fence) before it counts itself, nor the one that joins empty it.
+__device__ __forceinline__ void publish(float *p, float x, float y)
+{
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), __builtin_bit_cast(uint64_t, make_float2(x, y)),
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <bool SHARED>
+__device__ __forceinline__ float2 partial2(const float *p)
+{
+    if constexpr (!SHARED) return *reinterpret_cast<const float2 *>(p);
+    return __builtin_bit_cast(float2, __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED,
+                                                        __HIP_MEMORY_SCOPE_AGENT));
+}
+template <bool SHARED>
+__device__ __forceinline__ float4 partial4(const float *p)
+{
+    if constexpr (!SHARED) return *reinterpret_cast<const float4 *>(p);
+    const float2 x = partial2<true>(p), y = partial2<true>(p + 2);
+    return make_float4(x.x, x.y, y.x, y.y);
+}
+
 // Writes one row's EL consecutive values at d: the result, or a chunk's partial.
 template <int D, int EL>
 __device__ __forceinline__ void store_row(const AttnArgs &a, bool whole, uint32_t split, uint32_t token,
@@ -179,8 +204,14 @@ __device__ __forceinline__ void store_row(const AttnArgs &a, bool whole, uint32_
     } else {
         float *p = a.part + ((uint64_t)split * a.b.tokens * a.q_heads + r) * D + d;
 #pragma unroll
-        for (int e = 0; e < EL; e += 4)
-            *reinterpret_cast<float4 *>(p + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        for (int e = 0; e < EL; e += 4) {
+            if (a.arrived) {
+                publish(p + e, o[e], o[e + 1]);
+                publish(p + e + 2, o[e + 2], o[e + 3]);
+            } else {
+                *reinterpret_cast<float4 *>(p + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+        }
     }
 }
 
@@ -190,7 +221,7 @@ __device__ __forceinline__ void store_stats(const AttnArgs &a, bool whole, uint3
 {
     const uint64_t r = (uint64_t)token * a.q_heads + head;
     if (!whole)
-        a.part_ml[(uint64_t)split * a.b.tokens * a.q_heads + r] = make_float2(m, l);
+        publish(reinterpret_cast<float *>(a.part_ml + (uint64_t)split * a.b.tokens * a.q_heads + r), m, l);
     else if (a.lse)
         a.lse[r] = empty ? kNone : __builtin_fmaf(__log2f(l), 0.69314718055994530942f, m * a.scale);
 }
@@ -227,21 +258,22 @@ __device__ __forceinline__ void chunk_range(const Sequence &s, int32_t p, int32_
     s1 = hi < 0 ? 0 : (uint32_t)(hi - first) / chunk + 1;
 }
 
-// Every parts-th chunk of row r from s0 + part on, four in flight.
-template <int D>
+// Every parts-th chunk of row r from s0 + part on, four in flight (eight of a
+// launch's own, which come from further away).
+template <int D, bool SHARED>
 __device__ __forceinline__ void join_chunks(const AttnArgs &a, uint64_t r, uint32_t s0, uint32_t s1, uint32_t part,
                                             uint32_t parts, uint32_t lane, Joined &x)
 {
     const uint64_t stride = (uint64_t)a.b.tokens * a.q_heads;
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = SHARED ? 8 : 4;
     for (uint32_t k = s0 + part; k < s1; k += AHEAD * parts) {
         float2 ml[AHEAD];
         float4 v[AHEAD];
 #pragma unroll
         for (int e = 0; e < AHEAD; ++e) {
             const uint64_t at = min(k + e * parts, s1 - 1) * stride + r;
-            ml[e] = a.part_ml[at];
-            v[e] = *reinterpret_cast<const float4 *>(a.part + at * D + lane * 4);
+            ml[e] = partial2<SHARED>(reinterpret_cast<const float *>(a.part_ml + at));
+            v[e] = partial4<SHARED>(a.part + at * D + lane * 4);
         }
 #pragma unroll
         for (int e = 0; e < AHEAD; ++e)
@@ -654,19 +686,15 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     if (whole || a.arrived == nullptr) return;
 
     // The last chunk's workgroup to get here joins them.  Each has its
-    // partials written back (the wait, the barrier and the release) before it
-    // counts itself; the last one's count wraps to 0 for the next call, and
-    // it reads past its caches (the acquire).  The order of the sums is that
-    // of the chunks, whichever comes last.
+    // partials where all see them (publish, the wait and the barrier) before
+    // it counts itself, and the last one's count wraps to 0 for the next call.
+    // The order of the sums is that of the chunks, whichever comes last.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (threadIdx.x == 0) {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    if (threadIdx.x == 0)
         lds_last = atomicInc(a.arrived + (uint64_t)seq * a.c.heads + head, chunks - 1) == chunks - 1;
-    }
     __syncthreads();
     if (!lds_last) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     constexpr uint32_t LANES = D / 4, GROUPS = kAttnThreads / LANES;
     float4(*meet_o)[LANES] = reinterpret_cast<float4(*)[LANES]>(&lds_o[0][0][0]);
     float2 *meet_ml = &lds_ml[0][0];
@@ -681,7 +709,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
         if (r < rows) {
             uint32_t s0, s1;
             chunk_range(s, jpos, a.window, a.rows_chunk, s0, s1);
-            join_chunks<D>(a, (uint64_t)(s.start + jtok) * a.q_heads + jhead, s0, s1, part, parts, jlane, x);
+            join_chunks<D, true>(a, (uint64_t)(s.start + jtok) * a.q_heads + jhead, s0, s1, part, parts, jlane, x);
         }
         __syncthreads();
         meet_o[lanes_group][jlane] = x.o;
@@ -1241,7 +1269,7 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_
     const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES, part = group % parts;
     const uint32_t head = blockIdx.x % blocks * rows + group / parts;
     Joined x;
-    if (head < a.q_heads) join_chunks<D>(a, (uint64_t)t * a.q_heads + head, s0, s1, part, parts, lane, x);
+    if (head < a.q_heads) join_chunks<D, false>(a, (uint64_t)t * a.q_heads + head, s0, s1, part, parts, lane, x);
     if (parts > 1) {
         lds_o[group][lane] = x.o;
         if (lane == 0) lds_ml[group] = make_float2(x.m, x.l);
@@ -1286,12 +1314,14 @@ constexpr uint32_t kMinChunk = 128;           // keys: a block for each wave, tw
 constexpr uint32_t kMaxLeast = 1024;
 constexpr uint64_t kArrivals = SZ_ATTENTION_COUNTERS / 4;      // counters at the workspace's start
 constexpr uint64_t kJoinChunks = 64;
-// Up to so many workgroups join their chunks themselves.  It saves a launch
-// (one sequence of 1,001 tokens: 9.7 us where two launches take 12.8), but
-// each workgroup's release writes back its XCD's L2: with 256 workgroups a 64K
-// context took 43 us where sz_attn_join makes it 29, with 1,200 a step of 64
-// sequences 188 where it is 127.
-constexpr uint64_t kFusedGroups = 128;
+// Up to so many chunks of a sequence's head, and workgroups in all, are joined
+// by the workgroup that ends last, which saves a launch: 4 sequences of up to
+// 2,001 tokens 12 us (15), 47 of up to 217 12.5 (14), 1 of 4,001 13 (15).  With
+// more workgroups their writes past the L2 cost more than the launch (64 of up
+// to 8,192 tokens, six chunks each: 127 us for 125), with more chunks the one
+// workgroup reads them for longer (64K tokens, 64 chunks: 36 us for 30).
+constexpr uint32_t kFusedSplits = 32;
+constexpr uint64_t kFusedGroups = 1024;
 static_assert(kFusedGroups <= kArrivals);
 
 uint64_t round_up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
@@ -1378,7 +1408,8 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
         const bool split = tiles_wanted(seen, tiles, p.tile_waves, values) > 1;
         split_keys(span, split ? tiles_wanted(span, tiles, p.tile_waves, values) : 1, p.tile_chunk, p.tile_splits);
     }
-    p.fused = p.rows_splits > 1 && p.tile_splits == 1 && groups * p.rows_splits <= kFusedGroups;
+    p.fused = p.rows_splits > 1 && p.rows_splits <= kFusedSplits && p.tile_splits == 1 &&
+              groups * p.rows_splits <= kFusedGroups;
     return p;
 }
 
