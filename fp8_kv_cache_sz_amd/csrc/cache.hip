@@ -95,10 +95,11 @@ __device__ __forceinline__ void put_chunk(const PagedCache &c, uint64_t at, uint
 // neighbours in the tensors.
 // The BF16 side streams past the caches (non-temporal); the cache's side does
 // not, since attention reads it next.  Measured (MI355X): 65,536 tokens of 4
-// heads of 128, E5M2 -> BF16, 32 us, 6.2 TB/s (42 us with plain stores);
-// 74,251 tokens of 8 heads, E4M3 -> BF16, 83 us, 5.5 TB/s (99 us with four
-// pairs to a wave: too few waves to even out); 32,254 tokens of 8 heads, BF16
-// -> E4M3, 41 us, 4.9 TB/s (43 us with plain loads).
+// heads of 128, E5M2 -> BF16, 31 us, 6.5 TB/s (42 us with plain stores);
+// 74,251 tokens of 8 heads, E4M3 -> BF16, 85 us, 5.4 TB/s; 32,254 tokens of 8
+// heads, BF16 -> E4M3, 40 us, 5.0 TB/s (44 us with plain loads).  Of the last
+// two 7 and 2 us are the lookups.  8 tokens to a wave take 104 and 45 us, 32
+// 90 and 45, four pairs to a wave 99 (too few waves to even out).
 template <int DT, int D, bool WRITE>
 __global__ __launch_bounds__(kMoveThreads) void sz_cache_move(PagedCache c, PagedBatch b, Rows x)
 {
