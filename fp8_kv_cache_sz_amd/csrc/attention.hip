@@ -1515,7 +1515,6 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     a.c2 = scale * 1.44269504088896340736f;
     if (!(scale > 0.f) || !std::isfinite(a.c2) || window > 0x7FFFFFFFu) return SZ_E_ARG;
     if ((rc = check_rows(d_q, q_token_stride, q_head_stride, a.b.tokens, q_heads)) != SZ_OK) return rc;
-    if (a.b.tokens && !d_out) return SZ_E_ARG;
     if (!aligned16(d_out) || !aligned16(d_ws) || (reinterpret_cast<uintptr_t>(d_lse) & 3u)) return SZ_E_ALIGN;
     if (a.b.tokens == 0 || a.b.seqs == 0) return SZ_OK;
     a.group = q_heads / a.c.heads;
@@ -1526,6 +1525,7 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     const uint64_t rows = (uint64_t)a.b.tokens * q_heads;
     if (!d_ws) return SZ_E_ARG;
     if (ws_bytes < attn_ws_bytes(splits, rows, cache->head_dim)) return SZ_E_WORKSPACE;
+    if (!d_out) return SZ_E_ARG;
     a.q = static_cast<const uint16_t *>(d_q);
     a.q_token = q_token_stride;
     a.q_head = q_head_stride;

@@ -372,6 +372,28 @@ def test_attention_infinite_values_seen_by_all(dtype, new, later):
     assert not ref.close(out[..., rest], want[..., rest], tol[..., rest])
 
 
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (E4M3, 128)])
+@pytest.mark.parametrize("near", [0, 16])
+def test_attention_far_and_near_rows(dtype, D, near):
+    """32 rows, one half with scores of +-2^25 and the other with ordinary
+    ones: each half as it would be by itself."""
+    H, G, P, n, T = 1, 4, 16, 500, 8
+    table, kv, starts, T, pages = ref.layout([n], [T], P, seed=6)
+    data, scales = filled(dtype, pages, H, P, D, 13)
+    q = torch.randn(T, G, D, generator=gen(3))
+    rows = torch.arange(T * G).view(T, G)
+    at = (rows >= near) & (rows < near + 16)                   # the ordinary ones
+    q = torch.where(at.unsqueeze(-1), q, q * 2.0 ** 25).to(torch.bfloat16)
+    out, lse = sz().paged_attention(q.cuda(), on_gpu(dtype, data, scales),
+                                    batch_of(table, kv, starts, T, max_new=T, max_kv=n), lse=True)
+    want, want_l, tol, tol_l = ref.attention(q, data, scales, table, kv, starts, P, D ** -0.5, 0)
+    assert not ref.close(out[at.cuda()], want[at], tol[at])
+    assert not ref.close(lse[at.cuda()], want_l[at], tol_l[at])
+    # the leading score is far ahead of the next: its V row, rounded once
+    assert not ref.close(out[~at.cuda()], want[~at], want[~at].abs() * 2.0 ** -8)
+    assert not ref.close(lse[~at.cuda()], want_l[~at], want_l[~at].abs() * 2.0 ** -20)
+
+
 def test_attention_scores_out_of_range():
     """Scores of +-2^40 and beyond: the largest alone counts, nothing overflows."""
     H, D, P, n = 1, 64, 16, 90

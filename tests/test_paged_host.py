@@ -247,3 +247,23 @@ def test_python_layer_refuses_shared_rows_and_gradients():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="run on the GPU"):
             call()
+
+
+def test_attention_workspace_covers_every_window_of_many_shapes():
+    """As above over random shapes: the null output is the last check, so a
+    call that reaches it has passed the workspace's."""
+    import random
+    nat = _native()
+    rng = random.Random(5)
+    for _ in range(400):
+        heads, group = rng.choice([1, 2, 3, 8, 40]), rng.choice([1, 2, 4, 7, 16, 20, 32, 64])
+        seqs, page = rng.choice([1, 2, 5, 16, 64, 300, 1100]), rng.choice([16, 64, 1024])
+        max_kv = int(2 ** rng.uniform(0, 18))
+        max_new = rng.choice([1, 1, 2, 5, 17, 64, 500, 5000])
+        tokens = rng.choice([seqs * max_new, max(1, seqs * max_new // 3), seqs * max_new + 7])
+        c = cache_of(nat, dtype=rng.randrange(3), kv_heads=heads, head_dim=rng.choice([64, 128]), page_tokens=page)
+        b = batch_of(nat, seqs=seqs, tokens=tokens, max_new=max_new, max_kv=max_kv, table_width=-(-max_kv // page))
+        size = nat.sz_paged_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), heads * group)
+        for window in [0, 1, 16, 127, 1000, max_kv // 2, max_kv, 2 * max_kv + 5]:
+            got = calls(nat, c, b, q_heads=heads * group, window=window, ws_bytes=size, out=None)[2]
+            assert got == ARG, (heads, group, seqs, max_kv, max_new, tokens, window)
