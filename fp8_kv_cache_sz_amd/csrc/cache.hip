@@ -146,7 +146,7 @@ __global__ __launch_bounds__(kMoveThreads) void sz_cache_move(PagedCache c, Page
                 const uint32_t mid = i + (past - i) / 2;
                 (b.starts[mid] <= (int32_t)t ? i : past) = mid;
             }
-            s = sequence(b, i);
+            if (i < b.seqs) s = sequence(b, i);
         }
         const int32_t pos = s.len - s.n + ((int32_t)t - s.start);
         if ((int32_t)t >= s.start && (int32_t)t < s.start + s.n && pos >= 0) {

@@ -62,6 +62,7 @@ class PagedCache:
             raise ValueError("status is one int32 on the cache's device")
         self.dtype, self.data, self.scales, self.status = dtype, data, scales, status
         self.device = data.device
+        self._index = data.device.index if data.device.type == "cuda" else None
         self.pages, _, self.kv_heads, self.page_tokens, self.head_dim = data.shape
         c = _native.sz_cache(dtype, self.page_tokens, self.kv_heads, self.head_dim, self.pages, data.data_ptr(),
                              scales.data_ptr() if scales is not None else None)
@@ -149,13 +150,12 @@ def _run(name, call, cache, batch, args, stream, owned=()):
     """Launches a call on `stream` (None: the current one) with the cache's
     device current.  Memory that this layer took from the current stream's
     pool (`owned`) is handed over to a stream other than that."""
-    device = cache.device
+    device, index = cache.device, cache._index
     if batch.device != device:
         raise ValueError("the batch is on %s, the cache on %s" % (batch.device, device))
-    index = device.index
-    if device.type != "cuda":
+    if index is None:
         raise ValueError("the cache is on %s; its calls run on the GPU" % device)
-    if stream is None and torch.cuda.current_device() == index:
+    if stream is None and torch._C._cuda_getDevice() == index:
         # the common case, without a Stream object: small calls are as short as their launch
         rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status,
                   torch._C._cuda_getCurrentRawStream(index))
@@ -233,7 +233,8 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
 
 def attention_workspace(cache: PagedCache, batch: PageBatch, q_heads: int) -> torch.Tensor:
     """A workspace for ``paged_attention`` of this batch's bounds, with any
-    window.  Its first ``ARRIVALS`` bytes are zero, as every call leaves them."""
+    window.  Its first ``ARRIVALS`` bytes are zero, as every call leaves them
+    (they are cleared on the current stream, before any call that uses it)."""
     if q_heads <= 0 or q_heads % cache.kv_heads:
         raise ValueError("q_heads is a multiple of the cache's %d KV heads, got %d" % (cache.kv_heads, q_heads))
     n = _native.sz_paged_attention_workspace_size(cache._ref, batch._ref(cache.page_tokens), q_heads)

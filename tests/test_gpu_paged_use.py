@@ -291,3 +291,26 @@ def test_streams_of_another_device_are_refused():
                  lambda: sz().paged_attention(x, cache, batch, stream=other)):
         with pytest.raises(ValueError, match="stream is on"):
             call()
+
+
+@pytest.mark.parametrize("seqs", [62, 63, 64, 126, 127])
+def test_tokens_behind_the_last_sequence_belong_to_none(seqs):
+    """What lies in memory behind the batch's arrays, a sequence by its looks,
+    is not read: the tokens behind the last one are nobody's."""
+    m = sz()
+    H, D, P = 1, 64, 16
+    table = torch.arange(seqs + 1, dtype=torch.int32, device="cuda").view(-1, 1)
+    lens = torch.ones(seqs + 1, dtype=torch.int32, device="cuda")
+    starts = torch.arange(seqs + 2, dtype=torch.int32, device="cuda")
+    T = seqs + 1
+    cache = m.paged_cache(seqs + 1, P, H, D)
+    batch = m.PageBatch(table[:seqs], lens[:seqs], starts[:seqs + 1], T)
+    x = torch.ones(T, H, D, dtype=torch.bfloat16, device="cuda")
+    m.cache_write(cache, batch, x, x)
+    assert bool((cache.data[:seqs, :, :, 0] == 1).all()) and not bool(cache.data[seqs].any())
+    k, v = (torch.full((T, H, D), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    m.cache_read(cache, batch, out=(k, v))
+    out = torch.full((T, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    m.paged_attention(x, cache, batch, out=out)
+    for y in (k, v, out):
+        assert bool((y[:seqs] == 1).all()) and bool((y[seqs] == 3).all())
