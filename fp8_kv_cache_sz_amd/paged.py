@@ -28,6 +28,12 @@ from ._native import SZ_BF16, SZ_FP8_E4M3, SZ_FP8_E5M2, SplitZipError
 E4M3 = SZ_FP8_E4M3
 ARRIVALS = 4096         # bytes of counters at the start of an attention workspace
 
+# Looked up once: a small call is as short as the Python in front of its launch.
+_bfloat16 = torch.bfloat16
+_grad_enabled = torch.is_grad_enabled
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
 _ELEMENT = {SZ_BF16: torch.bfloat16, SZ_FP8_E5M2: torch.float8_e5m2, SZ_FP8_E4M3: torch.float8_e4m3fn}
 
 
@@ -62,7 +68,7 @@ class PagedCache:
             raise ValueError("status is one int32 on the cache's device")
         self.dtype, self.data, self.scales, self.status = dtype, data, scales, status
         self.device = data.device
-        self._index = data.device.index if data.device.type == "cuda" else None
+        self._index = data.get_device()                 # -1: not on a GPU
         self.pages, _, self.kv_heads, self.page_tokens, self.head_dim = data.shape
         c = _native.sz_cache(dtype, self.page_tokens, self.kv_heads, self.head_dim, self.pages, data.data_ptr(),
                              scales.data_ptr() if scales is not None else None)
@@ -112,6 +118,7 @@ class PageBatch:
             raise ValueError("tokens, max_new and max_kv count from 0")
         self.page_table, self.kv_lens, self.starts = page_table, kv_lens, starts
         self.device, self.seqs, self.width, self.tokens = page_table.device, seqs, width, tokens
+        self._index = page_table.get_device()
         self.max_new = tokens if max_new is None else max_new
         self.max_kv = max_kv
         self._by_page = {}
@@ -132,16 +139,16 @@ class PageBatch:
 
 
 def _rows(name, t, tokens, heads, cache):
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _bfloat16:
         raise TypeError("%s is a bfloat16 tensor, got %s" % (name, t.dtype))
     if t.shape != (tokens, heads, cache.head_dim):
         raise ValueError("%s is [%d, %d, %d], got %s" % (name, tokens, heads, cache.head_dim, tuple(t.shape)))
-    if t.device != cache.device:
+    if t.get_device() != cache._index:
         raise ValueError("%s is on %s, the cache on %s" % (name, t.device, cache.device))
     token, head, last = t.stride()
     if last != 1 and tokens:
         raise ValueError("%s needs contiguous rows (a last stride of 1)" % name)
-    if t.requires_grad and torch.is_grad_enabled():
+    if t.requires_grad and _grad_enabled():
         raise ValueError("%s requires a gradient, and the paged cache has none to give (torch.no_grad)" % name)
     return t.data_ptr(), token, head
 
@@ -150,18 +157,18 @@ def _run(name, call, cache, batch, args, stream, owned=()):
     """Launches a call on `stream` (None: the current one) with the cache's
     device current.  Memory that this layer took from the current stream's
     pool (`owned`) is handed over to a stream other than that."""
-    device, index = cache.device, cache._index
-    if batch.device != device:
-        raise ValueError("the batch is on %s, the cache on %s" % (batch.device, device))
-    if index is None:
-        raise ValueError("the cache is on %s; its calls run on the GPU" % device)
-    if stream is None and torch._C._cuda_getDevice() == index:
-        # the common case, without a Stream object: small calls are as short as their launch
-        rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status,
-                  torch._C._cuda_getCurrentRawStream(index))
+    index = cache._index
+    if batch._index != index:
+        raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
+    if index < 0:
+        raise ValueError("the cache is on %s; its calls run on the GPU" % cache.device)
+    if stream is None and _current_device() == index:            # the common case, without a Stream object
+        rc = call(cache._ref, batch._by_page.get(cache.page_tokens) or batch._ref(cache.page_tokens), *args,
+                  cache._status, _current_stream(index))
         if rc:
             _native.check(name, rc)
         return
+    device = cache.device
     if stream is not None and stream.device != device:
         raise ValueError("the stream is on %s, the cache on %s" % (stream.device, device))
     current = torch.cuda.current_stream(device)
@@ -211,7 +218,7 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
     tokens, heads, dim = batch.tokens, cache.kv_heads, cache.head_dim
     owned = ()
     if out is None:
-        both = torch.empty((2, tokens, heads, dim), dtype=torch.bfloat16, device=cache.device)
+        both = cache.data.new_empty((2, tokens, heads, dim), dtype=_bfloat16)
         owned = (both,)
         k, v = both.unbind(0)
         at, row = both.data_ptr(), heads * dim
@@ -252,9 +259,10 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
     head_dim**-0.5; with ``window`` > 0 a token sees the last ``window``
     positions up to its own.  Returns bfloat16 ``out``, or ``(out, lse)`` with
     ``lse`` true or a float32 ``[tokens, q_heads]`` tensor to write into."""
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q is [tokens, q_heads, head_dim]")
-    q_heads = q.shape[1]
+    q_heads = shape[1]
     qp, q_token, q_head = _rows("q", q, batch.tokens, q_heads, cache)
     if q_heads == 0 or q_heads % cache.kv_heads:
         raise ValueError("q has %d heads, not a multiple of the cache's %d KV heads" % (q_heads, cache.kv_heads))
@@ -277,7 +285,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
     if ws is None:
         ws = attention_workspace(cache, batch, q_heads)
         owned.append(ws)
-    elif not ws.is_contiguous() or ws.device != cache.device:
+    elif not ws.is_contiguous() or ws.get_device() != cache._index:
         raise ValueError("ws is a contiguous tensor on the cache's device (attention_workspace)")
     _run("sz_paged_attention", _native.lib.sz_paged_attention, cache, batch,
          (qp, q_heads, q_token, q_head, cache.head_dim ** -0.5 if scale is None else scale, min(window, 1 << 30),
