@@ -737,8 +737,8 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
 // Bound by the matrix unit with the vector unit's powers beside it: of a
 // tile's 3,300 cycles a wave (two share a SIMD) 1,024 are products and 900
 // powers.  Measured (MI355X, 8 KV heads of 128, 32 query heads): 2,048 tokens
-// over 16,384 in E5M2 542 us, 1,078 TFLOP/s; six BF16 prompts of up to 4,096
-// tokens 375 us, 893 TFLOP/s, 15 % of it the workgroups' starts.
+// over 16,384 in E5M2 539 us, 1,084 TFLOP/s; six BF16 prompts of up to 4,096
+// tokens 369 us, 907 TFLOP/s, 15 % of it the workgroups' starts.
 // ---------------------------------------------------------------------------
 // 16-byte pieces of a row are stored at piece ^ swizzle(row), so that 16 lanes
 // meet no bank twice: K reads take the same piece of 32 rows, V reads four
