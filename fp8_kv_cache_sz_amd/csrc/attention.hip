@@ -1202,6 +1202,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
         for (int r = 0; r < 16; ++r) top0 = fmaxf(top0, st[0][r]);
         settle(0);
         scale_late = false;                                                    // o is still zero
+        __syncthreads();                                                       // every wave has read tile 0: its K's half is free
         uint32_t t = 0;
         while (true) {
             const uint32_t even = t % 2, odd = even ^ 1;
