@@ -9,7 +9,7 @@ ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", name) for name in
            ("encode.hip", "decode.hip", "calibrate.hip", "runtime.hip", "transfer.hip", "cache.hip", "attention.hip")]
 HEADERS = [os.path.join(ROOT, "include", "splitzip.h"), os.path.join(HERE, "csrc", "common.hpp"),
-           os.path.join(HERE, "csrc", "paged.hpp")]
+           os.path.join(HERE, "csrc", "paged.hpp"), os.path.join(HERE, "csrc", "keys.hpp")]
 LIBRARY = os.path.join(HERE, "libsplitzip.so")
 ARCH = "gfx950"
 

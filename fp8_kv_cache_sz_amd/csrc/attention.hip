@@ -62,7 +62,7 @@ struct AttnArgs {
     uint32_t *arrived;        // [seqs][kv heads] chunks done, 0 between calls; null: sz_attn_join joins
     float scale, c2;          // c2: scale log2 e
     uint32_t group, q_heads;
-    int32_t window;           // 0: none
+    int32_t window;           // 0: none; window_keys()
     uint32_t rows_limit;      // sequences of up to so many rows are sz_attn_rows's
     uint32_t rows_chunk, rows_splits;      // keys of a chunk, chunks (sz_attn_rows)
     uint32_t tile_chunk, tile_splits;      // (sz_attn_tiles)
@@ -71,15 +71,14 @@ struct AttnArgs {
 // First key of sequence s that any of its new tokens sees, rounded down.
 __device__ __forceinline__ int32_t first_key(const Sequence &s, int32_t window)
 {
-    const int32_t lo = window > 0 ? max(0, s.len - s.n - window + 1) : 0;
-    return lo & ~(int32_t)(kKeyAlign - 1);
+    return first_seen(s.len - s.n, window) & ~(int32_t)(kKeyAlign - 1);
 }
 
 // The visible keys [lo, hi] of position p; none (hi < lo) for p < 0.
 __device__ __forceinline__ void visible(int32_t p, int32_t window, int32_t &lo, int32_t &hi)
 {
     hi = p;
-    lo = window > 0 ? max(0, p - window + 1) : 0;
+    lo = first_seen(p, window);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -411,7 +410,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     }
     bool far = false;
 
-    const int32_t all_lo = a.window > 0 ? max(0, s.len - a.window) : 0;      // every row sees [all_lo, all_hi]
+    const int32_t all_lo = first_seen(s.len - 1, a.window);                  // every row sees [all_lo, all_hi]
     const int32_t all_hi = s.len - s.n;
 
     constexpr int32_t STEP = 32 * WAVES;
@@ -514,7 +513,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
         bool wild = false;
         if constexpr (MASKED) {
             uint32_t found = 0;
-            const int32_t any_lo = a.window > 0 ? max(0, all_hi - a.window + 1) : 0;
+            const int32_t any_lo = first_seen(all_hi, a.window);
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 const int32_t key = kb + 16 * (r / 4) + 4 * (int32_t)g + r % 4;
@@ -919,11 +918,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
     const int32_t p_first = s.len - s.n + tok_first, p_last = s.len - s.n + tok_last;
     const bool whole = a.tile_splits == 1 || chunks_of(s, a.window, a.tile_chunk) == 1;
     const int64_t chunk0 = (int64_t)first_key(s, a.window) + (int64_t)split * a.tile_chunk;
-    const int32_t any_lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;  // some row sees [any_lo, p_last]
+    const int32_t any_lo = first_seen(p_first, a.window);                      // some row sees [any_lo, p_last]
     const int32_t begin = (int32_t)max(chunk0, (int64_t)(any_lo & ~(int32_t)(kTileKeys - 1)));
     const int32_t end = (int32_t)min((int64_t)p_last + 1, chunk0 + a.tile_chunk);
     if (whole ? split > 0 : begin >= end) return;                              // no row's chunk: nobody reads it
-    const int32_t all_lo = a.window > 0 ? max(0, p_last - a.window + 1) : 0;   // every row sees [all_lo, p_first]
+    const int32_t all_lo = first_seen(p_last, a.window);                       // every row sees [all_lo, p_first]
 
     bf16x8 q[D / 16];               // a row that is not there computes what the last one does, and stores nothing
 #pragma unroll
@@ -1519,7 +1518,8 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
     if (!aligned16(d_out) || !aligned16(d_ws) || (reinterpret_cast<uintptr_t>(d_lse) & 3u)) return SZ_E_ALIGN;
     if (a.b.tokens == 0 || a.b.seqs == 0) return SZ_OK;
     a.group = q_heads / a.c.heads;
-    const AttnPlan p = attn_plan(cache, a.b, a.group, window);
+    a.window = window_keys(window);
+    const AttnPlan p = attn_plan(cache, a.b, a.group, (uint32_t)a.window);
     const JoinPlan j = join_plan(a.b, p, a.group, q_heads, cache->head_dim);
     if (!launchable(a.c, a.b, p, j)) return SZ_E_ARG;
     const uint32_t splits = std::max(p.rows_splits, p.tile_splits);
@@ -1538,7 +1538,6 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
                                            up256(splits * rows * cache->head_dim * 4));
     a.scale = scale;
     a.q_heads = q_heads;
-    a.window = (int32_t)window;
     a.rows_limit = p.rows_limit;
     a.rows_chunk = p.rows_chunk;
     a.rows_splits = p.rows_splits;

@@ -11,6 +11,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "keys.hpp"
 
 namespace sz {
 
@@ -39,7 +40,6 @@ struct Sequence {
 
 constexpr uint32_t kMinPage = 16, kMaxPage = 1024;
 constexpr uint32_t kMaxHeads = 1024;
-constexpr uint32_t kMaxTokens = 1u << 30;       // of a batch, of a sequence: sums of two stay below 2^31
 
 inline uint32_t elem_bytes(uint32_t dtype) { return dtype == SZ_BF16 ? 2u : 1u; }
 
