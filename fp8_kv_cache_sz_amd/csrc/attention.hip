@@ -562,8 +562,9 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
             // Their upper 16 bits, and the rest in a second product: products
             // are cheap beside the reads (0 to 1 % of the time), and the result
             // is as exact as its own rounding.  Where every row sees every key
-            // the rest is 2^-133 at least (BF16's smallest): 0 times an
-            // infinite value is a NaN.
+            // the rest of a probability above 0 (2^-126 at least) is 2^-133 at
+            // least (BF16's smallest): 0 times an infinite value is a NaN.  A
+            // probability of 0 has no rest: its value does not count.
             u32x4 pw, rw;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -572,7 +573,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
                 for (int h = 0; h < 2; ++h) {
                     const float x = p[2 * e + h];
                     rest[h] = x - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xFFFF0000u);
-                    if constexpr (!MASKED) rest[h] = fmaxf(rest[h], 0x1p-133f);
+                    if constexpr (!MASKED) rest[h] = __builtin_amdgcn_fmed3f(rest[h], x, 0x1p-133f);   // max(rest, min(x, ..))
                 }
                 pw[e] = perm(__builtin_bit_cast(uint32_t, p[2 * e + 1]), __builtin_bit_cast(uint32_t, p[2 * e]),
                              0x07060302u);
