@@ -34,6 +34,7 @@ _grad_enabled = torch.is_grad_enabled
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
+_BAD_BATCH = "paged cache (device check of the batch)"
 _ELEMENT = {SZ_BF16: torch.bfloat16, SZ_FP8_E5M2: torch.float8_e5m2, SZ_FP8_E4M3: torch.float8_e4m3fn}
 
 
@@ -80,7 +81,8 @@ class PagedCache:
         status = int(self.status.item())
         if status != 0:
             self.status.zero_()
-            raise SplitZipError("paged cache (device check of the batch)", status)
+            torch.cuda.current_stream(self.device).synchronize()     # before a call on any stream reports again
+            raise SplitZipError(_BAD_BATCH, status)
 
 
 def paged_cache(pages: int, page_tokens: int, kv_heads: int, head_dim: int, dtype: int = SZ_BF16,
@@ -153,18 +155,20 @@ def _rows(name, t, tokens, heads, cache):
     return t.data_ptr(), token, head
 
 
-def _run(name, call, cache, batch, args, stream, owned=()):
+def _run(name, call, cache, batch, args, stream, owned=(), status=None):
     """Launches a call on `stream` (None: the current one) with the cache's
-    device current.  Memory that this layer took from the current stream's
+    device current, reporting into `status` (None: the cache's word).  Memory that this layer took from the current stream's
     pool (`owned`) is handed over to a stream other than that."""
     index = cache._index
+    if status is None:
+        status = cache._status
     if batch._index != index:
         raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
     if index < 0:
         raise ValueError("the cache is on %s; its calls run on the GPU" % cache.device)
     if stream is None and _current_device() == index:            # the common case, without a Stream object
         rc = call(cache._ref, batch._by_page.get(cache.page_tokens) or batch._ref(cache.page_tokens), *args,
-                  cache._status, _current_stream(index))
+                  status, _current_stream(index))
         if rc:
             _native.check(name, rc)
         return
@@ -176,7 +180,7 @@ def _run(name, call, cache, batch, args, stream, owned=()):
     if side is not None and owned:
         side.wait_stream(current)
     with torch.cuda.device(device):
-        rc = call(cache._ref, batch._ref(cache.page_tokens), *args, cache._status, (side or current).cuda_stream)
+        rc = call(cache._ref, batch._ref(cache.page_tokens), *args, status, (side or current).cuda_stream)
     _native.check(name, rc)
     if side is not None:
         for t in owned:
@@ -191,10 +195,18 @@ def _raise_status(cache, stream):
 
 def cache_check(cache: PagedCache, batch: PageBatch, stream=None) -> None:
     """Raises ``SplitZipError`` unless the batch fits the cache and no page is
-    written from two places (sz_cache_check); waits for the device."""
-    ws = torch.empty(_native.sz_cache_check_workspace_size(cache._ref), dtype=torch.uint8, device=cache.device)
-    _run("sz_cache_check", _native.lib.sz_cache_check, cache, batch, (ws.data_ptr(), ws.numel()), stream, (ws,))
-    _raise_status(cache, stream)
+    written from two places (sz_cache_check); waits for the device.  The check
+    reports into a word of its own: what earlier calls put into the cache's
+    stays there."""
+    nbytes = _native.sz_cache_check_workspace_size(cache._ref)
+    ws = torch.empty(nbytes // 4 + 1, dtype=torch.int32, device=cache.device)           # claims, then the word
+    _run("sz_cache_check", _native.lib.sz_cache_check, cache, batch, (ws.data_ptr(), nbytes), stream, (ws,),
+         ws.data_ptr() + nbytes)
+    if stream is not None:
+        stream.synchronize()
+    found = int(ws[-1].item())
+    if found != 0:
+        raise SplitZipError(_BAD_BATCH, found)
 
 
 def cache_write(cache: PagedCache, batch: PageBatch, k: torch.Tensor, v: torch.Tensor, stream=None,

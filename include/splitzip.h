@@ -375,7 +375,8 @@ int sz_cache_read(const sz_cache *cache, const sz_batch *batch, void *d_k, uint6
 /* Checks a batch before it is used: everything that the calls above and
  * below check as they go, for all pages of all sequences, and that every
  * page that a new token falls into is named only once among such pages.
- * Sets *d_status to SZ_OK or SZ_E_FORMAT.  d_ws: ws_bytes >=
+ * Sets *d_status to SZ_OK or SZ_E_FORMAT, whatever it held: where one word
+ * stands for a whole step, the check gets another.  d_ws: ws_bytes >=
  * sz_cache_check_workspace_size(cache), 4 bytes a page. */
 uint64_t sz_cache_check_workspace_size(const sz_cache *cache);
 int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uint64_t ws_bytes, int32_t *d_status,
