@@ -895,7 +895,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
         return (int64_t)(((uint64_t)(uint32_t)max(a.b.starts[i], 0) * a.group) / kTileRows) + i;
     };
     const int32_t found = wave_last_not_above(a.b.seqs, slot, first_slot);
-    if (found < 0) return;
+    if (found < 0) {                                                           // before the first sequence's slots
+        if (a.b.starts[0] > (int32_t)a.b.tokens) flag_batch(a.b);              // which may own none
+        return;
+    }
     const uint32_t seq = uniform((uint32_t)found);
     const Sequence s = sequence(a.b, seq);
     const uint64_t all_rows = (uint64_t)s.n * a.group;

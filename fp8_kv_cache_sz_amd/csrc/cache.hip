@@ -127,6 +127,15 @@ __global__ __launch_bounds__(kMoveThreads) void sz_cache_move(PagedCache c, Page
     const bool there = base + lane < b.seqs;
     const int32_t start = base + lane <= b.seqs ? b.starts[base + lane] : INT32_MAX;
     const int32_t len = there ? b.lens[base + lane] : 0;
+    // What no token's own sequence shows: starts that descend, and (the first
+    // wave's) an axis that begins or ends outside [0, tokens].
+    const int32_t after = __shfl_down(start, 1, 64);
+    bool wrong = lane < 63 && there && after < start;
+    if (unit == 0 && lane < 2) {
+        const int32_t edge = b.starts[lane * b.seqs];
+        wrong |= edge < 0 || edge > (int32_t)b.tokens;
+    }
+    if (wrong) flag_batch(b);
     uint32_t count = 0;                              // of the starts up to this lane's token
 #pragma unroll
     for (uint32_t j = 0; j < kMoveTokens; ++j) {

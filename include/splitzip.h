@@ -315,7 +315,9 @@ int sz_decode_noalloc(const void *d_in, uint64_t in_bytes, int dtype, void *d_ou
  * SZ_E_FORMAT when the batch contradicts itself, the host's bounds or the
  * cache (starts that descend or leave [0, tokens], a length outside [0,
  * max_kv], more than max_new new tokens, a page number outside the cache).
- * It is never cleared, except by sz_cache_check, so one word can stand for a
+ * A call reports what it meets: it looks up the sequences and pages of the
+ * tokens it has, sz_cache_check all of them.
+ * The word is never cleared, except by sz_cache_check, so it can stand for a
  * whole step.  Such a sequence (or token) is skipped, and what it would have
  * written keeps its old contents or, where a page number is wrong, is
  * unspecified in the outputs; memory outside the cache, the outputs and the

@@ -42,3 +42,48 @@ def test_a_check_does_not_clear_what_was_reported(dtype, side):
     with pytest.raises(m.SplitZipError):                       # a check alone reports into no other call
         m.cache_check(cache, bad)
     m.paged_attention(x, cache, good)
+
+
+STARTS = {"behind the axis": [9, 12], "all behind it": [200, 300], "past its end": [0, 2, 5], "before it": [-2, 0, 2],
+          "all before it": [-9, -3], "descending onto an empty one": [0, 2, 2, 1, 2]}
+
+
+@pytest.mark.parametrize("name", sorted(STARTS))
+@pytest.mark.parametrize("heads", [1, 32], ids=["few", "many"])
+def test_starts_outside_the_axis_are_reported(name, heads):
+    """Also where no token's own sequence is wrong, and no sequence has a token."""
+    m = sz()
+    starts = STARTS[name]
+    n = len(starts) - 1
+    cache = m.paged_cache(8, P, H, D)
+    before = cache.data.clone()
+    x = torch.ones(2, H, D, dtype=torch.bfloat16, device="cuda")
+    b = batch(list(range(n)), [3] * n, starts, 2)
+    m.cache_write(cache, b, x, x, check=False)
+    with pytest.raises(m.SplitZipError):
+        cache.raise_status()
+    with pytest.raises(m.SplitZipError):
+        m.cache_read(cache, b)
+    with pytest.raises(m.SplitZipError):
+        m.paged_attention(x.expand(2, heads, D).contiguous(), cache, b)
+    after = cache.data.clone()
+    with pytest.raises(m.SplitZipError):
+        m.cache_write(cache, b, x, x)
+    assert torch.equal(cache.data, after)                      # a checked write writes nothing
+    if "all" in name or name == "behind the axis":
+        assert torch.equal(after, before)
+
+
+def test_good_starts_are_not_reported():
+    """Gaps before the first sequence and behind the last, empty sequences."""
+    m = sz()
+    cache = m.paged_cache(300, P, H, D)
+    x = torch.ones(9, H, D, dtype=torch.bfloat16, device="cuda")
+    for starts in ([0, 9], [4, 9], [9, 9], [0, 0], [3, 3, 5, 5, 5, 7], [2] * 100 + [5] * 100 + [6], [9] * 200):
+        n = len(starts) - 1
+        b = batch(list(range(n)), [9] * n, starts, 9)
+        for heads in (1, 32):
+            m.cache_write(cache, b, x, x, check=False)
+            m.cache_read(cache, b)
+            m.paged_attention(x.expand(9, heads, D).contiguous(), cache, b)
+            cache.raise_status()
