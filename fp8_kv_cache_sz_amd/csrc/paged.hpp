@@ -147,7 +147,8 @@ __device__ __forceinline__ uint64_t row_index(const PagedCache &c, uint32_t page
 }
 
 // Two FP8 values (the low or high half of w) times 2^(byte - 127), as a BF16
-// pair; scale_bits = byte << 23.  One instruction, exact: an FP8 value has at
+// pair; scale_bits = byte << 23, of which the instruction takes the exponent:
+// byte 0 is 2^-127, 255 a NaN.  One instruction, exact: an FP8 value has at
 // most four significant bits and BF16 keeps eight, so the product rounds only
 // where it leaves BF16's range.
 template <int DT, bool HI>

@@ -290,7 +290,8 @@ int sz_decode_noalloc(const void *d_in, uint64_t in_bytes, int dtype, void *d_ou
  * dtype (index 0 of the second axis keys, 1 values), contiguous, 16-byte
  * aligned.  FP8 caches keep one scale byte for each row (one token's one
  * head, K or V) in scales, [pages][2][kv_heads][page_tokens], 16-byte
- * aligned: a row's values are q * 2^(byte - 127).  head_dim is 64 or 128,
+ * aligned: a row's values are q * 2^(byte - 127), and NaN where the byte is
+ * 255, which sz_cache_write never makes.  head_dim is 64 or 128,
  * page_tokens a power of two from 16 to 1024, kv_heads at most 1024.
  *
  * sz_batch (device arrays, int32, 4-byte aligned): sequence i has kv_lens[i]
