@@ -38,12 +38,32 @@ _BAD_BATCH = "paged cache (device check of the batch)"
 _ELEMENT = {SZ_BF16: torch.bfloat16, SZ_FP8_E5M2: torch.float8_e5m2, SZ_FP8_E4M3: torch.float8_e4m3fn}
 
 
-class PagedCache:
+class _Fixed:
+    """Attributes that the C structure of an object was made from are not
+    reassigned: the kernels would go on with the tensors and bounds it had."""
+    _made = False
+
+    def __setattr__(self, name, value):
+        if self._made and name in self._FIXED and value is not getattr(self, name):    # kv_lens += 1 assigns itself
+            raise AttributeError("%s.%s is what its calls were made from: make another %s"
+                                 % (type(self).__name__, name, type(self).__name__))
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in self._FIXED:
+            raise AttributeError("%s.%s is what its calls were made from" % (type(self).__name__, name))
+        object.__delattr__(self, name)
+
+
+class PagedCache(_Fixed):
     """One layer's pages.  ``data``: a contiguous device tensor ``[pages, 2,
     kv_heads, page_tokens, head_dim]`` of the element type (FP8 also as
     ``uint8``); ``scales``: ``uint8`` ``[pages, 2, kv_heads, page_tokens]``
-    for FP8, None for BF16.  The tensors stay the caller's.  ``status`` is the
-    device int32 that the calls report into."""
+    for FP8, None for BF16.  The tensors stay the caller's, and their memory
+    where it is (no ``set_`` or ``resize_``); the attributes are not reassigned.
+    ``status`` is the device int32 that the calls report into."""
+
+    _FIXED = frozenset(("dtype", "data", "scales", "status", "device", "pages", "kv_heads", "page_tokens", "head_dim"))
 
     def __init__(self, dtype: int, data: torch.Tensor, scales: torch.Tensor | None = None,
                  status: torch.Tensor | None = None):
@@ -74,6 +94,7 @@ class PagedCache:
         c = _native.sz_cache(dtype, self.page_tokens, self.kv_heads, self.head_dim, self.pages, data.data_ptr(),
                              scales.data_ptr() if scales is not None else None)
         self._c, self._ref, self._status = c, ctypes.byref(c), status.data_ptr()
+        self._made = True
 
     def raise_status(self) -> None:
         """Waits for the current stream, raises if a call found its batch
@@ -97,12 +118,16 @@ def paged_cache(pages: int, page_tokens: int, kv_heads: int, head_dim: int, dtyp
     return PagedCache(dtype, data, torch.full(shape[:-1], 127, dtype=torch.uint8, device=device))
 
 
-class PageBatch:
+class PageBatch(_Fixed):
     """The tokens of a call.  ``page_table`` int32 ``[seqs, width]``,
     ``kv_lens`` int32 ``[seqs]``, ``starts`` int32 ``[seqs + 1]``, contiguous,
     on one device; ``tokens`` the length of the packed axis.  ``max_new`` and
     ``max_kv`` bound a sequence's new tokens and length; without them the
-    launches are shaped for ``tokens`` and for full tables."""
+    launches are shaped for ``tokens`` and for full tables.  The tensors' values
+    may change between calls; their memory stays where it is, and the attributes
+    are not reassigned."""
+
+    _FIXED = frozenset(("page_table", "kv_lens", "starts", "device", "seqs", "width", "tokens", "max_new", "max_kv"))
 
     def __init__(self, page_table: torch.Tensor, kv_lens: torch.Tensor, starts: torch.Tensor, tokens: int,
                  max_new: int | None = None, max_kv: int | None = None):
@@ -124,6 +149,7 @@ class PageBatch:
         self.max_new = tokens if max_new is None else max_new
         self.max_kv = max_kv
         self._by_page = {}
+        self._made = True
 
     def _ref(self, page_tokens: int):
         """The sz_batch for caches of this page size (max_kv defaults to a
@@ -157,8 +183,9 @@ def _rows(name, t, tokens, heads, cache):
 
 def _run(name, call, cache, batch, args, stream, owned=(), status=None):
     """Launches a call on `stream` (None: the current one) with the cache's
-    device current, reporting into `status` (None: the cache's word).  Memory that this layer took from the current stream's
-    pool (`owned`) is handed over to a stream other than that."""
+    device current, reporting into `status` (None: the cache's word).  Memory
+    that this layer took from the current stream's pool (`owned`) is handed
+    over to a stream other than that."""
     index = cache._index
     if status is None:
         status = cache._status

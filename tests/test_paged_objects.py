@@ -1,0 +1,45 @@
+"""The Python objects of the paged cache on the CPU: what the C structures were
+made from does not change under them."""
+import pytest
+import torch
+
+
+def objects():
+    import fp8_kv_cache_sz_amd as sz
+    cache = sz.paged_cache(4, 16, 2, 64, sz.E4M3, device="cpu")
+    batch = sz.PageBatch(torch.zeros(2, 3, dtype=torch.int32), torch.tensor([3, 4], dtype=torch.int32),
+                         torch.tensor([0, 1, 2], dtype=torch.int32), 2, max_new=1, max_kv=40)
+    return cache, batch
+
+
+def test_fields_of_the_c_structures_are_not_reassigned():
+    """A new tensor or bound would be ignored, and the old one's memory freed
+    under the kernels that still use it."""
+    cache, batch = objects()
+    for name in ("data", "scales", "status", "dtype", "pages", "kv_heads", "page_tokens", "head_dim", "device"):
+        was = getattr(cache, name)
+        with pytest.raises(AttributeError, match="make another PagedCache"):
+            setattr(cache, name, was.clone() if isinstance(was, torch.Tensor) else object())
+        with pytest.raises(AttributeError):
+            delattr(cache, name)
+        assert getattr(cache, name) is was
+    for name in ("page_table", "kv_lens", "starts", "tokens", "max_new", "max_kv", "seqs", "width", "device"):
+        was = getattr(batch, name)
+        with pytest.raises(AttributeError, match="make another PageBatch"):
+            setattr(batch, name, was.clone() if isinstance(was, torch.Tensor) else object())
+        with pytest.raises(AttributeError):
+            delattr(batch, name)
+        assert getattr(batch, name) is was
+
+
+def test_other_attributes_and_values_in_place_are_free():
+    cache, batch = objects()
+    cache.layer = 3
+    cache.layer = 4
+    batch.note = "x"
+    del batch.note
+    cache.data.view(torch.uint8).fill_(1)
+    batch.kv_lens.add_(1)
+    lens = batch.kv_lens
+    batch.kv_lens += 2                                          # in place, then the same tensor assigned
+    assert batch.kv_lens is lens and lens.tolist() == [6, 7] and cache.layer == 4
