@@ -21,6 +21,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native
 from ._native import SZ_BF16, SZ_FP8_E4M3, SZ_FP8_E5M2, SplitZipError
@@ -69,6 +70,7 @@ class PagedCache(_Fixed):
                  status: torch.Tensor | None = None):
         if dtype not in _ELEMENT:
             raise ValueError("a paged cache holds BF16, E5M2 or E4M3, got dtype %r" % (dtype,))
+        _plain("data", data)
         if data.dtype != _ELEMENT[dtype] and not (dtype != SZ_BF16 and data.dtype == torch.uint8):
             raise TypeError("data is %s, the cache's element type is %s" % (data.dtype, _ELEMENT[dtype]))
         if data.dim() != 5 or data.shape[1] != 2 or not data.is_contiguous():
@@ -176,9 +178,17 @@ def _rows(name, t, tokens, heads, cache):
     token, head, last = t.stride()
     if last != 1 and tokens:
         raise ValueError("%s needs contiguous rows (a last stride of 1)" % name)
+    if forward_ad._current_level >= 0 or (t.requires_grad and _grad_enabled()):
+        _plain(name, t)
+    return t.data_ptr(), token, head
+
+
+def _plain(name, t):
+    """Refuses tensors that autograd follows: the calls have no derivative."""
     if t.requires_grad and _grad_enabled():
         raise ValueError("%s requires a gradient, and the paged cache has none to give (torch.no_grad)" % name)
-    return t.data_ptr(), token, head
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError("%s has a tangent, and the paged cache has none to give" % name)
 
 
 def _run(name, call, cache, batch, args, stream, owned=(), status=None):
@@ -313,6 +323,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
         owned.append(out)
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != cache.device:
         raise ValueError("out is a contiguous bfloat16 tensor of q's shape on the cache's device")
+    elif out.requires_grad or forward_ad._current_level >= 0:
+        _plain("out", out)
     if lse is True:
         lse = q.new_empty((batch.tokens, q_heads), dtype=torch.float32)
         owned.append(lse)
@@ -321,6 +333,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
     elif lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()
                               or lse.device != cache.device):
         raise ValueError("lse is a contiguous float32 [tokens, q_heads] tensor on the cache's device")
+    elif lse is not None and (lse.requires_grad or forward_ad._current_level >= 0):
+        _plain("lse", lse)
     if ws is None:
         ws = attention_workspace(cache, batch, q_heads)
         owned.append(ws)

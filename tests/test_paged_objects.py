@@ -43,3 +43,46 @@ def test_other_attributes_and_values_in_place_are_free():
     lens = batch.kv_lens
     batch.kv_lens += 2                                          # in place, then the same tensor assigned
     assert batch.kv_lens is lens and lens.tolist() == [6, 7] and cache.layer == 4
+
+
+def calls(sz, cache, batch, x, out=None, lse=False):
+    return [lambda: sz.cache_write(cache, batch, x, x, check=False),
+            lambda: sz.cache_read(cache, batch, out=(x, x.clone()), check=False),
+            lambda: sz.paged_attention(x, cache, batch, out=out, lse=lse, ws=torch.zeros(8), check=False)]
+
+
+def test_tensors_that_autograd_follows_are_refused():
+    """The calls have no derivative in either direction: what would lose a
+    gradient or a tangent is refused, also as an output."""
+    import fp8_kv_cache_sz_amd as sz
+    from torch.autograd import forward_ad
+    cache, batch = objects()
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    lse = torch.zeros(2, 2)
+    on_cpu = dict(match="run on the GPU")                       # the last refusal: all others are passed
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        for call in calls(sz, cache, batch, dual):
+            with pytest.raises(ValueError, match="has a tangent"):
+                call()
+        for call in calls(sz, cache, batch, x):                 # others inside the level are plain
+            with pytest.raises(ValueError, **on_cpu):
+                call()
+        with pytest.raises(ValueError, match="out has a tangent"):
+            calls(sz, cache, batch, x, out=dual)[2]()
+        with pytest.raises(ValueError, match="lse has a tangent"):
+            calls(sz, cache, batch, x, lse=forward_ad.make_dual(lse, lse))[2]()
+        with pytest.raises(ValueError, match="data has a tangent"):
+            sz.PagedCache(sz.BF16, forward_ad.make_dual(torch.zeros(4, 2, 2, 16, 64, dtype=torch.bfloat16),
+                                                        torch.zeros(4, 2, 2, 16, 64, dtype=torch.bfloat16)))
+    for out, rows in ((x.clone().requires_grad_(), lse), (x.clone(), lse.clone().requires_grad_())):
+        call = calls(sz, cache, batch, x, out=out, lse=rows)[2]
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, **on_cpu):
+            call()
+    leaf = torch.zeros(4, 2, 2, 16, 64, dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(ValueError, match="data requires a gradient"):
+        sz.PagedCache(sz.BF16, leaf)
+    with torch.no_grad():
+        sz.PagedCache(sz.BF16, leaf)
