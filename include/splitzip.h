@@ -396,18 +396,21 @@ int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uin
  * [tokens][q_heads][head_dim], contiguous.  d_lse: float [tokens][q_heads]
  * or NULL.  A token that sees no key gets 0 and -inf.  Keys that a token does
  * not see do not reach its result, NaN and infinities included (but for its
- * last bits, where other tokens of the sequence see them).  Sums,
- * scores and lse are 32-bit; with more than 16 rows (new tokens times query
- * heads of a KV head) in a sequence its probabilities may be rounded to BF16.
+ * last bits, where other tokens of the sequence see them).
+ * Sums, scores and lse are 32-bit.  With more than 16 rows (new tokens times
+ * query heads of a KV head) in a sequence its probabilities may be rounded to
+ * BF16; with 16 or less they are held to 2^-15 of each, or 2^-133.  One below
+ * 2^-126 may count as 0 (and 0 times an infinite value is a NaN), or as up to
+ * 2^-140 where later keys outweigh it (so that an infinite value of that kind
+ * stays infinite).  The sums of exp(s_j - m) V_j, with an m up to 8 / log2 e
+ * below the largest score, are divided at the end: values over 2^89 can take
+ * them out of 32 bits' range.  scale must be above 0, scale * log2 e finite.
  * A sequence's results depend on its own tokens and keys alone, and on the
  * call's host fields (seqs, tokens, max_new, max_kv, heads, window), through
  * which the keys are split and the kernels chosen: under the same ones they
  * are the same bit for bit, whatever the other sequences hold and wherever in
- * the batch it stands; under others the last bits differ.  scale must be
- * above 0, scale * log2 e finite.  A probability below 2^-126 may count as 0,
- * and 0 times an infinite value is a NaN.  The sums of exp(s_j - m) V_j, with
- * an m up to 8 / log2 e below the largest score, are divided at the end:
- * values over 2^89 can take them out of 32 bits' range.  d_ws: ws_bytes >=
+ * the batch it stands; under others the last bits differ.
+ * d_ws: ws_bytes >=
  * sz_paged_attention_workspace_size(cache, batch, q_heads) (0 for heads that
  * do not divide; host fields of cache and batch only).  Its first
  * SZ_ATTENTION_COUNTERS bytes are counters of chunks done: the caller clears
