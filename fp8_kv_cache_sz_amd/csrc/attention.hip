@@ -13,7 +13,10 @@
 // instructions take BF16 probabilities: sz_attn_rows, which waits for memory,
 // gives them what the rounding left as a second product; sz_attn_tiles, bound
 // by those products, rounds (at most 2^-8 of each, of either sign, as much as
-// the result's own rounding).
+// the result's own rounding: 0.0020 to 0.0024 of a result's size from the
+// 64-bit one where 32-bit probabilities leave 0.0016 to 0.0017).  A second
+// product would be half as many products again.  l adds the powers before the
+// rounding, so that lse keeps 32 bits.
 //
 // Rows are (token, head of the KV head's group), so one K/V row read serves
 // the G query heads of its KV head.  Both kernels compute S^T = K Q^T, whose
@@ -294,14 +297,14 @@ __device__ __forceinline__ void join_chunks(const AttnArgs &a, uint64_t r, uint3
 //     d = c D/16; byte permutes turn its 8 rows x D/16 values into D/16
 //     operands of 8 keys each.
 // Bound by reading K and V.  Measured (MI355X, 8 KV heads of 128, four query
-// heads each, contexts of 8,192): 100 sequences in BF16 551 us, 6.1 TB/s; 64
-// in E4M3 196 us, 5.5 TB/s (with three waves a SIMD, half of BF16's bytes
-// in flight, and converting); 64 of up to 8,192 124 us, 4.9 TB/s, for the
-// chunks that end late.  One context of 64K (4 heads, BF16) 24 us and 4 to
-// join, 4.8 TB/s: 256 workgroups of 1,024 keys.  The order of the loads and
-// the waits that count them carry this: where a wait in the loop was for all
-// loads in flight, 32 rows took 89 us instead of 83, and one spilled register
-// in it costs 8 %.
+// heads each, contexts of 8,192; two cards differ by 3 %): 100 sequences in
+// BF16 552 us, 6.1 TB/s; 64 in E4M3 194 us, 5.6 TB/s (with three waves a SIMD,
+// half of BF16's bytes in flight, and converting); 64 of up to 8,192 119 us,
+// 5.1 TB/s, for the chunks that end late.  One context of 64K (4 heads, BF16)
+// 24 us and 4.5 to join, 4.7 TB/s: 256 workgroups of 1,024 keys.  The order of
+// the loads and the waits that count them carry this: where a wait in the loop
+// was for all loads in flight, 32 rows took 89 us instead of 83, and one
+// spilled register in it cost 8 %.
 // ---------------------------------------------------------------------------
 template <int DT, int D>
 struct KeyBlock {
@@ -735,10 +738,12 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
 //   S^T: lane (row = lane % 32, g = lane / 32) holds keys 32 b + 8 i + 4 g +
 //     0..3, b = 0, 1, i = 0..3.
 // Bound by the matrix unit with the vector unit's powers beside it: of a
-// tile's 3,300 cycles a wave (two share a SIMD) 1,024 are products and 900
-// powers.  Measured (MI355X, 8 KV heads of 128, 32 query heads): 2,048 tokens
-// over 16,384 in E5M2 539 us, 1,084 TFLOP/s; six BF16 prompts of up to 4,096
-// tokens 369 us, 907 TFLOP/s, 15 % of it the workgroups' starts.
+// tile's 4,400 cycles of a SIMD, which two waves share, 2,048 are products and
+// 2,150 issue vector instructions, and a wave's own order keeps them apart
+// (counters; 256 registers leave no third wave).  Measured (MI355X, 8 KV heads
+// of 128, 32 query heads): 2,048 tokens over 16,384 in E5M2 541 us, 1,080
+// TFLOP/s (534 to 559 on several cards); six BF16 prompts of up to 4,096 tokens
+// 366 us, 914 TFLOP/s, 15 % of it the workgroups' starts.
 // ---------------------------------------------------------------------------
 // 16-byte pieces of a row are stored at piece ^ swizzle(row), so that 16 lanes
 // meet no bank twice: K reads take the same piece of 32 rows, V reads four
@@ -890,7 +895,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
     // Sequence i owns the slots from floor(starts[i] G / rows) + i on: at
     // least as many as its rows fill.  (One sequence after another: the heads
     // of one XCD then read the same keys out of its L2.  The longest tiles of
-    // all sequences first measured 445 us where this takes 385.)
+    // all sequences first measured 445 us where this took 385.)
     const auto first_slot = [&](uint32_t i) {
         return (int64_t)(((uint64_t)(uint32_t)max(a.b.starts[i], 0) * a.group) / kTileRows) + i;
     };
@@ -1307,28 +1312,38 @@ constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;                // of a launch
 // Workgroups that sz_attn_rows wants: enough to fill the card (768 run at a
 // time, and some chunks are behind their sequence's end), and up to kRowsEven
 // while their chunks have kRowsLong keys, to even out lengths.  Against 2,048
-// whatever the chunk's length: 128 sequences of up to 500 E4M3 tokens 24 us
-// (31), 4 of up to 8,192 21 us (26), 100 of 8,192 in BF16 555 us (574), 64 of
-// 8,192 in E4M3 202 us (196).  Against 768: 8 of up to 8,192 25 us (29);
-// against chunks of 2,048: 32 of up to 8,192 71 us (79).
+// whatever the chunk's length (8 KV heads of 128, four query heads each): 128
+// sequences of up to 500 E4M3 tokens 21 us (26), 4 of up to 8,192 21 (25), 100
+// of 8,192 in BF16 533 (549), 64 of 8,192 in E4M3 187 (180).  Against 768: 8
+// of up to 8,192 22 us (27); against chunks of 2,048: 32 of up to 8,192 66 us
+// (76).
 constexpr uint64_t kRowsFill = 1024;
 constexpr uint64_t kRowsEven = 3328;
 constexpr uint64_t kRowsLong = 1024;
 // Waves that sz_attn_tiles wants: two a SIMD.  With half, drafts of 16
-// sequences take 16.8 us instead of 15.7; with twice as many nothing changes.
+// sequences (5 tokens, window 1,000, two heads of 64) take 14.9 us instead of
+// 13.8; with twice as many nothing changes.
 constexpr uint64_t kTileWaves = 2048;
-constexpr uint32_t kMinChunk = 128;           // keys: a block for each wave, two tiles (256: drafts 16.7 us, not 15.7)
-// Chunks of a long context have 1,024 keys at least: 64K tokens take 29.7 us,
-// with 512 keys 32.2.
+// Keys of a chunk at least: a block for each wave, two tiles.  With 256 those
+// drafts take 14.5 us instead of 13.8; 47 sequences of up to 217 tokens, which
+// are then hardly cut, 10.5 instead of 12.9.
+constexpr uint32_t kMinChunk = 128;
+// Chunks of a long context have 1,024 keys at least: 64K tokens take 28.4 us,
+// with 512 keys 30.6.
 constexpr uint32_t kMaxLeast = 1024;
 constexpr uint64_t kArrivals = SZ_ATTENTION_COUNTERS / 4;      // counters at the workspace's start
 constexpr uint64_t kJoinChunks = 64;
 // Up to so many chunks of a sequence's head, and workgroups in all, are joined
-// by the workgroup that ends last, which saves a launch: 4 sequences of up to
-// 2,001 tokens 12 us (15), 47 of up to 217 12.5 (14), 1 of 4,001 13 (15).  With
-// more workgroups their writes past the L2 cost more than the launch (64 of up
-// to 8,192 tokens, six chunks each: 127 us for 125), with more chunks the one
-// workgroup reads them for longer (64K tokens, 64 chunks: 36 us for 30).
+// by the workgroup that ends last, which saves a launch: 1 sequence of 1,001
+// tokens 8.8 us (11.8), 1 of 2,001 9.7 (11.0), 4 of up to 2,001 10.8 (12.5), 47
+// of up to 217 12.9 (13.5).  The limits are on the high side, and do not look at
+// rows: at 24 and 32 chunks the launch is the shorter way again (1 of 3,001 11.6
+// for 10.9, 1 of 4,001 12.7 for 11.7, 4 of up to 8,192 21.2 for 19.5), and by
+// far where the one workgroup has 32 rows to read (15 of up to 15,241, two heads
+// of eight, four tokens each, FP8: 59 us for 33).  With more workgroups their
+// writes past the L2 cost more than the launch (64 of up to 8,192 tokens, six
+// chunks each: 121 us for 119), with more chunks the one workgroup reads them
+// for longer (64K tokens, 64 chunks: 34 us for 28).
 constexpr uint32_t kFusedSplits = 32;
 constexpr uint64_t kFusedGroups = 1024;
 static_assert(kFusedGroups <= kArrivals);
@@ -1341,10 +1356,11 @@ uint64_t rows_wanted(uint64_t span, uint64_t groups)
 }
 // A chunk's partials cost their way out and back, rows D 8 bytes; its keys are
 // the time that the others do not take.  span / n + rows D n / kPartialKeys is
-// least at n = sqrt(kPartialKeys span / (rows D)).  512 tokens by themselves
-// then stay whole, 20 us (26 in four chunks), 700 take 24.5 (29.7); with half
-// of kPartialKeys 64 tokens in each of 8 sequences of up to 1,064 take 33.5 us
-// (31), with a quarter 64 tokens behind 16,384 take 55.6 (48.3).
+// least at n = sqrt(kPartialKeys span / (rows D)).  BF16, 8 KV heads of 128,
+// four query heads each: 512 tokens by themselves then stay whole, 17 us (23
+// with 16 times kPartialKeys), 700 take 20 (26); with a quarter 64 tokens
+// behind 16,384 take 46 us (41), and with two query heads 64 tokens in each of
+// 8 sequences of up to 1,064 27.8 (25.7; with half 24.1).
 constexpr double kPartialKeys = 12500;
 uint64_t tiles_wanted(uint64_t span, uint64_t groups, uint32_t waves, uint64_t values)
 {
@@ -1370,22 +1386,27 @@ uint64_t most_splits(uint64_t span, uint64_t want)
 }
 
 // Waves of sz_attn_tiles, 32 rows each.  Eight share one conversion of each
-// FP8 tile where four need two: 606 against 635 us for 2,048 tokens over
-// 16,384, where the rows still fill the card.  BF16 tiles need none, and eight
-// waves at one barrier measured slower (408 against 400 us for six prompts).
+// FP8 tile where four need two: 541 against 557 us for 2,048 E5M2 tokens over
+// 16,384 (E4M3 543 and 561), where the rows still fill the card; six E5M2
+// prompts of up to 4,096 take 390 and 386.  BF16 tiles need no conversion, and
+// eight waves at one barrier are slower (391 against 381 us for six prompts).
 uint32_t tile_waves(uint32_t dtype, const PagedBatch &b, uint32_t kv_heads, uint32_t group)
 {
     const uint64_t rows = (uint64_t)b.tokens * group;
     return dtype != SZ_BF16 && rows >= 256ull * b.seqs && rows * kv_heads >= 256ull * kTileWaves / 8 ? 8 : 4;
 }
 
-// Whether sz_attn_rows takes 17 to 32 rows, as two of its products.  FP8: 64
-// sequences of up to 4,000 tokens, 32 rows, 83 us where sz_attn_tiles takes
-// 136, 15 of up to 15,246, 26 rows, 49 (82); BF16 with D = 64: 72 (84).  With
-// BF16 and D = 128 its registers leave two waves a SIMD, and it is no faster:
-// 15 of up to 15,241, 32 rows, 76 us (77), 20 rows over 1,005 tokens 17 (16).
-// 33 to 64 rows in two such workgroups gained little or nothing (FP8 58 for
-// 65 us and 38 for 38, BF16 90 for 60).
+// Whether sz_attn_rows takes 17 to 32 rows, as two of its products.  8 KV
+// heads, FP8: 64 sequences of up to 4,000 tokens, 32 rows, 79 us where
+// sz_attn_tiles takes 119, 15 of up to 15,246, 26 rows, 69 (129), with 4 heads
+// 60 (74); BF16 with D = 64, 64 of up to 4,000: 73 (80).  Where chunks are
+// joined in the launch (kFusedGroups) it is slower: 15 of up to 15,241 of two
+// heads, 32 rows, FP8 59 us (43; 33 if a launch joins them), BF16 with D = 64
+// 34 (29; 25).  With BF16 and D = 128 its registers leave two waves a SIMD: 15
+// of up to 15,241, 32 rows, 8 heads 112 us (135), but 4 heads 88 (71) and 2
+// heads 72 (39), and 20 rows over 1,005 tokens 14 (13).  33 to 64 rows in two
+// such workgroups gained little or nothing (FP8 58 for 65 us and 38 for 38,
+// BF16 90 for 60).
 constexpr bool row_pairs(uint32_t dtype, uint32_t head_dim) { return dtype != SZ_BF16 || head_dim == 64; }
 
 AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint32_t window)
@@ -1410,8 +1431,9 @@ AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint3
     if (p.rows) split_keys(span, rows_wanted(span, groups), p.rows_chunk, p.rows_splits);
     if (p.tiles) {
         // With a window a tile of rows sees less than its sequence's tokens
-        // together: no chunks where that would not be split (a window of 14
-        // over 488 new tokens 24 us in chunks, 14 without).
+        // together: no chunks where that would not be split (488 new tokens
+        // with a window of 14: one KV head of eight 15 us in chunks, 11
+        // without; behind 3,000, four heads of four, 17 and 11).
         const uint64_t tiles = (uint64_t)p.slots * c->kv_heads, tokens = 32 * p.tile_waves / group + 2;
         const uint64_t seen = window ? std::min(span, window + tokens + kTileKeys) : span;
         const bool split = tiles_wanted(seen, tiles, p.tile_waves, values) > 1;

@@ -41,8 +41,6 @@ struct Sequence {
 constexpr uint32_t kMinPage = 16, kMaxPage = 1024;
 constexpr uint32_t kMaxHeads = 1024;
 
-inline uint32_t elem_bytes(uint32_t dtype) { return dtype == SZ_BF16 ? 2u : 1u; }
-
 // Host checks of a cache and a batch (no device memory is touched).
 inline int check_paged(const sz_cache *c, const sz_batch *b, const int32_t *d_status, PagedCache &pc, PagedBatch &pb)
 {
