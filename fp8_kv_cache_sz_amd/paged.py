@@ -191,6 +191,31 @@ def _plain(name, t):
         raise ValueError("%s has a tangent, and the paged cache has none to give" % name)
 
 
+def _rows_meet(a, b, tokens, heads, dim):
+    """Whether rows of two [tokens, heads, dim] tensors of 2-byte values, as
+    _rows gives them, share memory.  Tensors that interleave (K and V of one
+    tensor) have the same strides: then a row of one meets a row of the other
+    where some (tokens, heads) apart is less than a row from their distance.
+    Tensors that overlap with other strides are taken to."""
+    (at, token, head), (bt, *strides) = a, b
+    size = lambda token, head: 2 * ((tokens - 1) * token + (heads - 1) * head + dim)
+    if at + size(token, head) <= bt or bt + size(*strides) <= at:
+        return False
+    token, head = token if tokens > 1 else 0, head if heads > 1 else 0
+    if [token, head] != [strides[0] if tokens > 1 else 0, strides[1] if heads > 1 else 0]:
+        return True
+    apart = (bt - at) // 2
+    block = (heads - 1) * head + dim                            # a token's rows
+    if token and block <= apart % token <= token - block:       # side by side: K and V of [tokens, 2, heads, dim]
+        return False
+    for h in range(1 - heads, heads):
+        rest = apart - h * head
+        t = 0 if token == 0 else max(1 - tokens, min(tokens - 1, rest // token))
+        if abs(rest - t * token) < dim or (t + 1 < tokens and abs(rest - (t + 1) * token) < dim):
+            return True
+    return False
+
+
 def _run(name, call, cache, batch, args, stream, owned=(), status=None):
     """Launches a call on `stream` (None: the current one) with the cache's
     device current, reporting into `status` (None: the cache's word).  Memory
@@ -281,6 +306,8 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
                 raise ValueError("out has rows that share memory")
         if tokens and args[0] == args[3]:
             raise ValueError("out's two tensors are one")
+        if tokens and _rows_meet(args[:3], args[3:], tokens, heads, dim):
+            raise ValueError("out's two tensors share memory")
     _run("sz_cache_read", _native.lib.sz_cache_read, cache, batch, args, stream, owned)
     if check:
         _raise_status(cache, stream)

@@ -86,3 +86,33 @@ def test_tensors_that_autograd_follows_are_refused():
         sz.PagedCache(sz.BF16, leaf)
     with torch.no_grad():
         sz.PagedCache(sz.BF16, leaf)
+
+
+def test_outputs_that_meet_are_refused():
+    """cache_read's two outputs: every pair of placements of two small tensors
+    in one memory, against their values one by one."""
+    from fp8_kv_cache_sz_amd.paged import _rows_meet
+    dim = 64
+    for tokens, heads in ((1, 1), (1, 3), (3, 1), (3, 2), (4, 3)):
+        for token, head in ((heads * dim, dim), (dim, tokens * dim), (2 * heads * dim, dim), (heads * 2 * dim, 2 * dim),
+                            (dim, 2 * tokens * dim), (heads * dim + 8, dim)):
+            own = {t * token + h * head + d for t in range(tokens) for h in range(heads) for d in range(dim)}
+            for apart in range(-1600, 1601, 8):
+                other = {x + apart for x in own}
+                want = bool(own & other)
+                assert _rows_meet((0, token, head), (2 * apart, token, head), tokens, heads, dim) == want, \
+                    (tokens, heads, token, head, apart)
+    import fp8_kv_cache_sz_amd as sz
+    cache, batch = objects()
+    store = torch.zeros(2000, dtype=torch.bfloat16)
+    view = lambda at, token, head: store.as_strided((2, 2, 64), (token, head, 1), at)
+    for a, b in ((view(0, 128, 64), view(64, 128, 64)), (view(0, 128, 64), view(128, 64, 128)),
+                 (view(0, 256, 64), view(136, 256, 64))):
+        for out in ((a, b), (b, a)):
+            with pytest.raises(ValueError, match="share memory"):
+                sz.cache_read(cache, batch, out=out, check=False)
+    for a, b in ((view(0, 128, 64), view(256, 128, 64)), (view(0, 256, 64), view(128, 256, 64)),
+                 (view(0, 256, 128), view(64, 256, 128)), (view(0, 128, 64), view(256, 64, 128))):
+        for out in ((a, b), (b, a)):
+            with pytest.raises(ValueError, match="run on the GPU"):
+                sz.cache_read(cache, batch, out=out, check=False)
