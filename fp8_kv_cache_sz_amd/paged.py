@@ -89,14 +89,13 @@ class PagedCache(_Fixed):
             status = torch.zeros(1, dtype=torch.int32, device=data.device)
         elif status.dtype != torch.int32 or status.numel() != 1 or status.device != data.device:
             raise ValueError("status is one int32 on the cache's device")
-        self.dtype, self.data, self.scales, self.status = dtype, data, scales, status
-        self.device = data.device
-        self._index = data.get_device()                 # -1: not on a GPU
-        self.pages, _, self.kv_heads, self.page_tokens, self.head_dim = data.shape
-        c = _native.sz_cache(dtype, self.page_tokens, self.kv_heads, self.head_dim, self.pages, data.data_ptr(),
+        pages, _, kv_heads, page_tokens, head_dim = data.shape
+        c = _native.sz_cache(dtype, page_tokens, kv_heads, head_dim, pages, data.data_ptr(),
                              scales.data_ptr() if scales is not None else None)
-        self._c, self._ref, self._status = c, ctypes.byref(c), status.data_ptr()
-        self._made = True
+        self.__dict__.update(                           # _index -1: not on a GPU
+            dtype=dtype, data=data, scales=scales, status=status, device=data.device, _index=data.get_device(),
+            pages=pages, kv_heads=kv_heads, page_tokens=page_tokens, head_dim=head_dim, _c=c, _ref=ctypes.byref(c),
+            _status=status.data_ptr(), _made=True)
 
     def raise_status(self) -> None:
         """Waits for the current stream, raises if a call found its batch
@@ -145,13 +144,10 @@ class PageBatch(_Fixed):
                 raise ValueError("page_table, kv_lens and starts are on different devices")
         if tokens < 0 or (max_new is not None and max_new < 0) or (max_kv is not None and max_kv < 0):
             raise ValueError("tokens, max_new and max_kv count from 0")
-        self.page_table, self.kv_lens, self.starts = page_table, kv_lens, starts
-        self.device, self.seqs, self.width, self.tokens = page_table.device, seqs, width, tokens
-        self._index = page_table.get_device()
-        self.max_new = tokens if max_new is None else max_new
-        self.max_kv = max_kv
-        self._by_page = {}
-        self._made = True
+        self.__dict__.update(
+            page_table=page_table, kv_lens=kv_lens, starts=starts, device=page_table.device, seqs=seqs, width=width,
+            tokens=tokens, _index=page_table.get_device(), max_new=tokens if max_new is None else max_new,
+            max_kv=max_kv, _by_page={}, _made=True)
 
     def _ref(self, page_tokens: int):
         """The sz_batch for caches of this page size (max_kv defaults to a
