@@ -34,7 +34,9 @@ __all__ = ["BF16", "E5M2", "TOP16", "TOP8", "TOP15S", "Codebook", "SplitZipError
            "reference_join", "profile_enable",
            "profile_collect",
            "E4M3", "PagedCache", "PageBatch", "paged_cache", "cache_write", "cache_read", "cache_check",
-           "paged_attention", "attention_workspace"]
+           "paged_attention", "attention_workspace",
+           "PagePool", "page_pool", "pages_assign", "assign_workspace", "draft_tree", "tree_words", "tree_attention", "Rotary",
+           "rotary_frequencies", "rotary_write", "CacheLayers", "cache_keep"]
 
 # An sz_codebook in device memory: u32 dtype, 16 exponent bytes (20 bytes,
 # padded to 32 so that the tensor size keeps 16-byte multiples).
@@ -354,3 +356,5 @@ def profile_collect() -> dict:
 
 from .paged import (E4M3, PageBatch, PagedCache, attention_workspace, cache_check, cache_read,  # noqa: E402
                     cache_write, paged_attention, paged_cache)
+from .step import (CacheLayers, PagePool, Rotary, assign_workspace, cache_keep, draft_tree, page_pool,  # noqa: E402
+                   pages_assign, rotary_frequencies, rotary_write, tree_attention, tree_words)

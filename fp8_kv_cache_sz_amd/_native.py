@@ -57,6 +57,19 @@ class sz_batch(ctypes.Structure):
                 ("max_new", ctypes.c_uint32), ("max_kv", ctypes.c_uint32)]
 
 
+class sz_pool(ctypes.Structure):
+    _fields_ = [("page_tokens", ctypes.c_uint32), ("pages", ctypes.c_uint32), ("queue", ctypes.c_void_p),
+                ("ends", ctypes.c_void_p)]
+
+
+class sz_rotary(ctypes.Structure):
+    _fields_ = [("d_turns", ctypes.c_void_p), ("dim", ctypes.c_uint32), ("interleaved", ctypes.c_uint32),
+                ("amplitude", ctypes.c_double)]
+
+
+SZ_TREE_WORDS = 16
+SZ_KEEP_LAYERS = 4096
+
 _u64, _i32, _vp = ctypes.c_uint64, ctypes.c_int, ctypes.c_void_p
 _u32, _f32 = ctypes.c_uint32, ctypes.c_float
 _cache_p, _batch_p = ctypes.POINTER(sz_cache), ctypes.POINTER(sz_batch)
@@ -121,6 +134,20 @@ lib.sz_paged_attention_workspace_size.restype = _u64
 lib.sz_paged_attention.argtypes = [_cache_p, _batch_p, _vp, _u32, _u64, _u64, _f32, _u32, _vp, _vp, _vp, _u64, _vp,
                                    _vp]
 lib.sz_paged_attention.restype = _i32
+lib.sz_pages_assign_workspace_size.argtypes = [_batch_p]
+lib.sz_pages_assign_workspace_size.restype = _u64
+lib.sz_pages_assign.argtypes = [ctypes.POINTER(sz_pool), _batch_p, _vp, _vp, _vp, _vp, _vp, _u64, _vp, _vp]
+lib.sz_pages_assign.restype = _i32
+lib.sz_draft_tree.argtypes = [_batch_p, _vp, _vp, _u32, _vp, _vp, _vp]
+lib.sz_draft_tree.restype = _i32
+lib.sz_tree_attention.argtypes = [_cache_p, _batch_p, _vp, _u32, _vp, _u32, _u64, _u64, _f32, _u32, _vp, _vp, _vp, _u64,
+                                  _vp, _vp]
+lib.sz_tree_attention.restype = _i32
+lib.sz_rotary_write.argtypes = [_cache_p, _batch_p, ctypes.POINTER(sz_rotary), _vp, _vp, _u32, _u64, _u64, _vp, _u64, _u64,
+                                _vp, _u64, _u64, _vp, _u64, _u64, _vp, _vp]
+lib.sz_rotary_write.restype = _i32
+lib.sz_cache_keep.argtypes = [_cache_p, _u32, _batch_p, _vp, _u32, _vp, _vp, _vp]
+lib.sz_cache_keep.restype = _i32
 
 EXPORTS = ("sz_calibrate", "sz_encoded_size", "sz_workspace_size", "sz_workspace_size_format",
            "sz_decode_workspace_size", "sz_encode", "sz_encode_devcb",
@@ -129,7 +156,9 @@ EXPORTS = ("sz_calibrate", "sz_encoded_size", "sz_workspace_size", "sz_workspace
            "sz_transfer", "sz_profile_enable", "sz_profile_collect", "sz_reference_copy",
            "sz_reference_split", "sz_reference_join", "sz_decode_noalloc_max_elems", "sz_decode_noalloc",
            "sz_cache_write", "sz_cache_read", "sz_cache_check_workspace_size", "sz_cache_check",
-           "sz_paged_attention_workspace_size", "sz_paged_attention")
+           "sz_paged_attention_workspace_size", "sz_paged_attention",
+           "sz_pages_assign_workspace_size", "sz_pages_assign", "sz_draft_tree", "sz_tree_attention",
+           "sz_rotary_write", "sz_cache_keep")
 
 SZ_FORMAT_TOP16 = 1
 SZ_FORMAT_TOP8 = 2
@@ -234,6 +263,10 @@ def sz_cache_check_workspace_size(cache) -> int:
 
 def sz_paged_attention_workspace_size(cache, batch, q_heads) -> int:
     return int(lib.sz_paged_attention_workspace_size(cache, batch, q_heads))
+
+
+def sz_pages_assign_workspace_size(batch) -> int:
+    return int(lib.sz_pages_assign_workspace_size(batch))
 
 
 def sz_reference_copy(d_src, d_dst, nbytes, stream) -> int:

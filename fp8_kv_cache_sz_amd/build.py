@@ -7,7 +7,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", name) for name in
-           ("encode.hip", "decode.hip", "calibrate.hip", "runtime.hip", "transfer.hip", "cache.hip", "attention.hip")]
+           ("encode.hip", "decode.hip", "calibrate.hip", "runtime.hip", "transfer.hip", "cache.hip", "attention.hip",
+            "rotary.hip", "tree.hip", "pool.hip")]
 HEADERS = [os.path.join(ROOT, "include", "splitzip.h"), os.path.join(HERE, "csrc", "common.hpp"),
            os.path.join(HERE, "csrc", "paged.hpp"), os.path.join(HERE, "csrc", "keys.hpp")]
 LIBRARY = os.path.join(HERE, "libsplitzip.so")

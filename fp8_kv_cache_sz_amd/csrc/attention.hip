@@ -69,6 +69,8 @@ struct AttnArgs {
     uint32_t rows_limit;      // sequences of up to so many rows are sz_attn_rows's
     uint32_t rows_chunk, rows_splits;      // keys of a chunk, chunks (sz_attn_rows)
     uint32_t tile_chunk, tile_splits;      // (sz_attn_tiles)
+    const uint64_t *masks;    // trees: [tokens][words], the new tokens that a token sees
+    uint32_t words;
 };
 
 // First key of sequence s that any of its new tokens sees, rounded down.
@@ -82,6 +84,45 @@ __device__ __forceinline__ void visible(int32_t p, int32_t window, int32_t &lo, 
 {
     hi = p;
     lo = first_seen(p, window);
+}
+
+// What a token of a tree sees: of the cached keys, which end before `past` =
+// len - n, those from lo on, and of the new ones those that its mask names.
+// Bits of new tokens that have no place are not looked at, nor is the mask of
+// a token without one (p < 0).
+struct Sight {
+    int32_t lo;
+    bool blind;               // sees nothing
+};
+// Bits 0..63: new tokens from..from + 63 that token tok of sequence s sees.
+__device__ __forceinline__ uint64_t new_seen(const AttnArgs &a, const Sequence &s, int32_t tok, int32_t from)
+{
+    const int32_t past = s.len - s.n, none = max(0, -past);          // the first new token with a place
+    if (tok < none || from >= s.n || from + 63 < none) return 0;
+    const uint64_t *row = a.masks + (uint64_t)(s.start + tok) * a.words;
+    const int32_t w = from >> 6, shift = from & 63;                  // w = -1: before the first
+    uint64_t bits = w >= 0 ? row[w] >> shift : 0;
+    if (shift && w + 1 < (int32_t)a.words) bits |= row[w + 1] << (64 - shift);
+    if (from < none) bits &= ~0ull << (none - from);
+    if (s.n - from < 64) bits &= ~(~0ull << (s.n - from));
+    return bits;
+}
+__device__ __forceinline__ Sight tree_sight(const AttnArgs &a, const Sequence &s, int32_t tok)
+{
+    int32_t count = 0;
+    for (int32_t from = 0; from < s.n; from += 64) count += (int32_t)__popcll(new_seen(a, s, tok, from));
+    const int32_t past = s.len - s.n;
+    Sight v;
+    v.lo = first_seen(past + max(count, 1) - 1, a.window);
+    v.blind = count == 0 && v.lo >= past;
+    return v;
+}
+// Bits 0..63: keys kb..kb + 63 that are cached before the new ones and seen.
+__device__ __forceinline__ uint64_t old_seen(int32_t lo, int32_t past, int32_t kb)
+{
+    const int32_t first = max(lo - kb, 0), end = min(past - kb, 64);
+    if (first >= end) return 0;
+    return (~0ull >> (64 - (end - first))) << first;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -157,7 +198,12 @@ __device__ __forceinline__ uint32_t finite(uint32_t w)
 {
     return w & ~(((not_finite(w) & kNotFinite) >> 15) * 0xFFFFu);
 }
-// 1.0 in the halves of a pair of keys that [lo, hi] holds
+// 1.0 in the halves of a pair of keys that bits 0 and 1 say
+__device__ __forceinline__ uint32_t seen_pair(uint64_t bits)
+{
+    return (bits & 1 ? 0x3F80u : 0u) | (bits & 2 ? 0x3F800000u : 0u);
+}
+// ... that [lo, hi] holds
 __device__ __forceinline__ uint32_t seen_pair(int32_t key, int32_t lo, int32_t hi)
 {
     return (key >= lo && key <= hi ? 0x3F80u : 0u) | (key + 1 >= lo && key + 1 <= hi ? 0x3F800000u : 0u);
@@ -250,9 +296,17 @@ struct Joined {
 };
 
 // The visible chunks [s0, s1) of a token at position p.
+// (Of a tree's: those from its first cached key, or the first new one, on.)
+template <bool TREE>
 __device__ __forceinline__ void chunk_range(const Sequence &s, int32_t p, int32_t window, uint32_t chunk, uint32_t &s0,
-                                            uint32_t &s1)
+                                            uint32_t &s1, int32_t tree_lo)
 {
+    if constexpr (TREE) {
+        const int32_t first = first_key(s, window);
+        s0 = s.len == 0 ? 0 : (uint32_t)(min(tree_lo, max(s.len - s.n, 0)) - first) / chunk;
+        s1 = s.len == 0 ? 0 : (uint32_t)(s.len - 1 - first) / chunk + 1;
+        return;
+    }
     int32_t lo, hi;
     visible(p, window, lo, hi);
     const int32_t first = first_key(s, window);
@@ -361,7 +415,7 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, uint32_t head, co
     }
 }
 
-template <int DT, int D, int NB>
+template <int DT, int D, int NB, bool TREE>
 __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void sz_attn_rows(AttnArgs a)
 {
     constexpr uint32_t ROWS = 16 * NB;
@@ -370,6 +424,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     __shared__ float lds_o[WAVES][ROWS][D + 4];
     __shared__ float2 lds_ml[WAVES][ROWS];
     __shared__ uint32_t lds_last;
+    __shared__ int32_t lds_lo[TREE ? ROWS : 1];     // of a row of a tree: its first cached key, INT32_MIN if it sees none at all
 
     const uint32_t head = blockIdx.x % a.c.heads;
     const uint32_t seq = blockIdx.x / a.c.heads % a.b.seqs;
@@ -388,12 +443,21 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     const uint32_t lane = lane_id(), wave = uniform(threadIdx.x / 64);
     const uint32_t n = lane % 16, g = lane / 16;
     // Row 16 b + n; one that is not there computes what the last one does.
+    const int32_t past = s.len - s.n;
     int32_t lo[NB], hi[NB];
+    uint32_t named[NB];                             // trees: the new tokens that the row sees, 32 at most
     bf16x8 q[NB][D / 32];                           // the products' second operand, in K's order of d
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const uint32_t r = min(16 * b + n, rows - 1), tok = r / a.group;
-        visible(s.len - s.n + (int32_t)tok, a.window, lo[b], hi[b]);
+        if constexpr (TREE) {
+            const Sight v = tree_sight(a, s, (int32_t)tok);
+            named[b] = (uint32_t)new_seen(a, s, (int32_t)tok, 0);
+            lo[b] = v.lo;
+            if (threadIdx.x < 16) lds_lo[16 * b + n] = v.blind ? INT32_MIN : v.lo;
+        } else {
+            visible(past + (int32_t)tok, a.window, lo[b], hi[b]);
+        }
         const uint16_t *p = a.q + (uint64_t)(s.start + tok) * a.q_token + (uint64_t)(head * a.group + r % a.group) * a.q_head;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
@@ -414,7 +478,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     bool far = false;
 
     const int32_t all_lo = first_seen(s.len - 1, a.window);                  // every row sees [all_lo, all_hi]
-    const int32_t all_hi = s.len - s.n;
+    const int32_t all_hi = TREE ? past - 1 : past;
 
     constexpr int32_t STEP = 32 * WAVES;
     int32_t kb = begin + 32 * (int32_t)wave;
@@ -514,15 +578,25 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
         // times a NaN is one.  NaN and infinities in the others are counted
         // further down.
         bool wild = false;
+        uint32_t sees[NB];                           // trees: bit j, key kb + 4 g + j
         if constexpr (MASKED) {
             uint32_t found = 0;
-            const int32_t any_lo = first_seen(all_hi, a.window);
+            const int32_t any_lo = first_seen(past, a.window);
+            if constexpr (TREE)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int32_t new0 = past - kb;  // the first new token's bit
+                    const uint64_t bits = old_seen(lo[b], past, kb) |
+                                          (new0 >= 32 || new0 <= -32 ? 0 : new0 >= 0 ? (uint64_t)named[b] << new0 : (uint64_t)named[b] >> -new0);
+                    sees[b] = (uint32_t)bits >> (4 * g);
+                }
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 const int32_t key = kb + 16 * (r / 4) + 4 * (int32_t)g + r % 4;
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    if (key < lo[b] || key > hi[b]) st[b][r / 4][r % 4] = kNone;
+                    if (TREE ? (sees[b] >> (16 * (r / 4) + r % 4) & 1) == 0 : key < lo[b] || key > hi[b])
+                        st[b][r / 4][r % 4] = kNone;
                 const bool dead = key < any_lo || key >= s.len;
 #pragma unroll
                 for (int e = 0; e < VD / 2; ++e) {
@@ -591,8 +665,10 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
             u32x4 sw[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-                sw[b] = u32x4{seen_pair(key, lo[b], hi[b]), seen_pair(key + 2, lo[b], hi[b]),
-                              seen_pair(key + 16, lo[b], hi[b]), seen_pair(key + 18, lo[b], hi[b])};
+                sw[b] = TREE ? u32x4{seen_pair(sees[b]), seen_pair(sees[b] >> 2), seen_pair(sees[b] >> 16),
+                                     seen_pair(sees[b] >> 18)}
+                             : u32x4{seen_pair(key, lo[b], hi[b]), seen_pair(key + 2, lo[b], hi[b]),
+                                     seen_pair(key + 16, lo[b], hi[b]), seen_pair(key + 18, lo[b], hi[b])};
             uint32_t even = 0x05040100u;
             asm volatile("" : "+s"(even));       // these permutes are not shared with the ones below, which would
 #pragma unroll                                   // keep all of them in registers
@@ -682,7 +758,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
             for (int j = 0; j < VD; ++j) acc[j] += lds_o[w][row][d + j] * f;
         }
         const uint32_t rtok = row / a.group, rhead = head * a.group + row % a.group;
-        const bool empty = s.len - s.n + (int32_t)rtok < 0;
+        const bool empty = TREE ? lds_lo[row] == INT32_MIN : past + (int32_t)rtok < 0;
         store_row<D, VD>(a, whole, split, s.start + rtok, rhead, d, acc, empty ? 0.f : 1.f / sum);
         if (d == 0) store_stats(a, whole, split, s.start + rtok, rhead, empty, top, sum);
     }
@@ -707,11 +783,12 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     for (uint32_t r0 = 0; r0 < rows; r0 += GROUPS / parts) {
         const uint32_t r = r0 + lanes_group / parts;
         const uint32_t jtok = r / a.group, jhead = head * a.group + r % a.group;
-        const int32_t jpos = s.len - s.n + (int32_t)jtok;
+        const int32_t jpos = past + (int32_t)jtok, jlo = TREE ? lds_lo[min(r, rows - 1)] : 0;
+        const bool empty = TREE ? jlo == INT32_MIN : jpos < 0;
         Joined x;
-        if (r < rows) {
+        if (r < rows && !(TREE && empty)) {
             uint32_t s0, s1;
-            chunk_range(s, jpos, a.window, a.rows_chunk, s0, s1);
+            chunk_range<TREE>(s, jpos, a.window, a.rows_chunk, s0, s1, jlo);
             join_chunks<D, true>(a, (uint64_t)(s.start + jtok) * a.q_heads + jhead, s0, s1, part, parts, jlane, x);
         }
         __syncthreads();
@@ -721,8 +798,8 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
         if (r < rows && part == 0) {
             for (uint32_t k = 1; k < parts; ++k) x.add(meet_ml[lanes_group + k], meet_o[lanes_group + k][jlane], a.c2);
             const float w[4] = {x.o.x, x.o.y, x.o.z, x.o.w};
-            store_row<D, 4>(a, true, 0, s.start + jtok, jhead, jlane * 4, w, jpos < 0 ? 0.f : 1.f / x.l);
-            if (jlane == 0) store_stats(a, true, 0, s.start + jtok, jhead, jpos < 0, x.m, x.l);
+            store_row<D, 4>(a, true, 0, s.start + jtok, jhead, jlane * 4, w, empty ? 0.f : 1.f / x.l);
+            if (jlane == 0) store_stats(a, true, 0, s.start + jtok, jhead, empty, x.m, x.l);
         }
     }
 }
@@ -783,20 +860,30 @@ typedef __attribute__((address_space(3))) uint16_t *LdsPtr;
 template <int D, int KV, int WAVES>
 struct FetchBf16 {
     static constexpr uint32_t ROWS = kTileKeys / WAVES, PIECES = D / 8, RPI = 64 / PIECES, PARTS = ROWS / RPI;
+#ifdef __HIP_DEVICE_COMPILE__        // the host pass does not know the type, and drops the kernel's second instance over it
     __amdgpu_buffer_rsrc_t rows;
+#endif
     __device__ __forceinline__ FetchBf16(const AttnArgs &a, uint32_t head, uint32_t page, int32_t key0)
     {
         const uint32_t row0 = (uint32_t)key0 & ((1u << a.c.lg_page) - 1);
         uint16_t *p = reinterpret_cast<uint16_t *>(a.c.data) + row_index(a.c, page, KV, head, row0) * D;
+#ifdef __HIP_DEVICE_COMPILE__
         rows = __builtin_amdgcn_make_buffer_rsrc(p, 0, ROWS * D * 2, 0x00027000);
+#else
+        (void)p;
+#endif
     }
     __device__ __forceinline__ void part(uint32_t wave, uint32_t i, LdsPtr to) const
     {
         const uint32_t r = i * RPI + lane_id() / PIECES;
+#ifdef __HIP_DEVICE_COMPILE__
         typedef __attribute__((address_space(3))) void *lds_ptr;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rows, (lds_ptr)(to + (ROWS * wave + i * RPI) * D), 16,
             (r * D + 8 * ((lane_id() % PIECES) ^ tile_swizzle<D, KV>(ROWS * wave + r))) * 2, 0, 0, 0);
+#else
+        (void)r;
+#endif
     }
 };
 
@@ -881,7 +968,7 @@ __device__ __forceinline__ bf16x8 v_operand(LdsPtr v, uint32_t place, uint32_t b
     return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <int DT, int D, int WAVES>
+template <int DT, int D, int WAVES, bool TREE>
 __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint32_t slots)
 {
     constexpr int DB = D / 32;
@@ -919,15 +1006,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
     const bool mine = wave * 32 + n < rows;
     const int32_t tok = (int32_t)(my_row / a.group);
     const uint32_t q_head = head * a.group + (uint32_t)(my_row % a.group);
-    const int32_t pos = s.len - s.n + tok;
+    const int32_t past = s.len - s.n, pos = past + tok;
     int32_t lo, hi;
-    visible(pos, a.window, lo, hi);
+    bool empty = pos < 0;
+    if constexpr (TREE) {
+        const Sight v = tree_sight(a, s, tok);
+        lo = v.lo;
+        empty = v.blind;
+    } else {
+        visible(pos, a.window, lo, hi);
+    }
 
-    // the keys of this tile of rows, and of its chunk
-    const int32_t p_first = s.len - s.n + tok_first, p_last = s.len - s.n + tok_last;
+    // the keys of this tile of rows, and of its chunk: every row sees the ones up to p_first, none one behind p_last
+    const int32_t p_first = TREE ? past - 1 : past + tok_first, p_last = TREE ? s.len - 1 : past + tok_last;
     const bool whole = a.tile_splits == 1 || chunks_of(s, a.window, a.tile_chunk) == 1;
     const int64_t chunk0 = (int64_t)first_key(s, a.window) + (int64_t)split * a.tile_chunk;
-    const int32_t any_lo = first_seen(p_first, a.window);                      // some row sees [any_lo, p_last]
+    const int32_t any_lo = first_seen(TREE ? past : p_first, a.window);        // some row may see [any_lo, p_last]
     const int32_t begin = (int32_t)max(chunk0, (int64_t)(any_lo & ~(int32_t)(kTileKeys - 1)));
     const int32_t end = (int32_t)min((int64_t)p_last + 1, chunk0 + a.tile_chunk);
     if (whole ? split > 0 : begin >= end) return;                              // no row's chunk: nobody reads it
@@ -981,6 +1075,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
         const int32_t kb = begin + (int32_t)(t * kTileKeys);
         return kb < all_lo || kb + (int32_t)kTileKeys - 1 > p_first;
     };
+    // Trees: the keys of the tile at kb that the lane's row sees, from its own first four on.
+    const auto tree_seen = [&](int32_t kb) SZ_INLINE {
+        return (old_seen(lo, past, kb) | new_seen(a, s, tok, kb - past)) >> (4 * g);
+    };
     // Hides tile t's scores and raises the running maximum.  The sums of the
     // tile before are not in o yet when it rises: o is scaled after them.
     float late = 1.f;
@@ -990,12 +1088,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
         float top = top0;
         if (masked(t)) {
             const int32_t kb = begin + (int32_t)(t * kTileKeys);
+            uint64_t sees = 0;
+            if constexpr (TREE) sees = tree_seen(kb);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int32_t k = kb + 32 * b + 8 * (r / 4) + 4 * (int32_t)g + r % 4;
-                    if (k < lo || k > hi) st[b][r] = kNone;
+                    const int32_t at = 32 * b + 8 * (r / 4) + r % 4, k = kb + at + 4 * (int32_t)g;
+                    if (TREE ? (sees >> at & 1) == 0 : k < lo || k > hi) st[b][r] = kNone;
                 }
             top = kNone;
 #pragma unroll
@@ -1066,8 +1166,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 const int32_t at = kb + 16 * k + 4 * (int32_t)g;
-                const u32x4 sw = {seen_pair(at, lo, hi), seen_pair(at + 2, lo, hi), seen_pair(at + 8, lo, hi),
-                                  seen_pair(at + 10, lo, hi)};
+                u32x4 sw;
+                if constexpr (TREE) {
+                    const uint64_t sees = tree_seen(kb) >> (16 * k);
+                    sw = u32x4{seen_pair(sees), seen_pair(sees >> 2), seen_pair(sees >> 8), seen_pair(sees >> 10)};
+                } else {
+                    sw = u32x4{seen_pair(at, lo, hi), seen_pair(at + 2, lo, hi), seen_pair(at + 8, lo, hi),
+                               seen_pair(at + 10, lo, hi)};
+                }
                 u32x4 w = __builtin_bit_cast(u32x4, v_operand<D>((LdsPtr)vt, v_at, 16 * k, j));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = kinds(w[e]);
@@ -1228,7 +1334,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
 
     l += __shfl_xor(l, 32, 64);
     if (!mine) return;
-    const bool empty = pos < 0;
     const float plain = exp2_fast(-ref.delta);                                 // to sums with m' itself as the reference
     l *= plain;
     const float inv = whole ? empty ? 0.f : plain / l : plain;
@@ -1254,7 +1359,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(AttnArgs a, uint3
 template <int D>
 constexpr uint32_t kJoinGroups = kAttnThreads / (D / 4);
 
-template <int D>
+template <int D, bool TREE>
 __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_t per_seq, uint32_t parts)
 {
     constexpr uint32_t LANES = D / 4, GROUPS = kJoinGroups<D>;
@@ -1279,7 +1384,9 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_
     if ((few ? a.rows_splits : a.tile_splits) == 1 || chunks_of(s, a.window, chunk) == 1) return;      // already whole
     const int32_t p = s.len - s.n + ((int32_t)t - s.start);
     uint32_t s0, s1;
-    chunk_range(s, p, a.window, chunk, s0, s1);
+    Sight v{0, p < 0};
+    if constexpr (TREE) v = tree_sight(a, s, (int32_t)t - s.start);
+    chunk_range<TREE>(s, p, a.window, chunk, s0, s1, v.lo);
     const uint32_t group = threadIdx.x / LANES, lane = threadIdx.x % LANES, part = group % parts;
     const uint32_t head = blockIdx.x % blocks * rows + group / parts;
     Joined x;
@@ -1293,8 +1400,8 @@ __global__ __launch_bounds__(kAttnThreads) void sz_attn_join(AttnArgs a, uint32_
     }
     if (head >= a.q_heads || part != 0) return;
     const float w[4] = {x.o.x, x.o.y, x.o.z, x.o.w};
-    store_row<D, 4>(a, true, 0, t, head, lane * 4, w, p < 0 ? 0.f : 1.f / x.l);
-    if (lane == 0) store_stats(a, true, 0, t, head, p < 0, x.m, x.l);
+    store_row<D, 4>(a, true, 0, t, head, lane * 4, w, v.blind ? 0.f : 1.f / x.l);
+    if (lane == 0) store_stats(a, true, 0, t, head, v.blind, x.m, x.l);
 }
 
 // ---------------------------------------------------------------------------
@@ -1477,31 +1584,37 @@ bool launchable(const PagedCache &c, const PagedBatch &b, const AttnPlan &p, con
            j.groups * kAttnThreads <= kMaxThreads;
 }
 
-template <int DT, int D>
-int launch_attention(const AttnArgs &a, const AttnPlan &p, const JoinPlan &j, hipStream_t s)
+template <int DT, int D, bool TREE>
+int launch_kernels(const AttnArgs &a, const AttnPlan &p, const JoinPlan &j, hipStream_t s)
 {
     if (p.rows) {
         const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits;
         LaunchScope scope("sz_attn_rows", s);
         if (p.rows_limit <= kRowsMax)
-            hipLaunchKernelGGL((sz_attn_rows<DT, D, 1>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+            hipLaunchKernelGGL((sz_attn_rows<DT, D, 1, TREE>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
         else if constexpr (row_pairs(DT, D))
-            hipLaunchKernelGGL((sz_attn_rows<DT, D, 2>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+            hipLaunchKernelGGL((sz_attn_rows<DT, D, 2, TREE>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
     }
     if (p.tiles) {
         const uint64_t groups = (uint64_t)a.c.heads * p.slots * p.tile_splits;
         LaunchScope scope("sz_attn_tiles", s);
         if (p.tile_waves == 4)
-            hipLaunchKernelGGL((sz_attn_tiles<DT, D, 4>), dim3((uint32_t)groups), dim3(256), 0, s, a, p.slots);
+            hipLaunchKernelGGL((sz_attn_tiles<DT, D, 4, TREE>), dim3((uint32_t)groups), dim3(256), 0, s, a, p.slots);
         else if constexpr (DT != SZ_BF16)
-            hipLaunchKernelGGL((sz_attn_tiles<DT, D, 8>), dim3((uint32_t)groups), dim3(512), 0, s, a, p.slots);
+            hipLaunchKernelGGL((sz_attn_tiles<DT, D, 8, TREE>), dim3((uint32_t)groups), dim3(512), 0, s, a, p.slots);
     }
     if (j.groups) {
         LaunchScope scope("sz_attn_join", s);
-        hipLaunchKernelGGL((sz_attn_join<D>), dim3((uint32_t)j.groups), dim3(kAttnThreads), 0, s, a, j.per_seq,
+        hipLaunchKernelGGL((sz_attn_join<D, TREE>), dim3((uint32_t)j.groups), dim3(kAttnThreads), 0, s, a, j.per_seq,
                            j.parts);
     }
     return hipGetLastError() == hipSuccess ? SZ_OK : SZ_E_HIP;
+}
+
+template <int DT, int D>
+int launch_attention(const AttnArgs &a, const AttnPlan &p, const JoinPlan &j, hipStream_t s)
+{
+    return a.masks == nullptr ? launch_kernels<DT, D, false>(a, p, j, s) : launch_kernels<DT, D, true>(a, p, j, s);
 }
 
 }  // namespace
@@ -1529,12 +1642,11 @@ extern "C" uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, con
     return attn_ws_bytes(splits, (uint64_t)b.tokens * q_heads, cache->head_dim);
 }
 
-extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void *d_q, uint32_t q_heads,
-                                  uint64_t q_token_stride, uint64_t q_head_stride, float scale, uint32_t window,
-                                  void *d_out, float *d_lse, void *d_ws, uint64_t ws_bytes, int32_t *d_status,
-                                  void *stream)
+// Both calls; masks: a tree's, with `a` zero but for them.
+static int attend(AttnArgs a, const sz_cache *cache, const sz_batch *batch, const void *d_q, uint32_t q_heads,
+                  uint64_t q_token_stride, uint64_t q_head_stride, float scale, uint32_t window, void *d_out, float *d_lse,
+                  void *d_ws, uint64_t ws_bytes, int32_t *d_status, void *stream)
 {
-    AttnArgs a{};
     int rc = check_paged(cache, batch, d_status, a.c, a.b);
     if (rc != SZ_OK) return rc;
     if (q_heads == 0 || q_heads > 0xFFFFu || q_heads % a.c.heads) return SZ_E_ARG;
@@ -1577,4 +1689,28 @@ extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, 
         return wide ? launch_attention<SZ_FP8_E5M2, 128>(a, p, j, s) : launch_attention<SZ_FP8_E5M2, 64>(a, p, j, s);
     default: return wide ? launch_attention<SZ_FP8_E4M3, 128>(a, p, j, s) : launch_attention<SZ_FP8_E4M3, 64>(a, p, j, s);
     }
+}
+
+extern "C" int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void *d_q, uint32_t q_heads,
+                                  uint64_t q_token_stride, uint64_t q_head_stride, float scale, uint32_t window,
+                                  void *d_out, float *d_lse, void *d_ws, uint64_t ws_bytes, int32_t *d_status,
+                                  void *stream)
+{
+    return attend(AttnArgs{}, cache, batch, d_q, q_heads, q_token_stride, q_head_stride, scale, window, d_out, d_lse, d_ws,
+                  ws_bytes, d_status, stream);
+}
+
+extern "C" int sz_tree_attention(const sz_cache *cache, const sz_batch *batch, const uint64_t *d_masks, uint32_t words,
+                                 const void *d_q, uint32_t q_heads, uint64_t q_token_stride, uint64_t q_head_stride,
+                                 float scale, uint32_t window, void *d_out, float *d_lse, void *d_ws, uint64_t ws_bytes,
+                                 int32_t *d_status, void *stream)
+{
+    if (!batch || words == 0 || words > SZ_TREE_WORDS || std::min(batch->max_new, batch->tokens) > 64ull * words) return SZ_E_ARG;
+    if (batch->tokens && batch->seqs && !d_masks) return SZ_E_ARG;
+    if (reinterpret_cast<uintptr_t>(d_masks) & 7u) return SZ_E_ALIGN;
+    AttnArgs a{};
+    a.masks = d_masks;
+    a.words = words;
+    return attend(a, cache, batch, d_q, q_heads, q_token_stride, q_head_stride, scale, window, d_out, d_lse, d_ws, ws_bytes,
+                  d_status, stream);
 }

@@ -23,69 +23,10 @@ namespace {
 constexpr uint32_t kMoveThreads = 256;
 constexpr uint32_t kMoveTokens = 16;     // of a wave: their places are found once
 
-// Lanes per row: each moves 8 values (16 bytes of BF16).
-template <int D>
-constexpr uint32_t kRowLanes = D / 8;
-
-// Maximum over the LANES (8 or 16) lanes of a row, DPP within 16 lanes:
-// quad_perm swaps of 1 and 2, then mirrors of 8 and 16.
-template <uint32_t LANES>
-__device__ __forceinline__ uint32_t row_max(uint32_t v)
-{
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
-    if (LANES == 16) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
-    return v;
-}
-
-template <int DT>
-__device__ __forceinline__ uint32_t fp8_pair(float lo, float hi, uint32_t into, bool high)
-{
-    if constexpr (DT == SZ_FP8_E4M3)
-        return high ? __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, into, true)
-                    : __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, into, false);
-    else
-        return high ? __builtin_amdgcn_cvt_pk_bf8_f32(lo, hi, into, true)
-                    : __builtin_amdgcn_cvt_pk_bf8_f32(lo, hi, into, false);
-}
-
 struct Rows {
     uint16_t *p[2];           // K and V: [tokens][heads][D]
     uint64_t token[2], head[2];
 };
-
-// One 16-byte chunk of a row, BF16 -> cache.
-template <int DT, int D>
-__device__ __forceinline__ void put_chunk(const PagedCache &c, uint64_t at, uint32_t off, uint4 v)
-{
-    if constexpr (DT == SZ_BF16) {
-        *reinterpret_cast<uint4 *>(c.data + (at * D + off) * 2) = v;
-    } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t a = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
-            a = max(a, lo < 0x7F80u ? lo : 0u);
-            a = max(a, hi < 0x7F80u ? hi : 0u);
-        }
-        a = row_max<kRowLanes<D>>(a);
-        // a = 1.m 2^(E-127): a <= 1.75 2^(EMAX+k) from k = E - 127 - EMAX, one more where 1.m > 1.75
-        constexpr int32_t EMAX = DT == SZ_FP8_E4M3 ? 8 : 15;
-        const int32_t byte = max(1, (int32_t)(a >> 7) - EMAX + ((a & 0x7Fu) > 0x60u ? 1 : 0));
-        const float inv = __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23);
-        uint32_t q[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float lo = __builtin_bit_cast(float, w[e] << 16) * inv;
-            const float hi = __builtin_bit_cast(float, w[e] & 0xFFFF0000u) * inv;
-            q[e / 2] = fp8_pair<DT>(lo, hi, q[e / 2], e % 2 == 1);
-        }
-        *reinterpret_cast<uint2 *>(c.data + at * D + off) = make_uint2(q[0], q[1]);
-        if (off == 0) c.scales[at] = (uint8_t)byte;
-    }
-}
 
 // A wave moves 16 tokens' rows of one (K or V, head) pair, WRITE: tensors ->
 // pages, else pages -> tensors.  Its lanes 0..15 find a token's place each; a
@@ -110,61 +51,17 @@ __global__ __launch_bounds__(kMoveThreads) void sz_cache_move(PagedCache c, Page
     if (t0 >= b.tokens) return;
     const uint32_t lane = lane_id();
 
-    // The place of token t0 + lane as a row of pair 0, or none.  Loads that
-    // wait for one another are most of a wave's time, so the starts and
-    // lengths of the 64 sequences from t0's on come in one (up to 63
-    // sequences: the first), and each token counts its own from there.
+    // The place of token t0 + lane as a row of pair 0, or none.
     constexpr uint64_t NONE = ~0ull;
     uint64_t mine = NONE;
-    uint32_t base = 0;
-    for (uint32_t span = b.seqs + 1; span > 64;) {
-        const uint32_t step = (span + 63) / 64, at = lane * step;
-        const uint32_t hits = (uint32_t)__popcll(__ballot(at < span && (int64_t)b.starts[base + min(at, span - 1)] <= t0));
-        const uint32_t skip = hits > 0 ? (hits - 1) * step : 0;
-        base += skip;
-        span = min(step, span - skip);
-    }
-    const bool there = base + lane < b.seqs;
-    const int32_t start = base + lane <= b.seqs ? b.starts[base + lane] : INT32_MAX;
-    const int32_t len = there ? b.lens[base + lane] : 0;
-    // What no token's own sequence shows: starts that descend, and (the first
-    // wave's) an axis that begins or ends outside [0, tokens].
-    const int32_t after = __shfl_down(start, 1, 64);
-    bool wrong = lane < 63 && there && after < start;
-    if (unit == 0 && lane < 2) {
-        const int32_t edge = b.starts[lane * b.seqs];
-        wrong |= edge < 0 || edge > (int32_t)b.tokens;
-    }
-    if (wrong) flag_batch(b);
-    uint32_t count = 0;                              // of the starts up to this lane's token
-#pragma unroll
-    for (uint32_t j = 0; j < kMoveTokens; ++j) {
-        const uint64_t passed = __ballot(start <= (int32_t)(t0 + j));
-        if (lane == j) count = (uint32_t)__popcll(passed);
-    }
-    const int32_t my_start = __shfl(start, (int)max(count, 1u) - 1, 64), my_next = __shfl(start, (int)min(count, 63u), 64);
-    const int32_t my_len = __shfl(len, (int)max(count, 1u) - 1, 64);
-    if (lane < kMoveTokens && t0 + lane < b.tokens && count > 0) {
-        const uint32_t t = t0 + lane;
-        uint32_t i = base + count - 1;
-        Sequence s{0, 0, 0};
-        if (count < 64) {
-            if (i < b.seqs) s = checked(b, my_start, my_next, my_len);
-        } else {                                     // 64 sequences on, or more
-            for (uint32_t past = b.seqs; past - i > 1;) {
-                const uint32_t mid = i + (past - i) / 2;
-                (b.starts[mid] <= (int32_t)t ? i : past) = mid;
-            }
-            if (i < b.seqs) s = sequence(b, i);
-        }
-        const int32_t pos = s.len - s.n + ((int32_t)t - s.start);
-        if ((int32_t)t >= s.start && (int32_t)t < s.start + s.n && pos >= 0) {
-            const uint32_t page = (uint32_t)b.table[(uint64_t)i * b.width + ((uint32_t)pos >> c.lg_page)];
-            if (page < c.pages)
-                mine = row_index(c, page, 0, 0, (uint32_t)pos & ((1u << c.lg_page) - 1));
-            else
-                flag_batch(b);
-        }
+    uint32_t i;
+    int32_t pos;
+    if (token_position<kMoveTokens>(b, t0, unit == 0, i, pos)) {
+        const uint32_t page = (uint32_t)b.table[(uint64_t)i * b.width + ((uint32_t)pos >> c.lg_page)];
+        if (page < c.pages)
+            mine = row_index(c, page, 0, 0, (uint32_t)pos & ((1u << c.lg_page) - 1));
+        else
+            flag_batch(b);
     }
     const uint32_t sub = lane / LPR, off = (lane % LPR) * 8;
     uint64_t place[PASSES];

@@ -1,0 +1,349 @@
+// Rotary positions on the way into the paged cache: new tokens' queries and
+// keys are turned by their positions, keys and values written into pages.
+//
+// Frequency f_i turns the pair (x, y) of a row, d = (i, i + R/2) ("half") or
+// (2i, 2i + 1) ("interleaved"), i < R/2, of a token at position p:
+//   x' = x c - y s,  y' = y c + x s,  c = A cos(p f_i),  s = A sin(p f_i)
+// and values from R on stay.
+//
+// The angle is taken modulo a turn before it is a floating number: the caller
+// gives f_i / 2 pi as a 64-bit fraction F_i of a turn, and p F_i wraps around
+// exactly as the angle does, off by at most p 2^-65 turns at any position
+// (2^-34 at 2^31), where 32-bit p f_i has lost a turn's 2^-7 at 2^17.  What is
+// left after the nearest quarter turn, at most pi/4, goes through the Taylor
+// series of sine and cosine, to the last bit of its type.
+//
+// Queries, and keys of BF16 caches, are computed in 32 bits.  Keys of FP8
+// caches in 64, rounded to 32: a row's scale depends on which side of a power
+// of two (times 1.75) its largest value is, and so should not depend on the
+// order of a kernel's roundings.
+//
+// A wave takes 4 (D = 64: 8) tokens and up to kHeads heads of q, k or v: the
+// sines are worked out once for the heads.  Bound by HBM in the large, by the
+// latency of four loads that wait for each other (starts, length, page, row)
+// in the small.
+#include "paged.hpp"
+
+#include <cmath>
+#include <type_traits>
+
+namespace sz {
+namespace {
+
+constexpr uint32_t kRotaryThreads = 256;
+constexpr uint32_t kHeads = 8;           // of a wave
+constexpr int kAhead = 4;                // rows that a lane has in flight
+
+struct RotaryArgs {
+    PagedCache c;
+    PagedBatch b;
+    const uint64_t *turns;    // [R / 2]
+    const int32_t *positions; // [tokens] or null: where the tokens stand
+    const uint16_t *q, *k, *v;
+    uint16_t *out;            // q's, turned
+    uint64_t q_token, q_head, out_token, out_head, k_token, k_head, v_token, v_head;
+    double amplitude;
+    uint32_t dim, q_heads;    // R; heads of q
+    uint32_t q_units, kv_units;                       // waves of a token's heads
+};
+
+// x - x^3/3! + ..., 1 - x^2/2! + ... for |x| <= pi/4.  The first term left out
+// is below 2^-28 (float) and 2^-56 (double).
+template <typename T>
+__device__ __forceinline__ void sin_cos_small(T x, T &s, T &c)
+{
+    constexpr int TERMS = std::is_same<T, float>::value ? 6 : 9;
+    const T z = x * x;
+    T a = 0, b = 0;
+#pragma unroll
+    for (int n = TERMS - 1; n >= 0; --n) {           // sum (-1)^n z^n / (2n+1)!, / (2n)!
+        double up = 1;
+        for (int i = 2; i <= 2 * n; ++i) up *= i;
+        const T even = (T)((n % 2 ? -1.0 : 1.0) / up), odd = (T)((n % 2 ? -1.0 : 1.0) / (up * (2 * n + 1)));
+        a = fma(a, z, odd);
+        b = fma(b, z, even);
+    }
+    s = a * x;
+    c = b;
+}
+
+// Sine and cosine of a 64-bit fraction of a turn.
+template <typename T>
+__device__ __forceinline__ void sin_cos(uint64_t turn, T &s, T &c)
+{
+    const uint64_t quarter = (turn + (1ull << 61)) >> 62;
+    const int64_t rest = (int64_t)(turn - (quarter << 62));              // [-1/8, 1/8) of a turn
+    T x;
+    if constexpr (std::is_same<T, float>::value)
+        x = (float)(int32_t)(rest >> 32) * (float)(6.283185307179586476925 / 4294967296.0);
+    else
+        x = (double)rest * (6.283185307179586476925 / 18446744073709551616.0);
+    T a, b;
+    sin_cos_small(x, a, b);
+    const bool swap = quarter & 1;
+    s = swap ? b : a;
+    c = swap ? a : b;
+    if (quarter & 2) s = -s;
+    if ((quarter + 1) & 2) c = -c;
+}
+
+__device__ __forceinline__ float low_value(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float high_value(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Where a lane's eight values of a row are: two runs of four.  A lane that
+// turns in the half layout holds d = 4 l.. and R/2 + 4 l.., whose pairs are
+// its own; others hold 8 l...
+template <bool HALF>
+__device__ __forceinline__ void lane_runs(uint32_t l, uint32_t dim, bool turns, uint32_t &first, uint32_t &second)
+{
+    first = HALF && turns ? 4 * l : 8 * l;
+    second = HALF && turns ? dim / 2 + 4 * l : 8 * l + 4;
+}
+
+// Eight values: runs a and b of four.  Lanes that do not turn keep them (0
+// times an infinity is a NaN).
+template <bool HALF, typename T>
+__device__ __forceinline__ void turn(const uint2 &a, const uint2 &b, bool turns, const T (&s)[4], const T (&c)[4],
+                                     float (&x)[8])
+{
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = low_value(w[e]);
+        x[2 * e + 1] = high_value(w[e]);
+    }
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = HALF ? e : 2 * e, j = HALF ? e + 4 : 2 * e + 1;
+        const T u = x[i], v = x[j];
+        y[i] = (float)fma(u, c[e], -(v * s[e]));
+        y[j] = (float)fma(v, c[e], u * s[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = turns ? y[e] : x[e];
+}
+
+// Eight values into a row of the cache, runs at `first` and `second`.  All of
+// a row's lanes take part.
+template <int DT, int D>
+__device__ __forceinline__ void put_values(const PagedCache &c, uint64_t at, uint32_t first, uint32_t second, bool scale,
+                                           const float (&x)[8])
+{
+    if constexpr (DT == SZ_BF16) {
+        uint16_t *p = reinterpret_cast<uint16_t *>(c.data) + at * D;
+        *reinterpret_cast<uint2 *>(p + first) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
+        *reinterpret_cast<uint2 *>(p + second) = make_uint2(bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+    } else {
+        uint32_t a = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t m = __builtin_bit_cast(uint32_t, x[e]) & 0x7FFFFFFFu;
+            a = max(a, m < 0x7F800000u ? m : 0u);
+        }
+        a = row_max<kRowLanes<D>>(a);
+        // as for BF16 rows: a <= 1.75 2^(EMAX+k)
+        constexpr int32_t EMAX = DT == SZ_FP8_E4M3 ? 8 : 15;
+        const int32_t byte = max(1, (int32_t)(a >> 23) - EMAX + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+        const float inv = __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23);
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e / 2] = fp8_pair<DT>(x[2 * e] * inv, x[2 * e + 1] * inv, w[e / 2], e % 2 == 1);
+        *reinterpret_cast<uint32_t *>(c.data + at * D + first) = w[0];
+        *reinterpret_cast<uint32_t *>(c.data + at * D + second) = w[1];
+        if (scale) c.scales[at] = (uint8_t)byte;
+    }
+}
+
+// Heads [head0, head0 + heads) of a wave's tokens, queries or keys.  place: the
+// token's key row in head 0.
+template <int DT, int D, bool HALF, bool QUERIES>
+__device__ __forceinline__ void turn_heads(const RotaryArgs &a, uint64_t turn_of, uint32_t token, bool there, uint64_t place,
+                                           uint32_t head0, uint32_t heads)
+{
+    using T = typename std::conditional<!QUERIES && DT != SZ_BF16, double, float>::type;
+    const uint32_t l = lane_id() % kRowLanes<D>;
+    const bool turns = 8 * l < a.dim;
+    uint32_t first, second;
+    lane_runs<HALF>(l, a.dim, turns, first, second);
+    const uint16_t *from = QUERIES ? a.q + (uint64_t)token * a.q_token : a.k + (uint64_t)token * a.k_token;
+    const uint64_t step = QUERIES ? a.q_head : a.k_head;
+    T s[4], c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sin_cos<T>(turn_of * a.turns[turns ? 4 * l + e : 0], s[e], c[e]);
+        s[e] *= (T)a.amplitude;
+        c[e] *= (T)a.amplitude;
+    }
+    if (!there) return;                                                  // whole rows: a row's lanes agree
+    for (uint32_t h0 = 0; h0 < heads; h0 += kAhead) {
+        uint2 x[kAhead], y[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const uint16_t *p = from + (uint64_t)(head0 + min(h0 + j, heads - 1)) * step;
+            x[j] = load_nt(reinterpret_cast<const uint2 *>(p + first));
+            y[j] = load_nt(reinterpret_cast<const uint2 *>(p + second));
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (h0 + j >= heads) break;
+            float v[8];
+            turn<HALF, T>(x[j], y[j], turns, s, c, v);
+            const uint32_t head = head0 + h0 + j;
+            if constexpr (QUERIES) {
+                uint16_t *p = a.out + (uint64_t)token * a.out_token + (uint64_t)head * a.out_head;
+                store_nt(reinterpret_cast<uint2 *>(p + first), make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])));
+                store_nt(reinterpret_cast<uint2 *>(p + second), make_uint2(bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])));
+            } else {
+                put_values<DT, D>(a.c, place + ((uint64_t)head << a.c.lg_page), first, second, l == 0, v);
+            }
+        }
+    }
+}
+
+// The same heads' values, as sz_cache_write writes them.
+template <int DT, int D>
+__device__ __forceinline__ void write_heads(const RotaryArgs &a, uint32_t token, bool there, uint64_t place, uint32_t head0,
+                                            uint32_t heads)
+{
+    const uint32_t off = lane_id() % kRowLanes<D> * 8;
+    if (!there) return;
+    const uint16_t *from = a.v + (uint64_t)token * a.v_token + off;
+    for (uint32_t h0 = 0; h0 < heads; h0 += kAhead) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            x[j] = load_nt(reinterpret_cast<const uint4 *>(from + (uint64_t)(head0 + min(h0 + j, heads - 1)) * a.v_head));
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (h0 + j < heads) put_chunk<DT, D>(a.c, place + ((uint64_t)(a.c.heads + head0 + h0 + j) << a.c.lg_page), off, x[j]);
+    }
+}
+
+template <int DT, int D, bool HALF>
+__global__ __launch_bounds__(kRotaryThreads) void sz_rotary_move(RotaryArgs a)
+{
+    constexpr uint32_t TOKENS = 64 / kRowLanes<D>;
+    const uint32_t units = a.q_units + 2 * a.kv_units;
+    const uint32_t unit = uniform(blockIdx.x * (kRotaryThreads / 64) + threadIdx.x / 64);
+    const uint32_t part = unit % units;
+    const uint64_t t64 = (uint64_t)(unit / units) * TOKENS;
+    if (t64 >= a.b.tokens) return;
+    const uint32_t t0 = (uint32_t)t64, lane = lane_id();
+    uint32_t i;
+    int32_t pos = 0;
+    const bool found = token_position<TOKENS>(a.b, t0, unit == 0, i, pos);
+    // a lane of TOKENS: its token's place (queries: only that it has one) and the position it turns by
+    constexpr uint64_t NONE = ~0ull;
+    uint64_t mine = NONE;
+    int32_t at = 0;
+    if (found) {
+        at = a.positions ? a.positions[t0 + lane] : pos;
+        if (part < a.q_units) {
+            mine = 0;
+        } else {
+            const uint32_t page = (uint32_t)a.b.table[(uint64_t)i * a.b.width + ((uint32_t)pos >> a.c.lg_page)];
+            if (page < a.c.pages)
+                mine = row_index(a.c, page, 0, 0, (uint32_t)pos & ((1u << a.c.lg_page) - 1));
+            else
+                flag_batch(a.b);
+        }
+    }
+    const int sub = (int)(lane / kRowLanes<D>);
+    const uint64_t place = __shfl(mine, sub, 64);
+    const uint64_t turn_of = (uint64_t)(int64_t)__shfl(at, sub, 64);
+    const bool there = place != NONE;
+    const uint32_t token = t0 + (uint32_t)sub;
+    if (part < a.q_units) {
+        const uint32_t head0 = part * kHeads;
+        turn_heads<DT, D, HALF, true>(a, turn_of, token, there, 0, head0, min(kHeads, a.q_heads - head0));
+    } else {
+        const bool keys = part < a.q_units + a.kv_units;
+        const uint32_t head0 = (part - a.q_units - (keys ? 0 : a.kv_units)) * kHeads, heads = min(kHeads, a.c.heads - head0);
+        if (keys)
+            turn_heads<DT, D, HALF, false>(a, turn_of, token, there, place, head0, heads);
+        else
+            write_heads<DT, D>(a, token, there, place, head0, heads);
+    }
+}
+
+template <int DT>
+void launch_rotary(const RotaryArgs &a, uint32_t head_dim, bool half, uint32_t groups, hipStream_t s)
+{
+    const dim3 grid(groups), block(kRotaryThreads);
+    if (head_dim == 128) {
+        if (half)
+            hipLaunchKernelGGL((sz_rotary_move<DT, 128, true>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((sz_rotary_move<DT, 128, false>), grid, block, 0, s, a);
+    } else {
+        if (half)
+            hipLaunchKernelGGL((sz_rotary_move<DT, 64, true>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((sz_rotary_move<DT, 64, false>), grid, block, 0, s, a);
+    }
+}
+
+}  // namespace
+}  // namespace sz
+
+using namespace sz;
+
+extern "C" int sz_rotary_write(const sz_cache *cache, const sz_batch *batch, const sz_rotary *rotary,
+                               const int32_t *d_positions, const void *d_q, uint32_t q_heads, uint64_t q_token_stride,
+                               uint64_t q_head_stride, void *d_out, uint64_t out_token_stride, uint64_t out_head_stride,
+                               const void *d_k, uint64_t k_token_stride, uint64_t k_head_stride, const void *d_v,
+                               uint64_t v_token_stride, uint64_t v_head_stride, int32_t *d_status, void *stream)
+{
+    RotaryArgs a{};
+    int rc = check_paged(cache, batch, d_status, a.c, a.b);
+    if (rc != SZ_OK) return rc;
+    if (!rotary || rotary->dim < 8 || rotary->dim % 8 || rotary->dim > cache->head_dim || !rotary->d_turns) return SZ_E_ARG;
+    if (rotary->interleaved > 1 || !std::isfinite(rotary->amplitude) || q_heads > 0xFFFFu) return SZ_E_ARG;
+    if (reinterpret_cast<uintptr_t>(rotary->d_turns) & 7u || reinterpret_cast<uintptr_t>(d_positions) & 3u) return SZ_E_ALIGN;
+    if (q_heads) {
+        if ((rc = check_rows(d_q, q_token_stride, q_head_stride, a.b.tokens, q_heads)) != SZ_OK) return rc;
+        if ((rc = check_rows(d_out, out_token_stride, out_head_stride, a.b.tokens, q_heads)) != SZ_OK) return rc;
+    }
+    if ((rc = check_rows(d_k, k_token_stride, k_head_stride, a.b.tokens, a.c.heads)) != SZ_OK) return rc;
+    if ((rc = check_rows(d_v, v_token_stride, v_head_stride, a.b.tokens, a.c.heads)) != SZ_OK) return rc;
+    if (a.b.tokens == 0 || a.b.seqs == 0) return SZ_OK;
+    a.turns = rotary->d_turns;
+    a.positions = d_positions;
+    a.q = static_cast<const uint16_t *>(d_q);
+    a.k = static_cast<const uint16_t *>(d_k);
+    a.v = static_cast<const uint16_t *>(d_v);
+    a.out = static_cast<uint16_t *>(d_out);
+    a.q_token = q_token_stride;
+    a.q_head = q_head_stride;
+    a.out_token = out_token_stride;
+    a.out_head = out_head_stride;
+    a.k_token = k_token_stride;
+    a.k_head = k_head_stride;
+    a.v_token = v_token_stride;
+    a.v_head = v_head_stride;
+    a.amplitude = rotary->amplitude;
+    a.dim = rotary->dim;
+    a.q_heads = q_heads;
+    a.q_units = (q_heads + kHeads - 1) / kHeads;
+    a.kv_units = (a.c.heads + kHeads - 1) / kHeads;
+    const uint32_t tokens = 512 / cache->head_dim;                       // of a wave
+    const uint64_t waves = (((uint64_t)a.b.tokens + tokens - 1) / tokens) * (a.q_units + 2 * a.kv_units);
+    const uint64_t groups = (waves + 3) / 4;
+    if (groups * kRotaryThreads > 0xFFFFFFFFull) return SZ_E_ARG;        // a launch's threads
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    LaunchScope scope("sz_rotary_write", s);
+    if (cache->dtype == SZ_BF16)
+        launch_rotary<SZ_BF16>(a, cache->head_dim, !rotary->interleaved, (uint32_t)groups, s);
+    else if (cache->dtype == SZ_FP8_E5M2)
+        launch_rotary<SZ_FP8_E5M2>(a, cache->head_dim, !rotary->interleaved, (uint32_t)groups, s);
+    else
+        launch_rotary<SZ_FP8_E4M3>(a, cache->head_dim, !rotary->interleaved, (uint32_t)groups, s);
+    return hipGetLastError() == hipSuccess ? SZ_OK : SZ_E_HIP;
+}

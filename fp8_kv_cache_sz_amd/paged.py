@@ -331,6 +331,11 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
     head_dim**-0.5; with ``window`` > 0 a token sees the last ``window``
     positions up to its own.  Returns bfloat16 ``out``, or ``(out, lse)`` with
     ``lse`` true or a float32 ``[tokens, q_heads]`` tensor to write into."""
+    return _attend("sz_paged_attention", _native.lib.sz_paged_attention, (), q, cache, batch, scale, window, out, lse, ws,
+                   stream, check)
+
+
+def _attend(name, call, masks, q, cache, batch, scale, window, out, lse, ws, stream, check):
     shape = q.shape
     if len(shape) != 3:
         raise ValueError("q is [tokens, q_heads, head_dim]")
@@ -363,8 +368,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, scale:
         owned.append(ws)
     elif not ws.is_contiguous() or ws.get_device() != cache._index:
         raise ValueError("ws is a contiguous tensor on the cache's device (attention_workspace)")
-    _run("sz_paged_attention", _native.lib.sz_paged_attention, cache, batch,
-         (qp, q_heads, q_token, q_head, cache.head_dim ** -0.5 if scale is None else scale, min(window, 1 << 30),
+    _run(name, call, cache, batch,
+         (*masks, qp, q_heads, q_token, q_head, cache.head_dim ** -0.5 if scale is None else scale, min(window, 1 << 30),
           out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes), stream, owned)
     if check:
         _raise_status(cache, stream)

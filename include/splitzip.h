@@ -423,6 +423,120 @@ int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void 
                        uint64_t q_token_stride, uint64_t q_head_stride, float scale, uint32_t window, void *d_out,
                        float *d_lse, void *d_ws, uint64_t ws_bytes, int32_t *d_status, void *stream);
 
+/* Pages for sequences, from their lengths.  sz_pool is a ring of free pages in
+ * device memory: queue[pages], of which the ends[1] entries from ends[0] on
+ * (modulo pages) are free page numbers; pages also bounds the page numbers.
+ * Sequence i of the batch holds the first d_held[i] entries of its row of
+ * page_table, which this call WRITES, and needs ceil(kv_lens[i] / page_tokens).
+ *   - Missing pages are taken from the ring's head, in the order of sequences
+ *     and then of the row.  A sequence gets all of its missing pages if the
+ *     free ones reach for it and all before it, else none: d_held_out[i] is
+ *     then d_held[i], its fresh entries become -1 (which no call of the cache
+ *     reads or writes at) and *d_status SZ_E_CAPACITY.
+ *   - Pages beyond need (a sequence that got shorter, or is done: length 0)
+ *     go behind the ring's free pages, in the same order, for later calls;
+ *     their entries of the row stay as they are.
+ *   - d_held_out and d_ends_out [2] receive the state after the call; they may
+ *     be d_held and pool->ends.  If they are not, a call can be made again with
+ *     the same result.
+ *   - d_slots (may be NULL), int64 [tokens]: page * page_tokens + row of each
+ *     of the batch's tokens after the call, -1 for tokens without a place (of
+ *     no sequence, p < 0, or of no page).
+ * A sequence whose length leaves [0, max_kv] or whose d_held leaves [0,
+ * table_width] is skipped (its d_held_out is its d_held), ends that contradict
+ * the ring count as no free pages, and more free pages than the ring has are
+ * cut to that many; each sets *d_status to SZ_E_FORMAT.  seqs, table_width,
+ * tokens and max_kv as in the calls above; max_new is used for shaping only
+ * (and for slots, which are those of sequences that fit it).  d_ws: ws_bytes
+ * >= sz_pages_assign_workspace_size(batch).  pages <= 2^30.  Calls that share
+ * a pool, a table or a workspace must not overlap. */
+typedef struct sz_pool {
+    uint32_t page_tokens;
+    uint32_t pages;
+    int32_t *queue;      /* [pages] */
+    const int32_t *ends; /* [2] */
+} sz_pool;
+
+uint64_t sz_pages_assign_workspace_size(const sz_batch *batch);
+int sz_pages_assign(const sz_pool *pool, const sz_batch *batch, const int32_t *d_held, int32_t *d_held_out,
+                    int32_t *d_ends_out, int64_t *d_slots, void *d_ws, uint64_t ws_bytes, int32_t *d_status,
+                    void *stream);
+
+/* Trees of drafted tokens: new token i of a sequence continues new token
+ * d_parents[start + i] < i of the same sequence, or (-1) what is cached before
+ * the new ones.  d_masks, uint64 [tokens][words]: bit j of word w of a token's
+ * row is set for 64 w + j = i and every token above it.  d_positions, int32
+ * [tokens]: kv_lens - n + the number of tokens above i, the position that
+ * token i stands at in its line (its place in the cache is that of any new
+ * token).  max_new <= 64 words, words <= SZ_TREE_WORDS.  A parent out of
+ * [-1, i) counts as -1.  d_status may be NULL: then nothing is reported.
+ * page_table is not read. */
+enum { SZ_TREE_WORDS = 16 };
+int sz_draft_tree(const sz_batch *batch, const int32_t *d_parents, uint64_t *d_masks, uint32_t words,
+                  int32_t *d_positions, int32_t *d_status, void *stream);
+
+/* sz_paged_attention for trees of drafted tokens, or any other masks among the
+ * new tokens: a token sees the keys j < len - n that are cached before the
+ * new ones, of its sequence's new tokens those that its row of d_masks names
+ * (bits of tokens that have no place, p < 0 or i >= n, are ignored; a token
+ * with p < 0 sees nothing), and no others.  window > 0: a token that names c
+ * new ones sees the last window - max(c, 1) of the cached ones, and all that
+ * it names.  A token that sees no key gets 0 and -inf.  words as above.  Other
+ * arguments, d_ws, its size and the return codes as sz_paged_attention, of
+ * which this is the same computation. */
+int sz_tree_attention(const sz_cache *cache, const sz_batch *batch, const uint64_t *d_masks, uint32_t words,
+                      const void *d_q, uint32_t q_heads, uint64_t q_token_stride, uint64_t q_head_stride, float scale,
+                      uint32_t window, void *d_out, float *d_lse, void *d_ws, uint64_t ws_bytes, int32_t *d_status,
+                      void *stream);
+
+/* Rotary positions.  Of each row the first dim values are turned: the pairs
+ * (d, d + dim/2), or (2d, 2d + 1) if interleaved is 1, d < dim/2, by the angle
+ * p f_d, and multiplied by amplitude:
+ *   x' = amplitude (x cos - y sin),  y' = amplitude (y cos + x sin);
+ * values from dim on are left.  d_turns[d], uint64 [dim/2] on the device, is
+ * the fraction f_d / 2 pi of a turn in units of 2^-64 (modulo 1), so that
+ * angles are exact at any position.  dim is a multiple of 8 up to head_dim. */
+typedef struct sz_rotary {
+    const uint64_t *d_turns;
+    uint32_t dim;
+    uint32_t interleaved;
+    double amplitude;
+} sz_rotary;
+
+/* Turns the new tokens' queries and keys and writes keys and values into their
+ * places: sz_cache_write with rotary positions.  p is the token's position
+ * (sz_batch), or d_positions[t], int32 [tokens], where that is not NULL (a
+ * tree's, say); the place in the cache does not depend on d_positions.  d_q and
+ * d_out: BF16 [tokens][q_heads][head_dim] with strides in elements, rows
+ * contiguous and 16-byte aligned; d_out may be d_q with the same strides, and
+ * must not meet any of the inputs otherwise.  q_heads 0: no queries.  Turned queries
+ * are computed in 32 bits and rounded to BF16 once.  Turned keys are rounded
+ * once to BF16 for BF16 caches (32 bits before that); for FP8 caches they are
+ * computed in 64 bits, rounded to 32 and then quantised as sz_cache_write
+ * quantises.  Values are written as sz_cache_write writes them.  Rows of
+ * d_out of tokens without a place stay as they are.  Return codes as
+ * sz_cache_write. */
+int sz_rotary_write(const sz_cache *cache, const sz_batch *batch, const sz_rotary *rotary, const int32_t *d_positions,
+                    const void *d_q, uint32_t q_heads, uint64_t q_token_stride, uint64_t q_head_stride, void *d_out,
+                    uint64_t out_token_stride, uint64_t out_head_stride, const void *d_k, uint64_t k_token_stride,
+                    uint64_t k_head_stride, const void *d_v, uint64_t v_token_stride, uint64_t v_head_stride,
+                    int32_t *d_status, void *stream);
+
+/* Keeps some of the new tokens: the rows (K, V, all heads, scale bytes) of new
+ * token d_kept[i][k] of sequence i move to the place of new token k, for k <
+ * d_counts[i], in every one of `layers` caches of one shape (dtype, pages,
+ * page_tokens, kv_heads, head_dim) and different memory.  d_kept, int32
+ * [seqs][kept_width], ascends strictly in each row, from 0 or more to below n;
+ * counts lie in [0, kept_width] and are at most n: a sequence that breaks this
+ * is left as it is and SZ_E_FORMAT reported.  The caller's next lengths are
+ * kv_lens - n + counts.  Rows behind the kept ones keep their contents; tokens
+ * with p < 0 are not moved, nor are rows whose page is none of the cache's.
+ * The places of different sequences' new tokens must be distinct
+ * (sz_cache_check).  Return codes as sz_cache_write. */
+enum { SZ_KEEP_LAYERS = 4096 };
+int sz_cache_keep(const sz_cache *caches, uint32_t layers, const sz_batch *batch, const int32_t *d_kept,
+                  uint32_t kept_width, const int32_t *d_counts, int32_t *d_status, void *stream);
+
 /* Instrumentation (not part of the codec).  While enabled, every kernel the
  * library launches is bracketed by a pair of HIP events recorded on the
  * launch stream.  sz_profile_collect waits for the recorded events, writes
