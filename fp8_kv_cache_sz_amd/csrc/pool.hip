@@ -15,21 +15,27 @@
 // the two prefix sums are known, and a page that was given up is not handed
 // out again while the step that read it may still run.
 //
-// Bound by latency: a launch, the lengths, the sums, the entries.  A small
-// batch is one workgroup's; of a large one a workgroup sums and a second
-// launch, as wide as the batch, moves.
+// Bound by latency: a launch, the lengths, the sums, the entries.  Up to
+// kOneSeqs sequences every workgroup of one launch works out all sums for
+// itself (they are a few KB, which the L2 has) and moves its share.  Where held
+// or the ring's ends are updated in place, the workgroup that arrives last
+// writes them, when all have read them; a count costs 10 ns or more, one after
+// another, so beyond kOneCounts workgroups, as for more sequences, a launch of one
+// workgroup sums and a second one moves.
 #include "paged.hpp"
 
 namespace sz {
 namespace {
 
-constexpr uint32_t kSumThreads = 1024;
-constexpr uint32_t kSmallSeqs = 1024;        // a thread each
-constexpr uint64_t kSmallPages = 4096;       // that the new tokens may fill
-constexpr uint32_t kSmallTokens = 4096;      // that get slots
-constexpr uint32_t kMoveGroup = 256;
+constexpr uint32_t kSumThreads = 1024;       // with 256, 1,000 prompts' slots (1.15M) take 18 us instead of 11
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kOneSeqs = 2048;          // of one launch: their moves fill 32 KB of LDS
+constexpr uint32_t kWaveTokens = 256;        // four a lane
+constexpr uint64_t kOneTokens = 1u << 18;    // that get slots, one a lane
+constexpr uint64_t kOneCounts = 128;
 constexpr uint32_t kNothing = 0xFFFFFFFFu;
 constexpr uint32_t kMaxPages = 1u << 30;     // ring positions: four times this stays in 32 bits
+constexpr uint32_t kMany = 0x7FFFFFFFu;      // sums stop here: above any ring's pages
 
 // What happens to a sequence, or happened: where its fresh entries come from
 // behind the ring's head (kNothing: not served), where those it gives go to
@@ -51,9 +57,8 @@ struct Pool {
     uint32_t pages, lg_page;
 };
 
-__device__ __forceinline__ Move want(const Pool &p, const PagedBatch &b, uint32_t i)
+__device__ __forceinline__ Move want(const Pool &p, const PagedBatch &b, int32_t len, int32_t held)
 {
-    const int32_t len = b.lens[i], held = p.held[i];
     if (len < 0 || len > (int32_t)b.max_kv || held < 0 || (uint32_t)held > b.width) {
         flag_batch(b);
         return Move{kNothing, 0, kNothing, kNothing};
@@ -84,51 +89,44 @@ __device__ __forceinline__ Ring ring(const Pool &p, const PagedBatch &b)
     return Ring{(uint32_t)head, (uint32_t)count, p.pages};
 }
 
-// Sum over the lanes up to this one.
-__device__ __forceinline__ uint64_t wave_sum_up_to(uint64_t x)
+// Sums of pages stop at kMany.
+__device__ __forceinline__ uint32_t plus(uint32_t x, uint32_t y) { return min(x + y, kMany); }
+struct Pair {
+    uint32_t take, give;
+};
+__device__ __forceinline__ Pair plus(Pair x, Pair y) { return Pair{plus(x.take, y.take), plus(x.give, y.give)}; }
+// Over the first `lanes` lanes up to this one.
+__device__ __forceinline__ Pair wave_sum(Pair x, int lanes)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint64_t y = __shfl_up(x, d, 64);
-        if (lane_id() >= (uint32_t)d) x += y;
+    for (int d = 1; d < lanes; d *= 2) {
+        const Pair y{(uint32_t)__shfl_up((int)x.take, d, 64), (uint32_t)__shfl_up((int)x.give, d, 64)};
+        if (lane_id() >= (uint32_t)d) x = plus(x, y);
     }
     return x;
 }
-
-// Sums over the workgroup's threads up to this one, and over all of them.
-// Called by all threads; lds holds a wave's sums.
-struct Sums {
-    uint64_t take[kSumThreads / 64], give[kSumThreads / 64];
-};
-__device__ __forceinline__ void group_sums(Sums &lds, uint64_t &take, uint64_t &give, uint64_t &all_take, uint64_t &all_give)
+// Over the threads of a workgroup before this one; all: over all of them.
+// Called by all threads.
+__device__ __forceinline__ Pair group_sum(Pair *lds, Pair mine, Pair &all)
 {
-    const uint32_t wave = threadIdx.x / 64, lane = lane_id();
-    take = wave_sum_up_to(take);
-    give = wave_sum_up_to(give);
+    const uint32_t wave = threadIdx.x / 64, waves = blockDim.x / 64, lane = lane_id();
+    const Pair upto = wave_sum(mine, 64);
     __syncthreads();                                                 // what was there has been read
-    if (lane == 63) {
-        lds.take[wave] = take;
-        lds.give[wave] = give;
-    }
+    if (lane == 63) lds[wave] = upto;
     __syncthreads();
-    all_take = all_give = 0;
-    for (uint32_t w = 0; w < blockDim.x / 64; ++w) {
-        if (w == wave) {
-            take += all_take;
-            give += all_give;
-        }
-        all_take += lds.take[w];
-        all_give += lds.give[w];
-    }
+    const Pair w = wave_sum(lds[min(lane, waves - 1)], 16);          // of at most 16 waves
+    all = Pair{(uint32_t)__shfl((int)w.take, (int)waves - 1, 64), (uint32_t)__shfl((int)w.give, (int)waves - 1, 64)};
+    const int last = (int)max(wave, 1u) - 1;
+    Pair before{(uint32_t)__shfl((int)w.take, last, 64), (uint32_t)__shfl((int)w.give, last, 64)};
+    if (wave == 0) before = Pair{0, 0};
+    const Pair lanes{(uint32_t)__shfl_up((int)upto.take, 1, 64), (uint32_t)__shfl_up((int)upto.give, 1, 64)};
+    return lane == 0 ? before : plus(before, lanes);
 }
 
-// With the sums up to a sequence, its own included.
-__device__ __forceinline__ bool served(const Ring &r, const Move &m, uint64_t take) { return m.held != kNothing && take <= r.count; }
-__device__ __forceinline__ Move placed(const Ring &r, Move m, uint64_t take, uint64_t give)
+// A sequence's move, from the sums over those before it.
+__device__ __forceinline__ Move placed(const Ring &r, Move m, Pair before)
 {
-    if (served(r, m, take)) m.take_at = (uint32_t)take - taken(m);
-    give -= given(m);
-    m.give_at = give < r.pages ? (uint32_t)give : 0;                 // over that: reported with the ends
+    if (m.held != kNothing && plus(before.take, taken(m)) <= r.count) m.take_at = before.take;
+    m.give_at = before.give < r.pages ? before.give : 0;             // over that: reported with the ends
     return m;
 }
 __device__ __forceinline__ void store_held(const Pool &p, uint32_t i, const Move &m)
@@ -142,14 +140,16 @@ __device__ __forceinline__ void store_held(const Pool &p, uint32_t i, const Move
 
 // The ring after the call.  More pages than the ring has: some sequence holds
 // what it does not own.
-__device__ __forceinline__ void store_ends(const Pool &p, const PagedBatch &b, const Ring &r, uint64_t all_taken, uint64_t all_given)
+__device__ __forceinline__ void store_ends(const Pool &p, const PagedBatch &b, const Ring &r, uint32_t wanted, uint32_t served,
+                                           uint32_t given)
 {
-    uint64_t count = r.count - all_taken + all_given;
+    if (wanted > r.count) *b.status = SZ_E_CAPACITY;
+    uint32_t count = r.count - served + given;                       // below 2^30 + 2^31
     if (count > r.pages) {
         flag_batch(b);
         count = r.pages;
     }
-    p.ends_out[0] = (int32_t)r.at((uint32_t)all_taken);
+    p.ends_out[0] = (int32_t)r.at(served);
     p.ends_out[1] = (int32_t)count;
 }
 
@@ -164,121 +164,193 @@ __device__ __forceinline__ void move_entries(const Pool &p, const PagedBatch &b,
         p.queue[r.at(r.count + m.give_at + e)] = row[m.need + e];
 }
 
-// Token t's slot after the call, or -1.  Its page is read from where the
-// table's entry comes from, the old table or the free pages, neither of which
-// the call writes: nobody waits for the new table.
+// Where the page of token t's place is read: the table's old entry, or the
+// ring's free page that comes there.  The call writes neither: nobody waits for
+// the new table.  row: in the page, or -1 for a token without a place.
 template <typename Moves>
-__device__ __forceinline__ int64_t slot_of(const Pool &p, const PagedBatch &b, const Ring &r, int32_t i, int32_t t, Moves moves)
+__device__ __forceinline__ const int32_t *page_at(const Pool &p, const PagedBatch &b, const Ring &r, const int32_t *starts,
+                                                  const int32_t *lens, int32_t i, int32_t t, Moves moves, int32_t &row)
 {
-    if (i < 0 || t >= (int32_t)b.tokens) return -1;
-    const Move m = moves((uint32_t)i);
-    const Sequence s = sequence(b, (uint32_t)i);
+    const uint32_t j = (uint32_t)max(i, 0);
+    const Move m = moves(j);
+    const Sequence s = i < 0 ? Sequence{0, 0, 0} : checked(b, starts[j], starts[j + 1], lens[j]);
     const int32_t pos = s.len - s.n + (t - s.start);
-    if (m.held == kNothing || t < s.start || t >= s.start + s.n || pos < 0) return -1;
     const uint32_t w = (uint32_t)pos >> p.lg_page;
-    uint32_t page = kNothing;
-    if (w < m.held)
-        page = (uint32_t)p.table[(uint64_t)(uint32_t)i * b.width + w];
-    else if (m.take_at != kNothing)
-        page = (uint32_t)p.queue[r.at(m.take_at + (w - m.held))];
-    if (page >= p.pages) return -1;
-    return ((int64_t)page << p.lg_page) + (pos & ((1 << p.lg_page) - 1));
+    const bool there = m.held != kNothing && t >= s.start && t < s.start + s.n && pos >= 0, old = w < m.held;
+    row = there && (old || m.take_at != kNothing) ? pos & ((1 << p.lg_page) - 1) : -1;
+    if (row < 0) return p.queue;
+    return old ? p.table + (uint64_t)j * b.width + w : p.queue + r.at(m.take_at + (w - m.held));
 }
 
-// Token t's sequence, or -1: a wave's tokens from t0 on.  The starts of the 64
-// sequences from t0's on come in one load and are searched in registers.
-__device__ __forceinline__ int32_t token_sequence(const PagedBatch &b, uint32_t t0, uint32_t t)
+// The sequences of a wave's tokens t0 + 64 k + lane, k < COUNT, or -1.  The
+// starts of the 64 sequences from t0's on come in one load.  Few of them begin
+// among the wave's tokens: counted one after another (1,000 prompts: 9 us where
+// a search takes 13); more: searched in registers.
+template <int COUNT>
+__device__ __forceinline__ void token_sequences(const PagedBatch &b, const int32_t *starts, uint32_t t0, int32_t (&seq)[COUNT])
 {
-    const int32_t first = wave_last_not_above(b.seqs + 1, t0, [&](uint32_t j) { return (int64_t)b.starts[j]; });
+    const int32_t first = wave_last_not_above(b.seqs + 1, t0, [&](uint32_t j) { return (int64_t)starts[j]; });
     const uint32_t base = (uint32_t)max(first, 0), lane = lane_id();
-    const int32_t start = base + lane <= b.seqs ? b.starts[base + lane] : INT32_MAX;
-    uint32_t count = 0;                                              // of them up to t
+    const int32_t start = base + lane <= b.seqs ? starts[base + lane] : INT32_MAX;
+    const int32_t top = __shfl(start, 63, 64), end = (int32_t)(t0 + 64 * COUNT - 1);
+    uint64_t inside = __ballot(start > (int32_t)t0 && start <= end);
+    if (__popcll(inside) <= 16 && top > end) {
 #pragma unroll
-    for (uint32_t step = 32; step; step /= 2)
-        if (__shfl(start, (int)(count + step - 1), 64) <= (int32_t)t) count += step;
-    if (count == 63 && __shfl(start, 63, 64) <= (int32_t)t) ++count;
-    uint32_t i = base + count;
-    if (count == 64)                                                 // 64 sequences on, or more
-        for (uint32_t past = b.seqs + 1; past > i;) {
-            const uint32_t mid = i + (past - i) / 2;
-            if (b.starts[mid] <= (int32_t)t)
-                i = mid + 1;
-            else
-                past = mid;
+        for (int k = 0; k < COUNT; ++k) seq[k] = first;
+        for (; inside; inside &= inside - 1) {
+            const int32_t at = __builtin_amdgcn_readlane(start, (int)__builtin_ctzll(inside));
+#pragma unroll
+            for (int k = 0; k < COUNT; ++k) seq[k] += (int32_t)(t0 + 64 * k + lane) >= at ? 1 : 0;
         }
-    return i == 0 || i > b.seqs ? -1 : (int32_t)i - 1;
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k)
+            if (seq[k] >= (int32_t)b.seqs || t0 + 64 * k + lane >= b.tokens) seq[k] = -1;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < COUNT; ++k) {
+        const int32_t t = (int32_t)(t0 + 64 * k + lane);
+        uint32_t count = 0;                                          // of them up to t
+#pragma unroll
+        for (uint32_t step = 32; step; step /= 2)
+            if (__shfl(start, (int)(count + step - 1), 64) <= t) count += step;
+        if (count == 63 && top <= t) ++count;
+        uint32_t i = base + count;
+        if (count == 64)                                             // 64 sequences on, or more
+            for (uint32_t past = b.seqs + 1; past > i;) {
+                const uint32_t mid = i + (past - i) / 2;
+                if (starts[mid] <= t)
+                    i = mid + 1;
+                else
+                    past = mid;
+            }
+        seq[k] = i == 0 || i > b.seqs || t >= (int32_t)b.tokens ? -1 : (int32_t)i - 1;
+    }
 }
 
-// A small batch: a thread per sequence sums, threads take tokens, and waves
-// move the entries of the sequences that have any.
-__global__ __launch_bounds__(kSumThreads) void sz_pages_assign_small(Pool p, PagedBatch b)
+template <int COUNT, typename Moves>
+__device__ __forceinline__ void store_slots(const Pool &p, const PagedBatch &b, const Ring &r, const int32_t *starts,
+                                            const int32_t *lens, uint32_t t0, Moves moves)
 {
-    __shared__ Sums sums;
-    __shared__ Move moves[kSmallSeqs];
-    const uint32_t i = threadIdx.x;
+    int32_t seq[COUNT];
+    token_sequences(b, starts, t0, seq);
+    int32_t row[COUNT];
+    uint32_t page[COUNT];
+#pragma unroll
+    for (int k = 0; k < COUNT; ++k)
+        page[k] = (uint32_t)*page_at(p, b, r, starts, lens, seq[k], (int32_t)(t0 + 64 * k + lane_id()), moves, row[k]);
+#pragma unroll
+    for (int k = 0; k < COUNT; ++k)
+        if (t0 + 64 * k + lane_id() < b.tokens)
+            p.slots[t0 + 64 * k + lane_id()] = row[k] < 0 || page[k] >= p.pages ? -1 : ((int64_t)page[k] << p.lg_page) + row[k];
+}
+
+// One launch: all sums in every workgroup, a share of the entries and tokens,
+// EACH tokens a lane.
+template <int EACH>
+__global__ __launch_bounds__(kSumThreads) void sz_pages_assign_one(Pool p, PagedBatch b, uint32_t *arrived)
+{
+    constexpr uint32_t SEQS = kOneSeqs / kSumThreads;                // of a thread
+    __shared__ Move moves[kOneSeqs];
+    __shared__ Pair sums[kSumThreads / 64];
+    __shared__ int32_t starts[kOneSeqs + 1], lens[kOneSeqs];
+    __shared__ uint32_t last;
+    const uint32_t wave = uniform(threadIdx.x / 64), waves = gridDim.x * (kSumThreads / 64), mine = blockIdx.x * (kSumThreads / 64) + wave;
     const Ring r = ring(p, b);
-    Move m{kNothing, 0, kNothing, kNothing};
-    if (i < b.seqs) m = want(p, b, i);
-    uint64_t take = taken(m), give = given(m), all_take, all_give;
-    group_sums(sums, take, give, all_take, all_give);
-    m = placed(r, m, take, give);
-    if (all_take > r.count) {                                        // of those that are served
-        uint64_t some = m.take_at == kNothing ? 0 : taken(m), none = 0, no;
-        if (i == 0) *b.status = SZ_E_CAPACITY;
-        group_sums(sums, some, none, all_take, no);
+    Move m[SEQS];
+    const uint32_t seqs_each = (b.seqs + kSumThreads - 1) / kSumThreads, i0 = threadIdx.x * seqs_each;
+    int32_t len[SEQS], held[SEQS];
+#pragma unroll
+    for (uint32_t k = 0; k < SEQS; ++k) {
+        const uint32_t i = min(i0 + min(k, seqs_each - 1), b.seqs - 1);
+        len[k] = b.seqs ? b.lens[i] : 0;
+        held[k] = b.seqs ? p.held[i] : 0;
     }
-    moves[i] = m;
-    __syncthreads();                                                 // held and ends, which may be the outputs, have been read
-    if (i < b.seqs) store_held(p, i, m);
-    if (i == 0) store_ends(p, b, r, all_take, all_give);
-    if (p.slots)
-        for (uint32_t t0 = uniform(threadIdx.x / 64 * 64); t0 < b.tokens; t0 += kSumThreads) {
-            const uint32_t t = t0 + lane_id();
-            const int64_t slot = slot_of(p, b, r, token_sequence(b, t0, t), (int32_t)t, [&](uint32_t j) { return moves[j]; });
-            if (t < b.tokens) p.slots[t] = slot;
+    if (p.slots) {
+        for (uint32_t i = threadIdx.x; i <= b.seqs; i += kSumThreads) starts[i] = b.starts[i];
+        for (uint32_t i = threadIdx.x; i < b.seqs; i += kSumThreads) lens[i] = b.lens[i];
+    }
+    Pair sum{0, 0}, all;
+#pragma unroll
+    for (uint32_t k = 0; k < SEQS; ++k) {
+        m[k] = Move{kNothing, 0, kNothing, kNothing};
+        if (k < seqs_each && i0 + k < b.seqs) m[k] = want(p, b, len[k], held[k]);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < SEQS; ++k) sum = plus(sum, Pair{taken(m[k]), given(m[k])});
+    Pair before = group_sum(sums, sum, all);
+    uint32_t got = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < SEQS; ++k) {
+        if (k >= seqs_each || i0 + k >= b.seqs) break;
+        m[k] = placed(r, m[k], before);
+        before = plus(before, Pair{taken(m[k]), given(m[k])});
+        if (m[k].take_at != kNothing) got += taken(m[k]);            // served: at most the ring's pages together
+        moves[i0 + k] = m[k];
+    }
+    bool writes = blockIdx.x == 0;
+    if (arrived) {
+        // held and the ring's ends, which this call may write, are here: the
+        // loads have been used.  Whoever counts last knows it of all.
+        __syncthreads();
+        if (threadIdx.x == 0) last = atomicInc(arrived, gridDim.x - 1) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (arrived) writes = last;
+    if (writes) {
+        uint32_t served = all.take;
+        if (all.take > r.count) {
+            Pair sum_got;
+            group_sum(sums, Pair{got, 0}, sum_got);
+            served = sum_got.take;
         }
-    uint64_t some = __ballot(m.need != m.held);
-    while (some) {
-        const uint32_t j = threadIdx.x / 64 * 64 + (uint32_t)__builtin_ctzll(some);
-        some &= some - 1;
-        move_entries(p, b, r, j, moves[j]);
+#pragma unroll
+        for (uint32_t k = 0; k < SEQS; ++k)
+            if (k < seqs_each && i0 + k < b.seqs) store_held(p, i0 + k, m[k]);
+        if (threadIdx.x == 0) store_ends(p, b, r, all.take, served, all.give);
+    }
+    const uint32_t t0 = mine * 64 * EACH;
+    if (p.slots && t0 < b.tokens) store_slots<EACH>(p, b, r, starts, lens, t0, [&](uint32_t j) { return moves[j]; });
+    for (uint32_t j0 = mine; j0 < b.seqs; j0 += 64 * waves) {        // every waves-th sequence, 64 looked at together
+        const uint32_t j = j0 + lane_id() * waves;
+        uint64_t some = __ballot(j < b.seqs && moves[min(j, b.seqs - 1)].need != moves[min(j, b.seqs - 1)].held);
+        while (some) {
+            const uint32_t x = j0 + (uint32_t)__builtin_ctzll(some) * waves;
+            some &= some - 1;
+            move_entries(p, b, r, x, moves[x]);
+        }
     }
 }
 
 // The sums of a large batch, kSumThreads sequences at a time.
 __global__ __launch_bounds__(kSumThreads) void sz_pages_assign_sum(Pool p, PagedBatch b)
 {
-    __shared__ Sums sums;
+    __shared__ Pair sums[kSumThreads / 64];
     const Ring r = ring(p, b);
-    uint64_t base_take = 0, base_give = 0, some = 0;
+    Pair base{0, 0}, all;
+    uint32_t got = 0;
     for (uint32_t i0 = 0; i0 < b.seqs; i0 += kSumThreads) {
         const uint32_t i = i0 + threadIdx.x;
         Move m{kNothing, 0, kNothing, kNothing};
-        if (i < b.seqs) m = want(p, b, i);
-        uint64_t take = taken(m), give = given(m), all_take, all_give;
-        group_sums(sums, take, give, all_take, all_give);
-        m = placed(r, m, take + base_take, give + base_give);
-        if (i < b.seqs) {
-            if (m.take_at != kNothing) some += taken(m);
-            p.moves[i] = make_uint4(m.take_at, m.give_at, m.held, m.need);
-            store_held(p, i, m);
-        }
-        base_take += all_take;
-        base_give += all_give;
+        if (i < b.seqs) m = want(p, b, b.lens[i], p.held[i]);
+        const Pair before = group_sum(sums, Pair{taken(m), given(m)}, all);
+        m = placed(r, m, plus(base, before));
+        base = plus(base, all);
+        if (i >= b.seqs) continue;
+        if (m.take_at != kNothing) got += taken(m);
+        p.moves[i] = make_uint4(m.take_at, m.give_at, m.held, m.need);
+        store_held(p, i, m);
     }
-    uint64_t none = 0, all_some, no;
-    group_sums(sums, some, none, all_some, no);
+    group_sum(sums, Pair{got, 0}, all);
     if (threadIdx.x == 0) {
-        if (base_take > r.count) *b.status = SZ_E_CAPACITY;
         p.moves[b.seqs] = make_uint4(r.head, r.count, 0, 0);         // ends_out may be ends
-        store_ends(p, b, r, all_some, base_give);
+        store_ends(p, b, r, base.take, all.take, base.give);
     }
 }
 
 // The entries and slots of a large batch: in the first `fills` workgroups a
 // wave takes a sequence, in the others kWaveTokens tokens.
-constexpr uint32_t kWaveTokens = 256;
-__global__ __launch_bounds__(kMoveGroup) void sz_pages_assign_move(Pool p, PagedBatch b, uint32_t fills)
+__global__ __launch_bounds__(kThreads) void sz_pages_assign_move(Pool p, PagedBatch b, uint32_t fills)
 {
     const uint4 ends = p.moves[b.seqs];
     const Ring r{ends.x, ends.y, p.pages};
@@ -288,17 +360,14 @@ __global__ __launch_bounds__(kMoveGroup) void sz_pages_assign_move(Pool p, Paged
     };
     const uint32_t wave = threadIdx.x / 64;
     if (blockIdx.x < fills) {
-        const uint32_t i = uniform(blockIdx.x * (kMoveGroup / 64) + wave);
+        const uint32_t i = uniform(blockIdx.x * (kThreads / 64) + wave);
         if (i < b.seqs) move_entries(p, b, r, i, move(i));
         return;
     }
-    const uint64_t from = ((uint64_t)(blockIdx.x - fills) * (kMoveGroup / 64) + wave) * kWaveTokens;
-    for (uint32_t k = 0; k < kWaveTokens; k += 64) {
-        if (from + k >= b.tokens) return;
-        const uint32_t t0 = uniform((uint32_t)from + k), t = t0 + lane_id();
-        const int64_t slot = slot_of(p, b, r, token_sequence(b, t0, t), (int32_t)t, move);
-        if (t < b.tokens) p.slots[t] = slot;
-    }
+    const uint64_t from = ((uint64_t)(blockIdx.x - fills) * (kThreads / 64) + wave) * kWaveTokens;
+    if (from >= b.tokens) return;
+    const uint32_t t0 = uniform((uint32_t)from);
+    store_slots<kWaveTokens / 64>(p, b, r, b.starts, b.lens, t0, move);
 }
 
 }  // namespace
@@ -308,7 +377,7 @@ using namespace sz;
 
 extern "C" uint64_t sz_pages_assign_workspace_size(const sz_batch *batch)
 {
-    return batch ? up256(16 * ((uint64_t)batch->seqs + 1)) : 0;
+    return batch ? (uint32_t)SZ_ASSIGN_COUNTERS + up256(16 * ((uint64_t)batch->seqs + 1)) : 0;
 }
 
 extern "C" int sz_pages_assign(const sz_pool *pool, const sz_batch *batch, const int32_t *d_held, int32_t *d_held_out,
@@ -328,8 +397,8 @@ extern "C" int sz_pages_assign(const sz_pool *pool, const sz_batch *batch, const
                           (const void *)d_ends_out})
         if (reinterpret_cast<uintptr_t>(x) & 3u) return SZ_E_ALIGN;
     if (reinterpret_cast<uintptr_t>(d_slots) & 7u || !aligned16(d_ws)) return SZ_E_ALIGN;
-    if (b.seqs && (!d_held || !d_held_out || !d_ws)) return SZ_E_ARG;
-    if (b.seqs && ws_bytes < sz_pages_assign_workspace_size(batch)) return SZ_E_WORKSPACE;
+    if (!d_ws || (b.seqs && (!d_held || !d_held_out))) return SZ_E_ARG;
+    if (ws_bytes < sz_pages_assign_workspace_size(batch)) return SZ_E_WORKSPACE;
     p.queue = pool->queue;
     p.ends = pool->ends;
     p.ends_out = d_ends_out;
@@ -337,13 +406,22 @@ extern "C" int sz_pages_assign(const sz_pool *pool, const sz_batch *batch, const
     p.held_out = d_held_out;
     p.table = const_cast<int32_t *>(b.table);
     p.slots = b.tokens ? d_slots : nullptr;
-    p.moves = static_cast<uint4 *>(d_ws);
+    p.moves = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(d_ws) + (uint32_t)SZ_ASSIGN_COUNTERS);
     p.pages = pool->pages;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const uint64_t fresh = (uint64_t)b.seqs * ((b.max_new >> p.lg_page) + 1);
-    if (b.seqs <= kSmallSeqs && fresh <= kSmallPages && (!p.slots || b.tokens <= kSmallTokens)) {
-        LaunchScope scope("sz_pages_assign_small", s);
-        hipLaunchKernelGGL(sz_pages_assign_small, dim3(1), dim3(kSumThreads), 0, s, p, b);
+    // one token a lane as long as the card has room for the waves
+    const uint64_t slots = p.slots ? b.tokens : 0;
+    const uint32_t each = slots <= kOneTokens ? 1 : kWaveTokens / 64;
+    const uint64_t groups = std::max<uint64_t>({1, (slots + kSumThreads * each - 1) / (kSumThreads * each), (b.seqs + 127) / 128});
+    const bool in_place = (d_held_out == d_held && b.seqs) || d_ends_out == pool->ends;
+    if (b.seqs <= kOneSeqs && (!in_place || groups <= kOneCounts)) {
+        uint32_t *arrived = in_place && groups > 1 ? static_cast<uint32_t *>(d_ws) : nullptr;
+        LaunchScope scope("sz_pages_assign", s);
+        const dim3 grid((uint32_t)groups), block(kSumThreads);
+        if (each == 1)
+            hipLaunchKernelGGL(sz_pages_assign_one<1>, grid, block, 0, s, p, b, arrived);
+        else
+            hipLaunchKernelGGL(sz_pages_assign_one<kWaveTokens / 64>, grid, block, 0, s, p, b, arrived);
     } else {
         const uint32_t fills = (b.seqs + 3) / 4;
         const uint32_t tokens = p.slots ? (b.tokens + 4 * kWaveTokens - 1) / (4 * kWaveTokens) : 0;
@@ -351,10 +429,8 @@ extern "C" int sz_pages_assign(const sz_pool *pool, const sz_batch *batch, const
             LaunchScope scope("sz_pages_assign_sum", s);
             hipLaunchKernelGGL(sz_pages_assign_sum, dim3(1), dim3(kSumThreads), 0, s, p, b);
         }
-        if (fills + tokens) {
-            LaunchScope scope("sz_pages_assign_move", s);
-            hipLaunchKernelGGL(sz_pages_assign_move, dim3(fills + tokens), dim3(kMoveGroup), 0, s, p, b, fills);
-        }
+        LaunchScope scope("sz_pages_assign_move", s);
+        hipLaunchKernelGGL(sz_pages_assign_move, dim3(fills + tokens), dim3(kThreads), 0, s, p, b, fills);
     }
     return hipGetLastError() == hipSuccess ? SZ_OK : SZ_E_HIP;
 }

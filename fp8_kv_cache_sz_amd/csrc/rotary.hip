@@ -18,10 +18,11 @@
 // of two (times 1.75) its largest value is, and so should not depend on the
 // order of a kernel's roundings.
 //
-// A wave takes 4 (D = 64: 8) tokens and up to kHeads heads of q, k or v: the
-// sines are worked out once for the heads.  Bound by HBM in the large, by the
-// latency of four loads that wait for each other (starts, length, page, row)
-// in the small.
+// A wave takes 4 (D = 64: 8) tokens and some heads of q, k or v: the sines are
+// worked out once for the heads.  Its first rows are on their way before it
+// looks up whose its tokens are.  Bound by HBM in the large, in the small by the
+// latency of loads that wait for each other (starts and lengths, page or
+// position, the store).
 #include "paged.hpp"
 
 #include <cmath>
@@ -31,7 +32,9 @@ namespace sz {
 namespace {
 
 constexpr uint32_t kRotaryThreads = 256;
-constexpr uint32_t kHeads = 8;           // of a wave
+// Heads of a wave.  64 trees of 24 tokens, 28 + 4 heads in BF16: 9.9 us (4: 10.5,
+// 16: 11.4); 32,254 tokens of prompts, 32 + 8 heads, E5M2: 116 (125, 117).
+constexpr uint32_t kHeads = 8;
 constexpr int kAhead = 4;                // rows that a lane has in flight
 
 struct RotaryArgs {
@@ -44,7 +47,7 @@ struct RotaryArgs {
     uint64_t q_token, q_head, out_token, out_head, k_token, k_head, v_token, v_head;
     double amplitude;
     uint32_t dim, q_heads;    // R; heads of q
-    uint32_t q_units, kv_units;                       // waves of a token's heads
+    uint32_t heads_each, q_units, kv_units;           // heads of a wave; waves of a token's heads
 };
 
 // x - x^3/3! + ..., 1 - x^2/2! + ... for |x| <= pi/4.  The first term left out
@@ -161,35 +164,79 @@ __device__ __forceinline__ void put_values(const PagedCache &c, uint64_t at, uin
     }
 }
 
-// Heads [head0, head0 + heads) of a wave's tokens, queries or keys.  place: the
-// token's key row in head 0.
+// A wave's tokens: t0 on, a row of lanes each.
+struct Token {
+    uint32_t t;               // the lane's row's
+    bool there;               // it has a place
+    uint64_t place;           // of its key in head 0, as a row of the cache
+    uint64_t turn;            // its position, as a factor of turns
+};
+template <int D, bool PLACES>
+__device__ __forceinline__ Token find_token(const RotaryArgs &a, uint32_t t0, bool edges)
+{
+    constexpr uint32_t TOKENS = 64 / kRowLanes<D>;
+    constexpr uint64_t NONE = ~0ull;
+    const uint32_t lane = lane_id();
+    int32_t at = a.positions && lane < TOKENS ? a.positions[min(t0 + lane, a.b.tokens - 1)] : 0, pos = 0;
+    uint32_t i;
+    uint64_t mine = NONE;
+    if (token_position<TOKENS>(a.b, t0, edges, i, pos)) {
+        if (!a.positions) at = pos;
+        mine = 0;
+        if constexpr (PLACES) {
+            const uint32_t page = (uint32_t)a.b.table[(uint64_t)i * a.b.width + ((uint32_t)pos >> a.c.lg_page)];
+            mine = NONE;
+            if (page < a.c.pages)
+                mine = row_index(a.c, page, 0, 0, (uint32_t)pos & ((1u << a.c.lg_page) - 1));
+            else
+                flag_batch(a.b);
+        }
+    }
+    const int sub = (int)(lane / kRowLanes<D>);
+    Token x;
+    x.t = t0 + (uint32_t)sub;
+    x.place = __shfl(mine, sub, 64);
+    x.there = x.place != NONE;
+    x.turn = (uint64_t)(int64_t)__shfl(at, sub, 64);
+    return x;
+}
+
+// Heads [head0, head0 + heads) of a wave's tokens, queries or keys.
 template <int DT, int D, bool HALF, bool QUERIES>
-__device__ __forceinline__ void turn_heads(const RotaryArgs &a, uint64_t turn_of, uint32_t token, bool there, uint64_t place,
-                                           uint32_t head0, uint32_t heads)
+__device__ __forceinline__ void turn_heads(const RotaryArgs &a, uint32_t t0, bool edges, uint32_t head0, uint32_t heads)
 {
     using T = typename std::conditional<!QUERIES && DT != SZ_BF16, double, float>::type;
-    const uint32_t l = lane_id() % kRowLanes<D>;
+    const uint32_t l = lane_id() % kRowLanes<D>, last = a.b.tokens - 1;
     const bool turns = 8 * l < a.dim;
     uint32_t first, second;
     lane_runs<HALF>(l, a.dim, turns, first, second);
-    const uint16_t *from = QUERIES ? a.q + (uint64_t)token * a.q_token : a.k + (uint64_t)token * a.k_token;
+    const uint32_t token = min(t0 + lane_id() / kRowLanes<D>, last);
+    const uint16_t *from = QUERIES ? a.q + (uint64_t)token * a.q_token + (uint64_t)head0 * a.q_head
+                                   : a.k + (uint64_t)token * a.k_token + (uint64_t)head0 * a.k_head;
     const uint64_t step = QUERIES ? a.q_head : a.k_head;
-    T s[4], c[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        sin_cos<T>(turn_of * a.turns[turns ? 4 * l + e : 0], s[e], c[e]);
-        s[e] *= (T)a.amplitude;
-        c[e] *= (T)a.amplitude;
-    }
-    if (!there) return;                                                  // whole rows: a row's lanes agree
-    for (uint32_t h0 = 0; h0 < heads; h0 += kAhead) {
-        uint2 x[kAhead], y[kAhead];
+    uint2 x[kAhead], y[kAhead];
+    const auto load = [&](uint32_t h0) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const uint16_t *p = from + (uint64_t)(head0 + min(h0 + j, heads - 1)) * step;
+            const uint16_t *p = from + (uint64_t)min(h0 + j, heads - 1) * step;
             x[j] = load_nt(reinterpret_cast<const uint2 *>(p + first));
             y[j] = load_nt(reinterpret_cast<const uint2 *>(p + second));
         }
+    };
+    uint64_t f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = a.turns[turns ? 4 * l + e : 0];
+    load(0);
+    const Token w = find_token<D, !QUERIES>(a, t0, edges);
+    T s[4], c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sin_cos<T>(w.turn * f[e], s[e], c[e]);
+        s[e] *= (T)a.amplitude;
+        c[e] *= (T)a.amplitude;
+    }
+    if (!w.there) return;                                                // whole rows: a row's lanes agree
+    for (uint32_t h0 = 0;;) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             if (h0 + j >= heads) break;
@@ -197,32 +244,43 @@ __device__ __forceinline__ void turn_heads(const RotaryArgs &a, uint64_t turn_of
             turn<HALF, T>(x[j], y[j], turns, s, c, v);
             const uint32_t head = head0 + h0 + j;
             if constexpr (QUERIES) {
-                uint16_t *p = a.out + (uint64_t)token * a.out_token + (uint64_t)head * a.out_head;
+                uint16_t *p = a.out + (uint64_t)w.t * a.out_token + (uint64_t)head * a.out_head;
                 store_nt(reinterpret_cast<uint2 *>(p + first), make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])));
                 store_nt(reinterpret_cast<uint2 *>(p + second), make_uint2(bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])));
             } else {
-                put_values<DT, D>(a.c, place + ((uint64_t)head << a.c.lg_page), first, second, l == 0, v);
+                put_values<DT, D>(a.c, w.place + ((uint64_t)head << a.c.lg_page), first, second, l == 0, v);
             }
         }
+        h0 += kAhead;
+        if (h0 >= heads) break;
+        load(h0);
     }
 }
 
 // The same heads' values, as sz_cache_write writes them.
 template <int DT, int D>
-__device__ __forceinline__ void write_heads(const RotaryArgs &a, uint32_t token, bool there, uint64_t place, uint32_t head0,
-                                            uint32_t heads)
+__device__ __forceinline__ void write_heads(const RotaryArgs &a, uint32_t t0, bool edges, uint32_t head0, uint32_t heads)
 {
     const uint32_t off = lane_id() % kRowLanes<D> * 8;
-    if (!there) return;
-    const uint16_t *from = a.v + (uint64_t)token * a.v_token + off;
-    for (uint32_t h0 = 0; h0 < heads; h0 += kAhead) {
-        uint4 x[kAhead];
+    const uint32_t token = min(t0 + lane_id() / kRowLanes<D>, a.b.tokens - 1);
+    const uint16_t *from = a.v + (uint64_t)token * a.v_token + (uint64_t)head0 * a.v_head + off;
+    uint4 x[kAhead];
+    const auto load = [&](uint32_t h0) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-            x[j] = load_nt(reinterpret_cast<const uint4 *>(from + (uint64_t)(head0 + min(h0 + j, heads - 1)) * a.v_head));
+            x[j] = load_nt(reinterpret_cast<const uint4 *>(from + (uint64_t)min(h0 + j, heads - 1) * a.v_head));
+    };
+    load(0);
+    const Token w = find_token<D, true>(a, t0, edges);
+    if (!w.there) return;
+    for (uint32_t h0 = 0;;) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-            if (h0 + j < heads) put_chunk<DT, D>(a.c, place + ((uint64_t)(a.c.heads + head0 + h0 + j) << a.c.lg_page), off, x[j]);
+            if (h0 + j < heads)
+                put_chunk<DT, D>(a.c, w.place + ((uint64_t)(a.c.heads + head0 + h0 + j) << a.c.lg_page), off, x[j]);
+        h0 += kAhead;
+        if (h0 >= heads) break;
+        load(h0);
     }
 }
 
@@ -232,45 +290,21 @@ __global__ __launch_bounds__(kRotaryThreads) void sz_rotary_move(RotaryArgs a)
     constexpr uint32_t TOKENS = 64 / kRowLanes<D>;
     const uint32_t units = a.q_units + 2 * a.kv_units;
     const uint32_t unit = uniform(blockIdx.x * (kRotaryThreads / 64) + threadIdx.x / 64);
-    const uint32_t part = unit % units;
     const uint64_t t64 = (uint64_t)(unit / units) * TOKENS;
     if (t64 >= a.b.tokens) return;
-    const uint32_t t0 = (uint32_t)t64, lane = lane_id();
-    uint32_t i;
-    int32_t pos = 0;
-    const bool found = token_position<TOKENS>(a.b, t0, unit == 0, i, pos);
-    // a lane of TOKENS: its token's place (queries: only that it has one) and the position it turns by
-    constexpr uint64_t NONE = ~0ull;
-    uint64_t mine = NONE;
-    int32_t at = 0;
-    if (found) {
-        at = a.positions ? a.positions[t0 + lane] : pos;
-        if (part < a.q_units) {
-            mine = 0;
-        } else {
-            const uint32_t page = (uint32_t)a.b.table[(uint64_t)i * a.b.width + ((uint32_t)pos >> a.c.lg_page)];
-            if (page < a.c.pages)
-                mine = row_index(a.c, page, 0, 0, (uint32_t)pos & ((1u << a.c.lg_page) - 1));
-            else
-                flag_batch(a.b);
-        }
-    }
-    const int sub = (int)(lane / kRowLanes<D>);
-    const uint64_t place = __shfl(mine, sub, 64);
-    const uint64_t turn_of = (uint64_t)(int64_t)__shfl(at, sub, 64);
-    const bool there = place != NONE;
-    const uint32_t token = t0 + (uint32_t)sub;
+    const uint32_t t0 = (uint32_t)t64;
+    uint32_t part = unit % units;
     if (part < a.q_units) {
-        const uint32_t head0 = part * kHeads;
-        turn_heads<DT, D, HALF, true>(a, turn_of, token, there, 0, head0, min(kHeads, a.q_heads - head0));
-    } else {
-        const bool keys = part < a.q_units + a.kv_units;
-        const uint32_t head0 = (part - a.q_units - (keys ? 0 : a.kv_units)) * kHeads, heads = min(kHeads, a.c.heads - head0);
-        if (keys)
-            turn_heads<DT, D, HALF, false>(a, turn_of, token, there, place, head0, heads);
-        else
-            write_heads<DT, D>(a, token, there, place, head0, heads);
+        const uint32_t head0 = part * a.heads_each;
+        turn_heads<DT, D, HALF, true>(a, t0, unit == 0, head0, min(a.heads_each, a.q_heads - head0));
+        return;
     }
+    part -= a.q_units;
+    const uint32_t head0 = part % a.kv_units * a.heads_each, heads = min(a.heads_each, a.c.heads - head0);
+    if (part < a.kv_units)
+        turn_heads<DT, D, HALF, false>(a, t0, unit == 0, head0, heads);
+    else                                                                 // V lies behind K: heads [H, 2 H) of the page
+        write_heads<DT, D>(a, t0, false, head0, heads);
 }
 
 template <int DT>
@@ -331,8 +365,9 @@ extern "C" int sz_rotary_write(const sz_cache *cache, const sz_batch *batch, con
     a.amplitude = rotary->amplitude;
     a.dim = rotary->dim;
     a.q_heads = q_heads;
-    a.q_units = (q_heads + kHeads - 1) / kHeads;
-    a.kv_units = (a.c.heads + kHeads - 1) / kHeads;
+    a.heads_each = kHeads;
+    a.q_units = (q_heads + a.heads_each - 1) / a.heads_each;
+    a.kv_units = (a.c.heads + a.heads_each - 1) / a.heads_each;
     const uint32_t tokens = 512 / cache->head_dim;                       // of a wave
     const uint64_t waves = (((uint64_t)a.b.tokens + tokens - 1) / tokens) * (a.q_units + 2 * a.kv_units);
     const uint64_t groups = (waves + 3) / 4;

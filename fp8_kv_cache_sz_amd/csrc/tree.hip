@@ -116,18 +116,25 @@ __global__ __launch_bounds__(64 * W) void sz_draft_tree_many(TreeArgs a)
 // all heads and layers.  kept ascends, so kept[k] >= k: a row is read before
 // any row that comes to its place is written if a head's rows are taken in
 // the order of k, some of them read, then written, then the next.  A wave does
-// that for `heads_each` heads of one sequence, layer and K or V; its lanes look
-// the places up once, 64 of them.  Bound by latency in the small (a launch, the lengths,
-// the kept tokens, their pages, the rows) and by HBM in the large.
+// that for `pairs_each` (K or V, head) pairs of one sequence and layer; its
+// lanes look the places up once, 64 of them.  Bound by latency in the small (a
+// launch, the lengths beside the kept tokens, their pages, the rows) and by
+// HBM in the large.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kLayers = 64;             // of a launch: their pointers are its arguments
-constexpr int kKeepPasses = 4;               // reads in flight
+constexpr int kKeepPasses = 8;               // reads in flight
+// Rows of a wave, and waves that a call should have.  32 layers of 8 heads, 5 of
+// 26 tokens of 16 sequences, BF16: 9.5 us with a pair (5 rows) to a wave, 8.9
+// with two, 7.7 with four, 7.4 with eight; 28 layers of 4 heads, 8 of 64 tokens
+// of 64 sequences, FP8: 12.8, 9.7, 7.9 and 8.0.
+constexpr uint32_t kKeepRows = 40;
+constexpr uint64_t kKeepWaves = 1024;
 
 struct KeepArgs {
     PagedBatch b;
     const int32_t *kept;      // [seqs][width]
     const int32_t *counts;    // [seqs]
-    uint32_t pages, heads, lg_page, width, layers, heads_each;
+    uint32_t pages, heads, lg_page, width, layers, pairs_each, parts;        // parts: waves of a sequence's layer
     uint8_t *data[kLayers], *scales[kLayers];
 };
 
@@ -135,21 +142,23 @@ template <int DT, int D>
 __global__ __launch_bounds__(256) void sz_cache_keep_rows(KeepArgs a)
 {
     constexpr uint32_t BYTES = D * (DT == SZ_BF16 ? 2 : 1), LPR = BYTES / 16, RPP = 64 / LPR;
-    const uint32_t groups = (a.heads + a.heads_each - 1) / a.heads_each;
-    const uint64_t unit = (uint64_t)blockIdx.x * 4 + threadIdx.x / 64;
-    const uint32_t part = uniform((uint32_t)(unit % (2 * groups * a.layers))), seq = uniform((uint32_t)(unit / (2 * groups * a.layers)));
+    const uint32_t unit = uniform(blockIdx.x * 4 + threadIdx.x / 64);
+    const uint32_t part = unit % (a.parts * a.layers), seq = unit / (a.parts * a.layers);
     if (seq >= a.b.seqs) return;
-    const uint32_t layer = part / (2 * groups), kv = part / groups % 2, head0 = part % groups * a.heads_each;
-    const uint32_t heads = min(a.heads_each, a.heads - head0);
+    const uint32_t layer = part / a.parts, pair0 = part % a.parts * a.pairs_each;
+    const uint32_t pairs = min(a.pairs_each, 2 * a.heads - pair0);
+    // what the wave needs to know, in loads that do not wait for each other
+    const int32_t lane = (int32_t)lane_id(), *kept = a.kept + (uint64_t)seq * a.width;
+    int32_t frm = kept[min(lane, (int32_t)a.width - 1)];
+    const int32_t count = a.counts[seq];
     const Sequence s = sequence(a.b, seq);
-    const int32_t count = a.counts[seq], past = s.len - s.n, lane = (int32_t)lane_id();
-    const int32_t *kept = a.kept + (uint64_t)seq * a.width;
+    const int32_t past = s.len - s.n;
     bool good = count >= 0 && count <= (int32_t)a.width && count <= s.n;
-    if (good)
-        for (int32_t k = lane; k < count; k += 64) {
-            const int32_t x = kept[k];
-            good &= x < s.n && (k == 0 ? x >= 0 : x > kept[k - 1]);
-        }
+    if (good) {
+        const int32_t before = __shfl_up(frm, 1, 64);
+        if (lane < count) good = frm < s.n && frm > (lane == 0 ? -1 : before);
+        for (int32_t k = lane + 64; k < count; k += 64) good &= kept[k] < s.n && kept[k] > kept[k - 1];
+    }
     if (!__all(good)) {
         flag_batch(a.b);
         return;
@@ -157,33 +166,33 @@ __global__ __launch_bounds__(256) void sz_cache_keep_rows(KeepArgs a)
     uint8_t *data = a.data[layer], *scales = a.scales[layer];
     const uint32_t page_mask = (1u << a.lg_page) - 1;
     for (int32_t k0 = 0; k0 < count; k0 += 64) {
-        // lane: the rows of kept token k0 + lane, in head 0
+        // lane: the rows of kept token k0 + lane, in pair 0
         constexpr uint64_t NONE = ~0ull;
         uint64_t from = NONE, to = NONE;
         const int32_t k = k0 + lane;
         if (k < count) {
-            const int32_t src = past + kept[k], dst = past + k;
+            if (k0 > 0) frm = kept[k];
+            const int32_t src = past + frm, dst = past + k;
             if (src != dst && dst >= 0) {
                 const int32_t *row = a.b.table + (uint64_t)seq * a.b.width;
                 const uint32_t x = (uint32_t)row[(uint32_t)src >> a.lg_page], y = (uint32_t)row[(uint32_t)dst >> a.lg_page];
                 if (x < a.pages && y < a.pages) {
-                    from = ((((uint64_t)x * 2 + kv) * a.heads) << a.lg_page) + ((uint32_t)src & page_mask);
-                    to = ((((uint64_t)y * 2 + kv) * a.heads) << a.lg_page) + ((uint32_t)dst & page_mask);
+                    from = (((uint64_t)x * 2 * a.heads) << a.lg_page) + ((uint32_t)src & page_mask);
+                    to = (((uint64_t)y * 2 * a.heads) << a.lg_page) + ((uint32_t)dst & page_mask);
                 } else {
                     flag_batch(a.b);
                 }
             }
         }
-        // rows (head, k) in order of k within a head, those that stay where they are left out
+        // rows (pair, k) in order of k within a pair, the first ones that stay where they are left out
         const uint64_t moving = __ballot(from != NONE);
         if (moving == 0) continue;
         const uint32_t first = (uint32_t)__builtin_ctzll(moving), many = (uint32_t)min(count - k0, 64) - first;
-        const uint32_t rows = heads * many;
+        const uint32_t rows = pairs * many, piece = lane_id() % LPR;
         for (uint32_t r0 = 0; r0 < rows; r0 += kKeepPasses * RPP) {
             v4u v[kKeepPasses];
             uint8_t sc[kKeepPasses];
             uint64_t put[kKeepPasses];
-            const uint32_t piece = lane_id() % LPR;
 #pragma unroll
             for (int p = 0; p < kKeepPasses; ++p) {
                 const uint32_t r = r0 + p * RPP + lane_id() / LPR;
@@ -192,9 +201,9 @@ __global__ __launch_bounds__(256) void sz_cache_keep_rows(KeepArgs a)
                 put[p] = __shfl(to, (int)at, 64);
                 if (r >= rows) put[p] = NONE;
                 if (put[p] == NONE) continue;
-                const uint64_t head = (uint64_t)(head0 + r / many) << a.lg_page;
-                get += head;
-                put[p] += head;
+                const uint64_t pair = (uint64_t)(pair0 + r / many) << a.lg_page;
+                get += pair;
+                put[p] += pair;
                 v[p] = *reinterpret_cast<const v4u *>(data + get * BYTES + 16 * piece);
                 if (DT != SZ_BF16 && piece == 0) sc[p] = scales[get];
             }
@@ -285,8 +294,12 @@ extern "C" int sz_cache_keep(const sz_cache *caches, uint32_t layers, const sz_b
             a.data[i] = static_cast<uint8_t *>(caches[i0 + i].data);
             a.scales[i] = static_cast<uint8_t *>(caches[i0 + i].scales);
         }
-        a.heads_each = 1;
-        const uint64_t units = (uint64_t)a.b.seqs * a.layers * 2 * ((a.heads + a.heads_each - 1) / a.heads_each);
+        // as many rows as a wave has in flight, unless that leaves the card without waves
+        const uint64_t all = (uint64_t)a.b.seqs * a.layers * 2 * a.heads;
+        const uint64_t rows = std::max<uint64_t>(1, std::min<uint64_t>(kKeepRows / kept_width, all / kKeepWaves));
+        a.pairs_each = (uint32_t)std::min<uint64_t>(rows, 2 * a.heads);
+        a.parts = (2 * a.heads + a.pairs_each - 1) / a.pairs_each;
+        const uint64_t units = (uint64_t)a.b.seqs * a.layers * a.parts;
         const uint64_t groups = (units + 3) / 4;
         if (groups * 256 > 0xFFFFFFFFull) return SZ_E_ARG;               // a launch's threads
         if (caches->dtype == SZ_BF16)

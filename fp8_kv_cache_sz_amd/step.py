@@ -24,7 +24,8 @@ from ._native import SZ_TREE_WORDS
 from .paged import (PageBatch, PagedCache, SplitZipError, _attend, _BAD_BATCH, _current_device, _current_stream, _Fixed,
                     _plain, _raise_status, _rows, _rows_meet, _run)
 
-_int32 = torch.int32
+_int32, _int64, _empty_like, _contiguous = torch.int32, torch.int64, torch.empty_like, torch.contiguous_format
+COUNTERS = 256          # bytes at the start of an assignment's workspace
 _ANY_PAGE = 1 << 30     # the page size of calls that look at no page: bounds of 2^30 tokens
 
 
@@ -112,9 +113,13 @@ def page_pool(pages: int, page_tokens: int, device="cuda") -> PagePool:
 
 
 def assign_workspace(batch: PageBatch) -> torch.Tensor:
-    """A workspace for ``pages_assign`` of batches of so many sequences."""
+    """A workspace for ``pages_assign`` of batches of so many sequences.  Its
+    first ``COUNTERS`` bytes are zero, as every call leaves them (they are
+    cleared on the current stream, before any call that uses it)."""
     n = _native.sz_pages_assign_workspace_size(batch._ref(_ANY_PAGE))
-    return torch.empty(n, dtype=torch.uint8, device=batch.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=batch.device)
+    ws[:COUNTERS].zero_()
+    return ws
 
 
 def pages_assign(pool: PagePool, batch: PageBatch, held: torch.Tensor, held_out: torch.Tensor | None = None,
@@ -147,7 +152,7 @@ def pages_assign(pool: PagePool, batch: PageBatch, held: torch.Tensor, held_out:
         owned.append(slots)
     elif slots is False:
         slots = None
-    elif slots is not None and (slots.dtype != torch.int64 or slots.shape != (batch.tokens,) or not slots.is_contiguous()
+    elif slots is not None and (slots.dtype != _int64 or slots.shape != (batch.tokens,) or not slots.is_contiguous()
                                 or slots.get_device() != index):
         raise ValueError("slots is a contiguous int64 [%d] tensor on the pool's device" % batch.tokens)
     if ws is None:
@@ -166,7 +171,10 @@ def pages_assign(pool: PagePool, batch: PageBatch, held: torch.Tensor, held_out:
 
 def tree_words(batch: PageBatch) -> int:
     """64-bit words of a token's mask in this batch."""
-    return max(1, (min(batch.max_new, batch.tokens) + 63) // 64)
+    words = batch.__dict__.get("_words")                # of fields that are not reassigned
+    if words is None:
+        words = batch.__dict__["_words"] = max(1, (min(batch.max_new, batch.tokens) + 63) // 64)
+    return words
 
 
 def draft_tree(batch: PageBatch, parents: torch.Tensor, out=None, status: torch.Tensor | None = None, stream=None,
@@ -186,9 +194,9 @@ def draft_tree(batch: PageBatch, parents: torch.Tensor, out=None, status: torch.
     at = _ints("parents", parents, (tokens,), index)
     owned = []
     if out is None:
-        masks = parents.new_empty((tokens, words), dtype=torch.int64)
-        positions = torch.empty_like(parents)
-        owned += [masks, positions]
+        masks = parents.new_empty((tokens, words), dtype=_int64)
+        positions = _empty_like(parents)
+        owned = [masks, positions]
     else:
         masks, positions = out
         words = _mask_words("out[0]", masks, batch, index)
@@ -212,7 +220,7 @@ def draft_tree(batch: PageBatch, parents: torch.Tensor, out=None, status: torch.
 
 
 def _mask_words(name, masks, batch, index):
-    if masks.dtype is not torch.int64 or masks.dim() != 2 or masks.shape[0] != batch.tokens or not masks.is_contiguous():
+    if masks.dtype is not _int64 or masks.dim() != 2 or masks.shape[0] != batch.tokens or not masks.is_contiguous():
         raise ValueError("%s is a contiguous int64 [%d, words] tensor" % (name, batch.tokens))
     if masks.get_device() != index:
         raise ValueError("%s is on %s, not on the call's device" % (name, masks.device))
@@ -327,7 +335,7 @@ def rotary_write(cache: PagedCache, batch: PageBatch, rotary: Rotary, q: torch.T
         heads, dim = q.shape[1], cache.head_dim
         queries = _rows("q", q, tokens, heads, cache)
         if out is None:
-            out = q.new_empty((tokens, heads, dim))
+            out = _empty_like(q, memory_format=_contiguous)
             owned = (out,)
             turned = (out.data_ptr(), heads * dim, dim)
         else:

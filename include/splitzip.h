@@ -446,9 +446,11 @@ int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void 
  * table_width] is skipped (its d_held_out is its d_held), ends that contradict
  * the ring count as no free pages, and more free pages than the ring has are
  * cut to that many; each sets *d_status to SZ_E_FORMAT.  seqs, table_width,
- * tokens and max_kv as in the calls above; max_new is used for shaping only
- * (and for slots, which are those of sequences that fit it).  d_ws: ws_bytes
- * >= sz_pages_assign_workspace_size(batch).  pages <= 2^30.  Calls that share
+ * tokens and max_kv as in the calls above; slots are those of sequences with
+ * at most max_new tokens.  d_ws: ws_bytes >=
+ * sz_pages_assign_workspace_size(batch); its first SZ_ASSIGN_COUNTERS bytes
+ * are cleared once by the caller, and every call finds and leaves them 0.
+ * pages <= 2^30.  Calls that share
  * a pool, a table or a workspace must not overlap. */
 typedef struct sz_pool {
     uint32_t page_tokens;
@@ -457,6 +459,7 @@ typedef struct sz_pool {
     const int32_t *ends; /* [2] */
 } sz_pool;
 
+enum { SZ_ASSIGN_COUNTERS = 256 };
 uint64_t sz_pages_assign_workspace_size(const sz_batch *batch);
 int sz_pages_assign(const sz_pool *pool, const sz_batch *batch, const int32_t *d_held, int32_t *d_held_out,
                     int32_t *d_ends_out, int64_t *d_slots, void *d_ws, uint64_t ws_bytes, int32_t *d_status,

@@ -86,6 +86,33 @@ def test_pages_assign(seqs, P, most, spare, place):
     pool.raise_status()
 
 
+def test_many_slots_in_place():
+    """More tokens than one launch gives slots to where the state is updated
+    in place, and than a lane takes one of."""
+    m = sz()
+    P = 16
+    for lens in ([90000, 1, 0, 60000, 7], [300000]):
+        held = [0] * len(lens)
+        width = -(-max(lens) // P)
+        pages = sum(-(-n // P) for n in lens) + 9
+        queue, ends = torch.randperm(pages, generator=gen(2)).to(torch.int32), ints([pages - 5, pages])
+        table = torch.full((len(lens), width), -1, dtype=torch.int32)
+        starts = [0]
+        for n in lens:
+            starts.append(starts[-1] + n)
+        want = step.assign(P, queue, ends, table, ints(lens), ints(held), width, width * P)
+        slots = step.slots(P, pages, want[2], lens, starts, starts[-1])
+        for beside in (False, True):
+            pool = m.PagePool(P, queue.cuda(), ends.cuda())
+            batch = batch_of(table, ints(lens), ints(starts), starts[-1])
+            h = ints(held).cuda()
+            kw = dict(held_out=h.clone(), ends_out=pool.ends.clone()) if beside else {}
+            got = m.pages_assign(pool, batch, h, slots=True, **kw)
+            assert got.tolist() == slots
+            assert batch.page_table.tolist() == want[2] and pool.queue.tolist() == want[0]
+            assert (kw.get("held_out", h)).tolist() == want[3] and kw.get("ends_out", pool.ends).tolist() == want[1]
+
+
 def test_pages_go_round():
     """Sequences that grow and end over a pool that is used many times over: no
     page is ever held twice, none is lost."""

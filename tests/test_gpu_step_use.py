@@ -321,5 +321,5 @@ def test_instrumentation_names_the_launches():
     torch.cuda.synchronize()
     names = m.profile_collect()
     m.profile_enable(False)
-    assert {"sz_pages_assign_small", "sz_draft_tree", "sz_rotary_write", "sz_cache_keep"} <= set(names)
+    assert {"sz_pages_assign", "sz_draft_tree", "sz_rotary_write", "sz_cache_keep"} <= set(names)
     assert "sz_attn_tiles" in names
