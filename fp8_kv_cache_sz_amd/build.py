@@ -8,9 +8,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", name) for name in
            ("encode.hip", "decode.hip", "calibrate.hip", "runtime.hip", "transfer.hip", "cache.hip", "attention.hip",
-            "rotary.hip", "tree.hip", "pool.hip")]
+            "tree_attention.hip", "rotary.hip", "tree.hip", "pool.hip")]
 HEADERS = [os.path.join(ROOT, "include", "splitzip.h"), os.path.join(HERE, "csrc", "common.hpp"),
-           os.path.join(HERE, "csrc", "paged.hpp"), os.path.join(HERE, "csrc", "keys.hpp")]
+           os.path.join(HERE, "csrc", "paged.hpp"), os.path.join(HERE, "csrc", "keys.hpp"),
+           os.path.join(HERE, "csrc", "attention.hpp")]
 LIBRARY = os.path.join(HERE, "libsplitzip.so")
 ARCH = "gfx950"
 
