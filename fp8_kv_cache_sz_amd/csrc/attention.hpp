@@ -51,6 +51,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define SZ_INLINE __attribute__((always_inline))
 
 constexpr uint32_t kAttnThreads = 256;
+constexpr uint32_t kRowsTokens = 256;    // of a tree in sz_attn_rows
 constexpr uint32_t kRowsMax = 16;        // rows of sz_attn_rows, or twice as many: its products have 16
 constexpr uint32_t kTileKeys = 64;
 constexpr uint32_t kKeyAlign = 64;       // chunks start at multiples of this
@@ -83,6 +84,7 @@ struct TreeArgs : AttnArgs {
     uint32_t words;
     uint32_t tiles_each;      // slots of a sequence, 0: as many as its tokens need, and one
     uint32_t fold;            // sequences in the order of their lengths (by_length), 0: in their own
+    uint32_t row_blocks;      // of a sequence's rows in sz_attn_rows
     static constexpr bool kTree = true;
 };
 
@@ -120,11 +122,14 @@ __device__ __forceinline__ uint64_t new_seen(const TreeArgs &a, const Sequence &
     if (s.n - from < 64) bits &= ~(~0ull << (s.n - from));
     return bits;
 }
+__device__ __forceinline__ uint32_t row_blocks(const TreeArgs &a) { return a.row_blocks; }
+__device__ __forceinline__ uint32_t row_blocks(const AttnArgs &) { return 1; }
 __device__ __forceinline__ Sight tree_sight(const TreeArgs &a, const Sequence &s, int32_t tok)
 {
+    const int32_t past = s.len - s.n;
+    if (a.window == 0 && past > 0) return Sight{0, false};           // whatever the mask says
     int32_t count = 0;
     for (int32_t from = 0; from < s.n; from += 64) count += (int32_t)__popcll(new_seen(a, s, tok, from));
-    const int32_t past = s.len - s.n;
     Sight v;
     v.lo = first_seen(past + max(count, 1) - 1, a.window);
     v.blind = count == 0 && v.lo >= past;
@@ -136,6 +141,14 @@ __device__ __forceinline__ uint64_t old_seen(int32_t lo, int32_t past, int32_t k
     const int32_t first = max(lo - kb, 0), end = min(past - kb, 64);
     if (first >= end) return 0;
     return (~0ull >> (64 - (end - first))) << first;
+}
+
+// A value that the compiler takes for a new one: what follows from it is worked
+// out here, not kept in registers from before.
+__device__ __forceinline__ uint32_t opaque(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -438,18 +451,23 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     __shared__ float lds_o[WAVES][ROWS][D + 4];
     __shared__ float2 lds_ml[WAVES][ROWS];
     __shared__ uint32_t lds_last;
-    // Of a row of a tree: its first cached key (INT32_MIN if it sees none at all) and the new tokens that it sees, 32 at
-    // most.  Every wave writes all of them, so each finds them without a barrier; only masked blocks look.
+    // Of a row of a tree: its first cached key (INT32_MIN if it sees none at all) and the new tokens that it sees, a word
+    // of zeros around them.  Every wave writes all of them, so each finds them without a barrier; only masked blocks look.
+    constexpr uint32_t NAMED = TREE ? kRowsTokens / 32 + 2 : 1;
     __shared__ int32_t lds_lo[TREE ? ROWS : 1];
-    __shared__ uint32_t lds_named[TREE ? ROWS : 1];
+    __shared__ uint32_t lds_named[TREE ? ROWS : 1][NAMED];
 
     const uint32_t head = blockIdx.x % a.c.heads;
-    const uint32_t seq = blockIdx.x / a.c.heads % a.b.seqs;
-    const uint32_t split = blockIdx.x / a.c.heads / a.b.seqs;
+    uint32_t unit = blockIdx.x / a.c.heads, row0 = 0;                       // trees: the first of the workgroup's rows
+    if constexpr (TREE) {                           // blocks of the same rows beside each other: they read the same keys
+        row0 = unit % a.row_blocks * ROWS;
+        unit /= a.row_blocks;
+    }
+    const uint32_t seq = unit % a.b.seqs, split = unit / a.b.seqs;
     const Sequence s = sequence(a.b, seq);
     const uint64_t all_rows = (uint64_t)s.n * a.group;
-    if (all_rows == 0 || all_rows > min(a.rows_limit, ROWS)) return;
-    const uint32_t rows = (uint32_t)all_rows;
+    if (TREE ? all_rows <= row0 || all_rows > a.rows_limit : all_rows == 0 || all_rows > min(a.rows_limit, ROWS)) return;
+    const uint32_t rows = TREE ? min((uint32_t)all_rows - row0, ROWS) : (uint32_t)all_rows;
     const uint32_t chunks = chunks_of(s, a.window, a.rows_chunk);
     const bool whole = chunks == 1;
     const int64_t begin64 = (int64_t)first_key(s, a.window) + (int64_t)split * a.rows_chunk;
@@ -461,19 +479,46 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     const uint32_t n = lane % 16, g = lane / 16;
     // Row 16 b + n; one that is not there computes what the last one does.
     const int32_t past = s.len - s.n;
+    constexpr int32_t STEP = 32 * WAVES;
+    int32_t kb = begin + 32 * (int32_t)wave;
+    // The pages of this wave's next 32 blocks, two lanes to a block: one load,
+    // so that no block's loads wait for its page number.  Positions behind the
+    // end take the last one's page; their keys are hidden.
+    uint32_t ahead = 0, at = 0;
+    const auto look_ahead = [&](int32_t from) {
+        ahead = page_of(a.c, a.b, seq,
+                        (uint32_t)min((int64_t)from + (int64_t)(lane / 2) * STEP + 16 * (lane % 2), (int64_t)s.len - 1));
+        at = 0;
+    };
+    if constexpr (TREE) {
+        if (kb < end) look_ahead(kb);               // on its way beside the masks
+#pragma unroll 1                                    // one row of a lane after another: the registers are q's
+        for (int b = 0; b < NB; ++b) {
+            const int32_t tok = (int32_t)((row0 + min(16 * b + n, rows - 1)) / a.group);
+            uint32_t *named = lds_named[16 * b + n];
+            int32_t count = 0;
+#pragma unroll 1
+            for (uint32_t w = 0; w < kRowsTokens / 64; ++w) {
+                const uint64_t bits = new_seen(a, s, tok, 64 * (int32_t)w);
+                count += (int32_t)__popcll(bits);
+                if (g == 0) {
+                    named[2 * w + 1] = (uint32_t)bits;
+                    named[2 * w + 2] = (uint32_t)(bits >> 32);
+                }
+            }
+            const int32_t first = first_seen(past + max(count, 1) - 1, a.window);
+            if (g == 0) {
+                lds_lo[16 * b + n] = count == 0 && first >= past ? INT32_MIN : first;
+                named[0] = named[NAMED - 1] = 0;
+            }
+        }
+    }
     int32_t lo[NB], hi[NB];
     bf16x8 q[NB][D / 32];                           // the products' second operand, in K's order of d
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        const uint32_t r = min(16 * b + n, rows - 1), tok = r / a.group;
-        if constexpr (TREE) {
-            const uint32_t named = (uint32_t)new_seen(a, s, (int32_t)tok, 0);
-            const int32_t first = first_seen(past + max((int32_t)__popc(named), 1) - 1, a.window);
-            if (g == 0) {
-                lds_lo[16 * b + n] = named == 0 && first >= past ? INT32_MIN : first;
-                lds_named[16 * b + n] = named;
-            }
-        } else {
+        const uint32_t r = row0 + min(16 * b + n, rows - 1), tok = r / a.group;
+        if constexpr (!TREE) {
             visible(past + (int32_t)tok, a.window, lo[b], hi[b]);
         }
         const uint16_t *p = a.q + (uint64_t)(s.start + tok) * a.q_token + (uint64_t)(head * a.group + r % a.group) * a.q_head;
@@ -498,18 +543,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     const int32_t all_lo = first_seen(s.len - 1, a.window);                  // every row sees [all_lo, all_hi]
     const int32_t all_hi = TREE ? past - 1 : past;
 
-    constexpr int32_t STEP = 32 * WAVES;
-    int32_t kb = begin + 32 * (int32_t)wave;
     KeyBlock<DT, D> cur;
-    // The pages of this wave's next 32 blocks, two lanes to a block: one load,
-    // so that no block's loads wait for its page number.  Positions behind the
-    // end take the last one's page; their keys are hidden.
-    uint32_t ahead = 0, at = 0;
-    const auto look_ahead = [&](int32_t from) {
-        ahead = page_of(a.c, a.b, seq,
-                        (uint32_t)min((int64_t)from + (int64_t)(lane / 2) * STEP + 16 * (lane % 2), (int64_t)s.len - 1));
-        at = 0;
-    };
     uint32_t page[2];
     const auto next_pages = [&]() {
         page[0] = __builtin_amdgcn_readlane(ahead, at);
@@ -525,7 +559,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
             for (int i = 0; i < D / 32; ++i) asm volatile("" : "+v"(q[b][i]));
     };
     if (kb < end) {
-        look_ahead(kb);
+        if (!TREE) look_ahead(kb);
         next_pages();
         have_q();
         load_keys<DT, D>(a, head, page, kb, cur);
@@ -603,11 +637,14 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
             if constexpr (TREE)
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const int32_t first = lds_lo[16 * b + n], new0 = past - kb;          // new0: the first new token's bit
-                    const uint32_t named = lds_named[16 * b + n];
-                    const int32_t from = max(first - kb, 0), end = first == INT32_MIN ? 0 : min(new0, 32);
+                    const uint32_t row = 16 * b + opaque(n);
+                    const int32_t first = lds_lo[row], at = kb - past;            // at: the new token of bit 0
+                    const int32_t from = max(first - kb, 0), end = first == INT32_MIN ? 0 : min(-at, 32);
                     uint32_t bits = from < end ? (~0u >> (32 - (end - from))) << from : 0u;
-                    if (new0 < 32 && new0 > -32) bits |= new0 >= 0 ? named << new0 : named >> -new0;
+                    if (at > -32 && at < (int32_t)kRowsTokens) {
+                        const uint32_t *named = lds_named[row] + ((at >> 5) + 1);
+                        bits |= __builtin_amdgcn_alignbit(named[1], named[0], (uint32_t)at & 31);
+                    }
                     sees[b] = bits >> (4 * g);
                 }
 #pragma unroll
@@ -781,7 +818,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
 #pragma unroll
             for (int j = 0; j < VD; ++j) acc[j] += lds_o[w][row][d + j] * f;
         }
-        const uint32_t rtok = row / a.group, rhead = head * a.group + row % a.group;
+        const uint32_t rtok = (row0 + row) / a.group, rhead = head * a.group + (row0 + row) % a.group;
         const bool empty = TREE ? lds_lo[row] == INT32_MIN : past + (int32_t)rtok < 0;
         store_row<D, VD>(a, whole, split, s.start + rtok, rhead, d, acc, empty ? 0.f : 1.f / sum);
         if (d == 0) store_stats(a, whole, split, s.start + rtok, rhead, empty, top, sum);
@@ -795,7 +832,8 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0)
-        lds_last = atomicInc(a.arrived + (uint64_t)seq * a.c.heads + head, chunks - 1) == chunks - 1;
+        lds_last = atomicInc(a.arrived + (TREE ? blockIdx.x - (uint64_t)split * a.b.seqs * a.c.heads * row_blocks(a)
+                                                : (uint64_t)seq * a.c.heads + head), chunks - 1) == chunks - 1;
     __syncthreads();
     if (!lds_last) return;
     constexpr uint32_t LANES = D / 4, GROUPS = kAttnThreads / LANES;
@@ -806,7 +844,7 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
     const uint32_t lanes_group = threadIdx.x / LANES, jlane = threadIdx.x % LANES, part = lanes_group % parts;
     for (uint32_t r0 = 0; r0 < rows; r0 += GROUPS / parts) {
         const uint32_t r = r0 + lanes_group / parts;
-        const uint32_t jtok = r / a.group, jhead = head * a.group + r % a.group;
+        const uint32_t jtok = (row0 + r) / a.group, jhead = head * a.group + (row0 + r) % a.group;
         const int32_t jpos = past + (int32_t)jtok, jlo = TREE ? lds_lo[min(r, rows - 1)] : 0;
         const bool empty = TREE ? jlo == INT32_MIN : jpos < 0;
         Joined x;
@@ -950,12 +988,7 @@ struct FetchFp8 {
 
 // The places that a lane reads differ between the pieces of a row by an
 // exclusive or of constants, and between rows by constants: one register
-// holds them all.  opaque() keeps the compiler from holding each.
-__device__ __forceinline__ uint32_t opaque(uint32_t x)
-{
-    asm volatile("" : "+v"(x));
-    return x;
-}
+// holds them all; opaque() keeps the compiler from holding each.
 
 // K of 32 keys as the first operand: key 32 b + lane % 32, d = 16 i + 8 g + 0..7.
 template <int D>
@@ -1482,7 +1515,8 @@ struct AttnPlan {
     uint32_t rows_limit;              // of sz_attn_rows
     uint32_t rows_chunk, rows_splits, tile_chunk, tile_splits, slots, tiles_each;
     uint32_t grid_slots;              // that the launch has: slots, or fewer
-    uint32_t fold;
+    uint32_t fold, row_blocks;
+    bool row_pairs;                   // two products of rows to a workgroup of sz_attn_rows
 };
 
 constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;                // of a launch
@@ -1586,6 +1620,25 @@ inline uint32_t tile_waves(uint32_t dtype, const PagedBatch &b, uint32_t kv_head
 // BF16 90 for 60).
 constexpr bool row_pairs(uint32_t dtype, uint32_t head_dim) { return dtype != SZ_BF16 || head_dim == 64; }
 
+// Whether sz_attn_rows takes all rows of a batch of trees, 16 of them to a
+// workgroup, which read the same keys out of the L2.  Such calls wait for
+// latency, and its workgroups start and join sooner than sz_attn_tiles'.  Over
+// 374 shapes within these limits (1 to 16 sequences, 60 to 3,000 keys, 20 to 800
+// rows, every type) it takes 0.79 of the time, 8 heads of 128, BF16: 13 tokens of
+// four heads over 300 keys 11.3 us (13.6), over 1,000 13.6 (15.2); FP8 over 300
+// 10.7 (15.0).  Over 3,000 keys one workgroup joins more chunks than that saves
+// (20 us for 15), and with twice as much to do the products win (16 sequences of
+// up to 500, 104 rows, BF16: 29 us for 20).
+constexpr uint64_t kBlocksKeys = 2048;
+constexpr uint64_t kBlocksBytes = 1 << 17;       // workgroups times 128-key steps times bytes of a row
+inline uint64_t row_blocks(const PagedBatch &b, uint32_t group) { return ((uint64_t)b.max_new * group + kRowsMax - 1) / kRowsMax; }
+inline bool rows_in_blocks(const sz_cache *c, const PagedBatch &b, uint32_t group)
+{
+    const uint64_t steps = std::max<uint64_t>(1, ((uint64_t)b.max_kv + 127) / 128), row = c->head_dim * (c->dtype == SZ_BF16 ? 2 : 1);
+    return b.max_new <= kRowsTokens && b.max_kv <= kBlocksKeys &&
+           (uint64_t)b.seqs * c->kv_heads * row_blocks(b, group) * steps <= kBlocksBytes / row;
+}
+
 inline AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint32_t window, bool tree)
 {
     AttnPlan p{};
@@ -1599,13 +1652,21 @@ inline AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group
     // rows all go the same way) or every sequence has max_new tokens.
     p.rows = !p.tiles || (b.seqs > 1 && group <= kRowsMax && b.tokens != (uint64_t)b.seqs * b.max_new);
     if (!p.rows) p.rows_limit = 0;
-    p.tile_waves = tile_waves(c->dtype, b, c->kv_heads, group);
+    p.row_blocks = 1;
+    p.row_pairs = p.rows_limit > kRowsMax;
+    if (tree && rows_in_blocks(c, b, group)) {
+        p.rows = true;
+        p.tiles = p.row_pairs = false;
+        p.rows_limit = b.max_new * group;
+        p.row_blocks = (uint32_t)row_blocks(b, group);
+    }
+    p.tile_waves = tree ? 4 : tile_waves(c->dtype, b, c->kv_heads, group);
     p.slots = (uint32_t)std::min<uint64_t>((uint64_t)b.tokens * group / (32 * p.tile_waves) + b.seqs, 0x7FFFFFFFu);
     const uint64_t each = ((uint64_t)b.max_new * group + 32 * p.tile_waves - 1) / (32 * p.tile_waves);
     if (tree && each * b.seqs <= p.slots) p.tiles_each = (uint32_t)each;
     p.rows_splits = p.tile_splits = 1;
     p.rows_chunk = p.tile_chunk = kMinChunk;
-    const uint64_t groups = (uint64_t)b.seqs * c->kv_heads;
+    const uint64_t groups = (uint64_t)b.seqs * c->kv_heads * p.row_blocks;
     const uint64_t values = (uint64_t)b.tokens * group * c->kv_heads * c->head_dim;
     if (p.rows) split_keys(span, rows_wanted(span, groups), p.rows_chunk, p.rows_splits);
     if (p.tiles) {
@@ -1658,7 +1719,7 @@ inline JoinPlan join_plan(const PagedBatch &b, const AttnPlan &p, uint32_t group
 // Whether the launches stay within a launch's threads.
 inline bool launchable(const PagedCache &c, const PagedBatch &b, const AttnPlan &p, const JoinPlan &j)
 {
-    return (!p.rows || (uint64_t)c.heads * b.seqs * p.rows_splits * kAttnThreads <= kMaxThreads) &&
+    return (!p.rows || (uint64_t)c.heads * b.seqs * p.rows_splits * p.row_blocks * kAttnThreads <= kMaxThreads) &&
            (!p.tiles || (uint64_t)c.heads * p.grid_slots * p.tile_splits * 64 * p.tile_waves <= kMaxThreads) &&
            j.groups * kAttnThreads <= kMaxThreads;
 }
@@ -1667,9 +1728,9 @@ template <int DT, int D, typename Args>
 int launch_attention(const Args &a, const AttnPlan &p, const JoinPlan &j, hipStream_t s)
 {
     if (p.rows) {
-        const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits;
+        const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits * p.row_blocks;
         LaunchScope scope("sz_attn_rows", s);
-        if (p.rows_limit <= kRowsMax)
+        if (!p.row_pairs)
             hipLaunchKernelGGL((sz_attn_rows<DT, D, 1, Args>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
         else if constexpr (row_pairs(DT, D))
             hipLaunchKernelGGL((sz_attn_rows<DT, D, 2, Args>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
@@ -1679,7 +1740,7 @@ int launch_attention(const Args &a, const AttnPlan &p, const JoinPlan &j, hipStr
         LaunchScope scope("sz_attn_tiles", s);
         if (p.tile_waves == 4)
             hipLaunchKernelGGL((sz_attn_tiles<DT, D, 4, Args>), dim3((uint32_t)groups), dim3(256), 0, s, a, p.grid_slots);
-        else if constexpr (DT != SZ_BF16)
+        else if constexpr (DT != SZ_BF16 && !Args::kTree)
             hipLaunchKernelGGL((sz_attn_tiles<DT, D, 8, Args>), dim3((uint32_t)groups), dim3(512), 0, s, a, p.grid_slots);
     }
     if (j.groups) {
@@ -1733,6 +1794,7 @@ int attend(Args a, const sz_cache *cache, const sz_batch *batch, const void *d_q
     if constexpr (Args::kTree) {
         a.tiles_each = p.tiles_each;
         a.fold = p.fold;
+        a.row_blocks = p.row_blocks;
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool wide = cache->head_dim == 128;

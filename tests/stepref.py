@@ -84,9 +84,9 @@ def named(masks, tok, first, n):
             if x >> (j - 64 * w) & 1 and first <= j < n]
 
 
-def tree_attention(q, data, scales, table, lens, starts, page, scale, window, masks):
+def tree_attention(q, data, scales, table, lens, starts, page, scale, window, masks, only=None):
     """(out, lse, tol_out, tol_lse) as pagedref.attention, the visible keys by
-    the masks; the bounds are derived there."""
+    the masks; the bounds are derived there.  `only`: the tokens to look at."""
     T, Hq, D = q.shape
     H = data.shape[2]
     u = 2.0 ** -24
@@ -101,6 +101,8 @@ def tree_attention(q, data, scales, table, lens, starts, page, scale, window, ma
         kv = ref.gather(data, scales, table, i, n, page)
         for r in range(s1 - s0):
             at = []
+            if only is not None and s0 + r not in only:
+                continue
             if past + r >= 0:
                 new = named(masks, s0 + r, max(0, -past), s1 - s0)
                 lo = max(0, past + max(1, len(new)) - window) if window else 0

@@ -422,7 +422,13 @@ ATTEND = [  # dtype, H, G, D, page, lens, new, window
 ]
 
 
-def check_tree(case, kind, tight, extra=0):
+def widened(table, page, keys):
+    """The table with columns for so many keys: the launch is shaped for them."""
+    more = -(-keys // page) - table.shape[1]
+    return torch.cat([table, torch.full((len(table), max(0, more)), -7, dtype=torch.int32)], 1)
+
+
+def check_tree(case, kind, tight, extra=0, keys=0):
     dtype, H, G, D, P, lens, new, window = case
     print("attend", ref.NAMES[dtype], case[1:], kind, tight, flush=True)
     m = sz()
@@ -432,8 +438,8 @@ def check_tree(case, kind, tight, extra=0):
     words = max(1, -(-(max(new) if tight else T) // 64)) + extra
     masks = random_masks(lens, new, T, starts, words, g, kind)
     q = torch.randn(T, H * G, D, generator=g).to(torch.bfloat16)
-    bounds = dict(max_new=max(new), max_kv=max(lens)) if tight else {}
-    cache, batch = on_gpu(dtype, data, scales), batch_of(table, kv, starts, T, **bounds)
+    bounds = dict(max_new=max(new), max_kv=max(max(lens), keys)) if tight else {}
+    cache, batch = on_gpu(dtype, data, scales), batch_of(widened(table, P, keys), kv, starts, T, **bounds)
     out = torch.full((T, H * G, D), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((T, H * G), 7.0, device="cuda")
     scale = 0.7 / math.sqrt(D)
@@ -448,8 +454,37 @@ def check_tree(case, kind, tight, extra=0):
 
 @pytest.mark.parametrize("case", ATTEND, ids=lambda c: "%s-%s" % (ref.NAMES[c[0]], "-".join(map(str, c[1:]))))
 @pytest.mark.parametrize("kind", ["tree", "any"])
-def test_tree_attention(case, kind):
-    check_tree(case, kind, True)
+@pytest.mark.parametrize("keys", [0, 2500], ids=["small", "large"])
+def test_tree_attention(case, kind, keys):
+    """Small batches take their rows in blocks of 16, large ones (by the host's
+    bounds) in tiles of 128."""
+    check_tree(case, kind, True, keys=keys)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (E4M3, 128), (E5M2, 64)])
+@pytest.mark.parametrize("seqs", [3, 40, 64, 70])
+def test_tree_attention_of_many_sequences(dtype, D, seqs):
+    """More workgroups than the card holds at once, whose order follows the
+    sequences' lengths (up to 64 of them), equal and empty ones among them."""
+    H, G, P = 8, 4, 16
+    lens = [(37 * i) % 50 + 1 for i in range(seqs)]
+    lens[1] = lens[2] = 50
+    new = [min(33, n) for n in lens]
+    lens[0], new[0] = 0, 0
+    m = sz()
+    g = gen(seqs)
+    table, kv, starts, T, pages = ref.layout(lens, new, P, seed=4)
+    data, scales = filled(dtype, pages, H, P, D, 21)
+    masks = random_masks(lens, new, T, starts, 1, g, "tree")
+    q = torch.randn(T, H * G, D, generator=g).to(torch.bfloat16)
+    # every sequence may have 33 tokens: the axis is padded behind the last
+    batch = batch_of(widened(table, P, 2500), kv, starts, max(T, 33 * seqs), max_new=33, max_kv=2500)
+    pad = lambda t: torch.cat([t, t.new_zeros(max(0, 33 * seqs - T), *t.shape[1:])])
+    out, lse = m.tree_attention(pad(q).cuda(), on_gpu(dtype, data, scales), batch, pad(masks).cuda(), lse=True)
+    keep = torch.arange(0, T, 7)                             # a seventh of the rows against 64 bits
+    want, want_l, tol, tol_l = step.tree_attention(q, data, scales, table, kv, starts, P, D ** -0.5, 0, masks, only=set(keep.tolist()))
+    assert ref.close(out[keep], want[keep], tol[keep]) == ""
+    assert ref.close(lse[keep], want_l[keep], tol_l[keep]) == ""
 
 
 @pytest.mark.parametrize("case", ATTEND[2:9:2], ids=lambda c: "%s-%s" % (ref.NAMES[c[0]], "-".join(map(str, c[1:]))))

@@ -322,4 +322,4 @@ def test_instrumentation_names_the_launches():
     names = m.profile_collect()
     m.profile_enable(False)
     assert {"sz_pages_assign", "sz_draft_tree", "sz_rotary_write", "sz_cache_keep"} <= set(names)
-    assert "sz_attn_tiles" in names
+    assert {"sz_attn_rows", "sz_attn_tiles"} & set(names)
