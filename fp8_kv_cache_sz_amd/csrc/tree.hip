@@ -248,9 +248,10 @@ extern "C" int sz_draft_tree(const sz_batch *batch, const int32_t *d_parents, ui
     a.masks = d_masks;
     a.positions = d_positions;
     a.words = words;
+    const uint32_t blocks = (a.b.max_new + 63) / 64;                 // of a sequence's tokens
+    if ((uint64_t)a.b.seqs * 64 * (blocks <= 4 ? 4 : blocks <= 8 ? 8 : 16) > 0xFFFFFFFFull) return SZ_E_ARG;   // a launch's threads
     hipStream_t s = static_cast<hipStream_t>(stream);
     LaunchScope scope("sz_draft_tree", s);
-    const uint32_t blocks = (a.b.max_new + 63) / 64;                 // of a sequence's tokens
     if (blocks <= 1)
         hipLaunchKernelGGL(sz_draft_tree_one, dim3((a.b.seqs + 3) / 4), dim3(256), 0, s, a);
     else if (blocks <= 2)

@@ -132,6 +132,7 @@ def test_bad_tree_calls_are_refused():
     assert attend(nat, c, many) == ARG and tree(nat, many) == ARG          # 65 tokens do not fit a word
     for kw in (dict(words=0), dict(words=17), dict(parents=None), dict(masks=None), dict(positions=None)):
         assert tree(nat, b, **kw) == ARG, kw
+    assert tree(nat, batch_of(nat, seqs=1 << 24, tokens=1 << 30, max_new=1000), words=16) == ARG   # more threads than a launch has
     for kw in (dict(parents=DUMMY + 2), dict(masks=DUMMY + 4), dict(positions=DUMMY + 1)):
         assert tree(nat, b, **kw) == ALIGN, kw
 
@@ -172,6 +173,32 @@ def test_nothing_to_do_is_no_error():
         assert keep(nat, [c], b) == 0
         assert tree(nat, b, parents=None, masks=None, positions=None) == 0
     assert keep(nat, [c], batch_of(nat), width=0, kept=None, counts=None) == 0
+
+
+def test_attention_workspace_covers_trees_of_many_shapes():
+    """The size that attention_workspace reports is enough for a tree of any
+    window, and a call says so where it is not."""
+    import random
+    nat = _native()
+    rnd = random.Random(3)
+    short = 0
+    for _ in range(600):
+        heads, dim, page = rnd.choice([1, 2, 3, 8]), rnd.choice([64, 128]), rnd.choice([16, 64])
+        c = cache_of(nat, dtype=rnd.choice([0, 1, 2]), kv_heads=heads, head_dim=dim, page_tokens=page)
+        seqs, new = int(2 ** rnd.uniform(0, 9)), int(2 ** rnd.uniform(0, 9))
+        width = int(2 ** rnd.uniform(0, 12))
+        max_kv = max(1, int(width * page * rnd.uniform(0.3, 1)))
+        tokens = max(1, int(seqs * new * rnd.choice([1, rnd.random()])))
+        q_heads = heads * rnd.choice([1, 2, 4, 7, 8])
+        b = batch_of(nat, seqs=seqs, table_width=width, tokens=tokens, max_new=new, max_kv=max_kv)
+        n = nat.lib.sz_paged_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), q_heads)
+        kw = dict(words=8, q_heads=q_heads, token=q_heads * dim, head=dim, out=None)           # no output: the last refusal
+        for window in (0, 1, rnd.randint(1, max_kv), (1 << 31) - 1):
+            assert attend(nat, c, b, ws_bytes=n, window=window, **kw) == ARG
+            least = attend(nat, c, b, ws_bytes=4096, window=window, **kw)
+            assert least in (ARG, WORKSPACE)
+            short += least == WORKSPACE
+    assert short > 100                                       # shapes that are split are among them
 
 
 def small():
