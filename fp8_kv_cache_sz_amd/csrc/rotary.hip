@@ -99,35 +99,60 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// Where a lane's eight values of a row are: two runs of four.  A lane that
-// turns in the half layout holds d = 4 l.. and R/2 + 4 l.., whose pairs are
-// its own; others hold 8 l...
-template <bool HALF>
+// How a lane's eight values of a row lie, and where their partners are.
+//   kPairs   interleaved: d = 8 l.., four pairs
+//   kHalves  half, R a multiple of 16: d = 8 l.., the partners in the lane R/16
+//            away, which has the same sines
+//   kRuns    half, other R: d = 4 l.. and R/2 + 4 l.., four pairs; lanes that do
+//            not turn split what is behind R alike
+// kRuns needs no other lane's values, but its 8-byte pieces are worth less where
+// a run of them is short.  42,000 tokens of 36 heads and 4 of V, FP8, kHalves
+// (kRuns): D = 64 71 us (91), D = 128 R = 64 127 (172), R = 128 127 (127).
+enum Layout { kPairs, kHalves, kRuns };
+
+template <int D, int L>
 __device__ __forceinline__ void lane_runs(uint32_t l, uint32_t dim, bool turns, uint32_t &first, uint32_t &second)
 {
-    first = HALF && turns ? 4 * l : 8 * l;
-    second = HALF && turns ? dim / 2 + 4 * l : 8 * l + 4;
+    first = L != kRuns ? 8 * l : turns ? 4 * l : dim + 4 * (l - dim / 8);
+    second = L != kRuns ? 8 * l + 4 : first + (turns ? dim : D - dim) / 2;
+}
+template <int L>
+constexpr int kSines = L == kHalves ? 8 : 4;             // of a lane
+// The first of the four frequencies whose sines a lane finds.  kHalves: the
+// lanes of two partners find four each of their eight.
+template <int L>
+__device__ __forceinline__ uint32_t frequencies(uint32_t l, uint32_t dim)
+{
+    return L != kHalves ? 4 * l : l < dim / 16 ? 8 * l : 8 * (l - dim / 16) + 4;
 }
 
-// Eight values: runs a and b of four.  Lanes that do not turn keep them (0
-// times an infinity is a NaN).
-template <bool HALF, typename T>
-__device__ __forceinline__ void turn(const uint2 &a, const uint2 &b, bool turns, const T (&s)[4], const T (&c)[4],
-                                     float (&x)[8])
+// Eight values.  Lanes that do not turn keep them (0 times an infinity is a
+// NaN).  kHalves: s has the sign that the partner's value takes.
+template <int L, typename T>
+__device__ __forceinline__ void turn(const uint4 &own, const uint4 &partner, bool turns, const T (&s)[kSines<L>],
+                                     const T (&c)[kSines<L>], float (&x)[8])
 {
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+    const uint32_t w[4] = {own.x, own.y, own.z, own.w}, p[4] = {partner.x, partner.y, partner.z, partner.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         x[2 * e] = low_value(w[e]);
         x[2 * e + 1] = high_value(w[e]);
     }
     float y[8];
+    if constexpr (L == kHalves) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int i = HALF ? e : 2 * e, j = HALF ? e + 4 : 2 * e + 1;
-        const T u = x[i], v = x[j];
-        y[i] = (float)fma(u, c[e], -(v * s[e]));
-        y[j] = (float)fma(v, c[e], u * s[e]);
+        for (int e = 0; e < 8; ++e) {
+            const T v = e % 2 ? high_value(p[e / 2]) : low_value(p[e / 2]);
+            y[e] = (float)fma((T)x[e], c[e], v * s[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = L == kRuns ? e : 2 * e, j = L == kRuns ? e + 4 : 2 * e + 1;
+            const T u = x[i], v = x[j];
+            y[i] = (float)fma(u, c[e], -(v * s[e]));
+            y[j] = (float)fma(v, c[e], u * s[e]);
+        }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = turns ? y[e] : x[e];
@@ -135,14 +160,19 @@ __device__ __forceinline__ void turn(const uint2 &a, const uint2 &b, bool turns,
 
 // Eight values into a row of the cache, runs at `first` and `second`.  All of
 // a row's lanes take part.
-template <int DT, int D>
+template <int DT, int D, int L>
 __device__ __forceinline__ void put_values(const PagedCache &c, uint64_t at, uint32_t first, uint32_t second, bool scale,
                                            const float (&x)[8])
 {
     if constexpr (DT == SZ_BF16) {
         uint16_t *p = reinterpret_cast<uint16_t *>(c.data) + at * D;
-        *reinterpret_cast<uint2 *>(p + first) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
-        *reinterpret_cast<uint2 *>(p + second) = make_uint2(bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+        const uint4 t = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+        if constexpr (L == kRuns) {
+            *reinterpret_cast<uint2 *>(p + first) = make_uint2(t.x, t.y);
+            *reinterpret_cast<uint2 *>(p + second) = make_uint2(t.z, t.w);
+        } else {
+            *reinterpret_cast<uint4 *>(p + first) = t;
+        }
     } else {
         uint32_t a = 0;
 #pragma unroll
@@ -158,8 +188,12 @@ __device__ __forceinline__ void put_values(const PagedCache &c, uint64_t at, uin
         uint32_t w[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e / 2] = fp8_pair<DT>(x[2 * e] * inv, x[2 * e + 1] * inv, w[e / 2], e % 2 == 1);
-        *reinterpret_cast<uint32_t *>(c.data + at * D + first) = w[0];
-        *reinterpret_cast<uint32_t *>(c.data + at * D + second) = w[1];
+        if constexpr (L == kRuns) {
+            *reinterpret_cast<uint32_t *>(c.data + at * D + first) = w[0];
+            *reinterpret_cast<uint32_t *>(c.data + at * D + second) = w[1];
+        } else {
+            *reinterpret_cast<uint2 *>(c.data + at * D + first) = make_uint2(w[0], w[1]);
+        }
         if (scale) c.scales[at] = (uint8_t)byte;
     }
 }
@@ -202,38 +236,56 @@ __device__ __forceinline__ Token find_token(const RotaryArgs &a, uint32_t t0, bo
 }
 
 // Heads [head0, head0 + heads) of a wave's tokens, queries or keys.
-template <int DT, int D, bool HALF, bool QUERIES>
+template <int DT, int D, int L, bool QUERIES>
 __device__ __forceinline__ void turn_heads(const RotaryArgs &a, uint32_t t0, bool edges, uint32_t head0, uint32_t heads)
 {
     using T = typename std::conditional<!QUERIES && DT != SZ_BF16, double, float>::type;
     const uint32_t l = lane_id() % kRowLanes<D>, last = a.b.tokens - 1;
     const bool turns = 8 * l < a.dim;
     uint32_t first, second;
-    lane_runs<HALF>(l, a.dim, turns, first, second);
+    lane_runs<D, L>(l, a.dim, turns, first, second);
     const uint32_t token = min(t0 + lane_id() / kRowLanes<D>, last);
     const uint16_t *from = QUERIES ? a.q + (uint64_t)token * a.q_token + (uint64_t)head0 * a.q_head
                                    : a.k + (uint64_t)token * a.k_token + (uint64_t)head0 * a.k_head;
     const uint64_t step = QUERIES ? a.q_head : a.k_head;
-    uint2 x[kAhead], y[kAhead];
+    uint4 x[kAhead];
     const auto load = [&](uint32_t h0) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const uint16_t *p = from + (uint64_t)min(h0 + j, heads - 1) * step;
-            x[j] = load_nt(reinterpret_cast<const uint2 *>(p + first));
-            y[j] = load_nt(reinterpret_cast<const uint2 *>(p + second));
+            if constexpr (L == kRuns) {
+                const uint2 u = load_nt(reinterpret_cast<const uint2 *>(p + first)), v = load_nt(reinterpret_cast<const uint2 *>(p + second));
+                x[j] = make_uint4(u.x, u.y, v.x, v.y);
+            } else {
+                x[j] = load_nt(reinterpret_cast<const uint4 *>(p + first));
+            }
         }
     };
+    constexpr int SINES = kSines<L>;
     uint64_t f[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = a.turns[turns ? 4 * l + e : 0];
+    for (int e = 0; e < 4; ++e) f[e] = a.turns[turns ? frequencies<L>(l, a.dim) + e : 0];
+    const bool low = l < a.dim / 16;                                     // kHalves: the pairs' first values
+    const int partner = (int)(lane_id() + (!turns ? 0 : low ? a.dim / 16 : 0u - a.dim / 16));
     load(0);
     const Token w = find_token<D, !QUERIES>(a, t0, edges);
-    T s[4], c[4];
+    T s[SINES], c[SINES];
+    const T amplitude = (T)a.amplitude;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         sin_cos<T>(w.turn * f[e], s[e], c[e]);
-        s[e] *= (T)a.amplitude;
-        c[e] *= (T)a.amplitude;
+        s[e] *= amplitude;
+        c[e] *= amplitude;
+    }
+    if constexpr (L == kHalves) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const T u = __shfl(s[e], partner, 64), v = __shfl(c[e], partner, 64);
+            s[e + 4] = low ? -u : s[e];
+            c[e + 4] = low ? v : c[e];
+            s[e] = low ? -s[e] : u;
+            c[e] = low ? c[e] : v;
+        }
     }
     if (!w.there) return;                                                // whole rows: a row's lanes agree
     for (uint32_t h0 = 0;;) {
@@ -241,14 +293,23 @@ __device__ __forceinline__ void turn_heads(const RotaryArgs &a, uint32_t t0, boo
         for (int j = 0; j < kAhead; ++j) {
             if (h0 + j >= heads) break;
             float v[8];
-            turn<HALF, T>(x[j], y[j], turns, s, c, v);
+            uint4 other = x[j];
+            if constexpr (L == kHalves)
+                other = make_uint4((uint32_t)__shfl((int)x[j].x, partner, 64), (uint32_t)__shfl((int)x[j].y, partner, 64),
+                                   (uint32_t)__shfl((int)x[j].z, partner, 64), (uint32_t)__shfl((int)x[j].w, partner, 64));
+            turn<L, T>(x[j], other, turns, s, c, v);
             const uint32_t head = head0 + h0 + j;
             if constexpr (QUERIES) {
                 uint16_t *p = a.out + (uint64_t)w.t * a.out_token + (uint64_t)head * a.out_head;
-                store_nt(reinterpret_cast<uint2 *>(p + first), make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])));
-                store_nt(reinterpret_cast<uint2 *>(p + second), make_uint2(bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])));
+                const uint4 t = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+                if constexpr (L == kRuns) {
+                    store_nt(reinterpret_cast<uint2 *>(p + first), make_uint2(t.x, t.y));
+                    store_nt(reinterpret_cast<uint2 *>(p + second), make_uint2(t.z, t.w));
+                } else {
+                    store_nt(reinterpret_cast<uint4 *>(p + first), t);
+                }
             } else {
-                put_values<DT, D>(a.c, w.place + ((uint64_t)head << a.c.lg_page), first, second, l == 0, v);
+                put_values<DT, D, L>(a.c, w.place + ((uint64_t)head << a.c.lg_page), first, second, l == 0, v);
             }
         }
         h0 += kAhead;
@@ -284,7 +345,7 @@ __device__ __forceinline__ void write_heads(const RotaryArgs &a, uint32_t t0, bo
     }
 }
 
-template <int DT, int D, bool HALF>
+template <int DT, int D, int L>
 __global__ __launch_bounds__(kRotaryThreads) void sz_rotary_move(RotaryArgs a)
 {
     constexpr uint32_t TOKENS = 64 / kRowLanes<D>;
@@ -296,32 +357,35 @@ __global__ __launch_bounds__(kRotaryThreads) void sz_rotary_move(RotaryArgs a)
     uint32_t part = unit % units;
     if (part < a.q_units) {
         const uint32_t head0 = part * a.heads_each;
-        turn_heads<DT, D, HALF, true>(a, t0, unit == 0, head0, min(a.heads_each, a.q_heads - head0));
+        turn_heads<DT, D, L, true>(a, t0, unit == 0, head0, min(a.heads_each, a.q_heads - head0));
         return;
     }
     part -= a.q_units;
     const uint32_t head0 = part % a.kv_units * a.heads_each, heads = min(a.heads_each, a.c.heads - head0);
     if (part < a.kv_units)
-        turn_heads<DT, D, HALF, false>(a, t0, unit == 0, head0, heads);
+        turn_heads<DT, D, L, false>(a, t0, unit == 0, head0, heads);
     else                                                                 // V lies behind K: heads [H, 2 H) of the page
         write_heads<DT, D>(a, t0, false, head0, heads);
 }
 
-template <int DT>
-void launch_rotary(const RotaryArgs &a, uint32_t head_dim, bool half, uint32_t groups, hipStream_t s)
+template <int DT, int D>
+void launch_layout(const RotaryArgs &a, bool interleaved, uint32_t groups, hipStream_t s)
 {
     const dim3 grid(groups), block(kRotaryThreads);
-    if (head_dim == 128) {
-        if (half)
-            hipLaunchKernelGGL((sz_rotary_move<DT, 128, true>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((sz_rotary_move<DT, 128, false>), grid, block, 0, s, a);
-    } else {
-        if (half)
-            hipLaunchKernelGGL((sz_rotary_move<DT, 64, true>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((sz_rotary_move<DT, 64, false>), grid, block, 0, s, a);
-    }
+    if (interleaved)
+        hipLaunchKernelGGL((sz_rotary_move<DT, D, kPairs>), grid, block, 0, s, a);
+    else if (a.dim % 16 == 0)
+        hipLaunchKernelGGL((sz_rotary_move<DT, D, kHalves>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((sz_rotary_move<DT, D, kRuns>), grid, block, 0, s, a);
+}
+template <int DT>
+void launch_rotary(const RotaryArgs &a, uint32_t head_dim, bool interleaved, uint32_t groups, hipStream_t s)
+{
+    if (head_dim == 128)
+        launch_layout<DT, 128>(a, interleaved, groups, s);
+    else
+        launch_layout<DT, 64>(a, interleaved, groups, s);
 }
 
 }  // namespace
@@ -375,10 +439,10 @@ extern "C" int sz_rotary_write(const sz_cache *cache, const sz_batch *batch, con
     hipStream_t s = static_cast<hipStream_t>(stream);
     LaunchScope scope("sz_rotary_write", s);
     if (cache->dtype == SZ_BF16)
-        launch_rotary<SZ_BF16>(a, cache->head_dim, !rotary->interleaved, (uint32_t)groups, s);
+        launch_rotary<SZ_BF16>(a, cache->head_dim, rotary->interleaved != 0, (uint32_t)groups, s);
     else if (cache->dtype == SZ_FP8_E5M2)
-        launch_rotary<SZ_FP8_E5M2>(a, cache->head_dim, !rotary->interleaved, (uint32_t)groups, s);
+        launch_rotary<SZ_FP8_E5M2>(a, cache->head_dim, rotary->interleaved != 0, (uint32_t)groups, s);
     else
-        launch_rotary<SZ_FP8_E4M3>(a, cache->head_dim, !rotary->interleaved, (uint32_t)groups, s);
+        launch_rotary<SZ_FP8_E4M3>(a, cache->head_dim, rotary->interleaved != 0, (uint32_t)groups, s);
     return hipGetLastError() == hipSuccess ? SZ_OK : SZ_E_HIP;
 }
