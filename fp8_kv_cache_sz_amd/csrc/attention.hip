@@ -21,6 +21,10 @@ extern "C" uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, con
     if (p.tiles)
         splits = std::max(splits, most_splits(b.max_kv, tiles_wanted(b.max_kv, (uint64_t)p.slots * cache->kv_heads, p.tile_waves,
                                                                      (uint64_t)b.tokens * q_heads * cache->head_dim)));
+    const AttnPlan t = attn_plan(cache, b, q_heads / cache->kv_heads, 0, true);
+    if (t.tiles)
+        splits = std::max(splits, most_splits(b.max_kv, tiles_wanted(b.max_kv, (uint64_t)t.grid_slots * cache->kv_heads, t.tile_waves,
+                                                                     (uint64_t)b.tokens * q_heads * cache->head_dim)));
     if (rows_in_blocks(cache, b, q_heads / cache->kv_heads))             // trees
         splits = std::max(splits, most_splits(b.max_kv, rows_wanted(b.max_kv, (uint64_t)b.seqs * cache->kv_heads *
                                                                                   row_blocks(b, q_heads / cache->kv_heads))));

@@ -1664,22 +1664,25 @@ inline AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group
     p.slots = (uint32_t)std::min<uint64_t>((uint64_t)b.tokens * group / (32 * p.tile_waves) + b.seqs, 0x7FFFFFFFu);
     const uint64_t each = ((uint64_t)b.max_new * group + 32 * p.tile_waves - 1) / (32 * p.tile_waves);
     if (tree && each * b.seqs <= p.slots) p.tiles_each = (uint32_t)each;
+    p.grid_slots = p.tiles_each ? p.tiles_each * b.seqs : p.slots;
     p.rows_splits = p.tile_splits = 1;
     p.rows_chunk = p.tile_chunk = kMinChunk;
     const uint64_t groups = (uint64_t)b.seqs * c->kv_heads * p.row_blocks;
     const uint64_t values = (uint64_t)b.tokens * group * c->kv_heads * c->head_dim;
     if (p.rows) split_keys(span, rows_wanted(span, groups), p.rows_chunk, p.rows_splits);
     if (p.tiles) {
-        // With a window a tile of rows sees less than its sequence's tokens
+        // Trees count the workgroups that there are, not the slots that other
+        // lengths could need: 16 of up to 8,192, 61 tokens of 32 heads, E4M3 134 us
+        // (173), 30 tokens in BF16 87 (105); 16 of up to 1,500, 30 tokens, BF16 33
+        // (30).  With a window a tile of rows sees less than its sequence's tokens
         // together: no chunks where that would not be split (488 new tokens
         // with a window of 14: one KV head of eight 15 us in chunks, 11
         // without; behind 3,000, four heads of four, 17 and 11).
-        const uint64_t tiles = (uint64_t)p.slots * c->kv_heads, tokens = 32 * p.tile_waves / group + 2;
+        const uint64_t tiles = (uint64_t)p.grid_slots * c->kv_heads, tokens = 32 * p.tile_waves / group + 2;
         const uint64_t seen = window ? std::min(span, window + tokens + kTileKeys) : span;
         const bool split = tiles_wanted(seen, tiles, p.tile_waves, values) > 1;
         split_keys(span, split ? tiles_wanted(span, tiles, p.tile_waves, values) : 1, p.tile_chunk, p.tile_splits);
     }
-    p.grid_slots = p.tiles_each ? p.tiles_each * b.seqs : p.slots;
     // Workgroups of sequences of different lengths, as long as one wave can sort
     // them and more than one comes to a CU: the long ones first, and if no more than
     // two come to a CU, the shortest beside the longest.
