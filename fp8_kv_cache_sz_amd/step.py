@@ -200,8 +200,10 @@ def draft_tree(batch: PageBatch, parents: torch.Tensor, out=None, status: torch.
     else:
         masks, positions = out
         words = _mask_words("out[0]", masks, batch, index)
-        if _ints("out[1]", positions, (tokens,), index) == at:
-            raise ValueError("positions would be written over parents")
+        spans = sorted(((at, 4 * tokens), (_ints("out[1]", positions, (tokens,), index), 4 * tokens),
+                        (masks.data_ptr(), 8 * tokens * words)))
+        if spans[0][0] + spans[0][1] > spans[1][0] or spans[1][0] + spans[1][1] > spans[2][0]:
+            raise ValueError("masks, positions and parents share memory")
     own = None
     if status is None:
         if check:
@@ -293,8 +295,8 @@ class Rotary(_Fixed):
         if dim < 8 or dim % 8 or dim > 128:
             raise ValueError("4, 8, ... or 64 frequencies turn 8, 16, ... or 128 values, got %d" % len(frequencies))
         values = frequencies.double().tolist()
-        if not all(map(math.isfinite, values)) or not math.isfinite(amplitude):
-            raise ValueError("frequencies and amplitude are finite")
+        if not all(map(math.isfinite, values)) or not abs(amplitude) < 2.0 ** 128:
+            raise ValueError("frequencies are finite, amplitude is in 32 bits")
         turns = torch.tensor([_turn(f) for f in values], dtype=torch.int64)
         if device is None:
             device = frequencies.device if frequencies.is_cuda else "cuda"

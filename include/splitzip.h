@@ -442,7 +442,8 @@ int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void 
  *   - d_slots (may be NULL), int64 [tokens]: page * page_tokens + row of each
  *     of the batch's tokens after the call, -1 for tokens without a place (of
  *     no sequence, p < 0, or of no page).
- * A sequence whose length leaves [0, max_kv] or whose d_held leaves [0,
+ * A page has one holder: one that two rows hold would come back twice.  A
+ * sequence whose length leaves [0, max_kv] or whose d_held leaves [0,
  * table_width] is skipped (its d_held_out is its d_held), ends that contradict
  * the ring count as no free pages, and more free pages than the ring has are
  * cut to that many; each sets *d_status to SZ_E_FORMAT.  seqs, table_width,
@@ -498,7 +499,8 @@ int sz_tree_attention(const sz_cache *cache, const sz_batch *batch, const uint64
  *   x' = amplitude (x cos - y sin),  y' = amplitude (y cos + x sin);
  * values from dim on are left.  d_turns[d], uint64 [dim/2] on the device, is
  * the fraction f_d / 2 pi of a turn in units of 2^-64 (modulo 1), so that
- * angles are exact at any position.  dim is a multiple of 8 up to head_dim. */
+ * angles are exact at any position.  dim is a multiple of 8 up to head_dim,
+ * amplitude finite in 32 bits. */
 typedef struct sz_rotary {
     const uint64_t *d_turns;
     uint32_t dim;

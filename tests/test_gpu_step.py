@@ -494,14 +494,15 @@ def test_tree_attention_loose_bounds_and_spare_words(case):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("new", [3, 8, 40, 90])
-def test_chains_are_causal_attention(dtype, new):
+@pytest.mark.parametrize("keys", [0, 2500], ids=["small", "large"])
+def test_chains_are_causal_attention(dtype, new, keys):
     """A tree without branches sees what paged_attention sees."""
     m = sz()
     H, G, D, P = 2, 4, 128, 16
     lens = [new + 300, new, new + 63]
     table, kv, starts, T, pages = ref.layout(lens, [new] * 3, P, seed=4)
     data, scales = filled(dtype, pages, H, P, D, 5)
-    cache, batch = on_gpu(dtype, data, scales), batch_of(table, kv, starts, T, max_new=new)
+    cache, batch = on_gpu(dtype, data, scales), batch_of(widened(table, P, keys), kv, starts, T, max_new=new)
     masks, positions = m.draft_tree(batch, ints([i - 1 for i in range(new)] * 3).cuda())
     assert positions.tolist() == [n - new + i for n in lens for i in range(new)]
     q = torch.randn(T, H * G, D, generator=gen(3)).to(torch.bfloat16).cuda()
@@ -525,7 +526,8 @@ def cache_values(cache):
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("case", [(BF16, 2, 4, 128, 4), (E5M2, 2, 4, 64, 8), (E5M2, 2, 4, 128, 70), (BF16, 1, 4, 64, 45)],
                          ids=str)
-def test_tree_attention_hidden_values_stay_hidden(case, value):
+@pytest.mark.parametrize("keys", [0, 2500], ids=["small", "large"])
+def test_tree_attention_hidden_values_stay_hidden(case, value, keys):
     """NaN and infinities in K and V of branches that a token does not see, of
     tokens that nobody sees, before the window and behind the end."""
     dtype, H, G, D, new = case
@@ -542,8 +544,9 @@ def test_tree_attention_hidden_values_stay_hidden(case, value):
             for x in (range(0, j + 1, 2) if j % 2 == 0 else [j]):
                 masks[s0 + j, x // 64] |= (1 << x % 64) - (2 ** 64 if x % 64 == 63 else 0)
     q = torch.randn(T, H * G, D, generator=g).to(torch.bfloat16)
-    clean = m.tree_attention(q.cuda(), on_gpu(dtype, data, scales), batch_of(table, kv, starts, T, max_new=new), masks.cuda(),
-                             window=window, lse=True)
+    run = lambda d: m.tree_attention(q.cuda(), on_gpu(dtype, d, scales), batch_of(widened(table, P, keys), kv, starts, T, max_new=new),
+                                     masks.cuda(), window=window, lse=True)
+    clean = run(data)
     bad = data.clone()
     def spoil(i, p):
         pg = int(table[i, p // P])
@@ -559,8 +562,7 @@ def test_tree_attention_hidden_values_stay_hidden(case, value):
                 spoil(i, p)
         for p in range(0, max(0, past + 1 - window)):        # no window reaches it
             spoil(i, p)
-    got = m.tree_attention(q.cuda(), on_gpu(dtype, bad, scales), batch_of(table, kv, starts, T, max_new=new), masks.cuda(),
-                           window=window, lse=True)
+    got = run(bad)
     seen = torch.zeros(T, dtype=torch.bool)
     for i in range(2):
         seen[int(starts[i]) + 1] = True

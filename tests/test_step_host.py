@@ -103,7 +103,7 @@ def test_bad_rotary_writes_are_refused():
     c, b = cache_of(nat), batch_of(nat)
     assert write(nat, c, b, None) == ARG
     for kw in (dict(d_turns=None), dict(dim=0), dict(dim=4), dict(dim=12), dict(dim=136), dict(interleaved=2),
-               dict(amplitude=math.nan), dict(amplitude=math.inf)):
+               dict(amplitude=math.nan), dict(amplitude=math.inf), dict(amplitude=1e39)):
         assert write(nat, c, b, rotary_of(nat, **kw)) == ARG, kw
     assert write(nat, cache_of(nat, head_dim=64), b, rotary_of(nat, dim=72)) == ARG
     assert write(nat, c, b, rotary_of(nat, d_turns=DUMMY + 4)) == ALIGN
@@ -218,6 +218,13 @@ def test_python_layer_refuses_trees():
                 (torch.zeros(2, 17, dtype=torch.int64), positions), (masks.expand(2, 2), positions), (masks, parents)):
         with pytest.raises(ValueError):
             sz.draft_tree(batch, parents, out=out, check=False)
+    eight = torch.zeros(8, dtype=torch.int32)
+    for p, out in ((eight[:2], (masks, eight[1:3])), (eight[:2], (eight[:4].view(torch.int64).view(2, 1), positions)),
+                   (parents, (eight[:4].view(torch.int64).view(2, 1), eight[3:5]))):
+        with pytest.raises(ValueError, match="share memory"):
+            sz.draft_tree(batch, p, out=out, check=False)
+    with pytest.raises(ValueError, match="runs on the GPU"):             # side by side
+        sz.draft_tree(batch, eight[:2], out=(eight[2:6].view(torch.int64).view(2, 1), eight[6:8]), check=False)
     for status in (torch.zeros(2, dtype=torch.int32), torch.zeros(1)):
         with pytest.raises(ValueError):
             sz.draft_tree(batch, parents, status=status, check=False)
@@ -247,8 +254,9 @@ def test_python_layer_refuses_rotary():
     for bad in (f[:3], f[None], f.long(), torch.ones(68), torch.tensor([1.0, math.nan, 1.0, 1.0]), f[:0]):
         with pytest.raises(ValueError):
             sz.Rotary(bad, device="cpu")
-    with pytest.raises(ValueError):
-        sz.Rotary(f, amplitude=math.inf, device="cpu")
+    for bad in (math.inf, -math.inf, math.nan, 1e39):
+        with pytest.raises(ValueError):
+            sz.Rotary(f, amplitude=bad, device="cpu")
     with pytest.raises(ValueError):
         sz.Rotary(f.clone().requires_grad_(), device="cpu")
     for bad in (dict(dim=0), dict(dim=7), dict(dim=8, base=0.0), dict(dim=8, stretch=0.0),
