@@ -1565,6 +1565,17 @@ inline uint64_t rows_wanted(uint64_t span, uint64_t groups)
 {
     return std::max(kRowsFill / groups, std::min(kRowsEven / groups, span / kRowsLong));
 }
+// Trees have more rows, whose partials cost more, and every workgroup its start
+// (4 to 5 us): no more of them than one a CU.  Over 676 shapes (1 to 200 sequences,
+// 500 to 32,000 keys, 4 to 32 rows, every type, lengths equal and not) that takes
+// 0.86 of the time of the rule above, 320 as many 0.87, 192 and 384 0.91.  8 KV
+// heads of 128, E5M2, 32 rows: 32 sequences of 2,000 30 us (57), 64 of 4,000 94
+// (122), 64 of up to 4,000 74 (83); 4 rows in BF16, 64 of up to 8,192 255 (220).
+constexpr uint64_t kTreeFill = 256;
+// Up to so many values of partials are joined in the launch: 8 KV heads of 128,
+// E5M2, 4 sequences of 16,000 in 8 chunks, 4 rows 27.5 us (29.1 with a launch), 16
+// rows 30.6 (29.1), 32 rows 38.2 (34.2).
+constexpr uint64_t kTreeJoin = 1 << 14;
 // A chunk's partials cost their way out and back, rows D 8 bytes; its keys are
 // the time that the others do not take.  span / n + rows D n / kPartialKeys is
 // least at n = sqrt(kPartialKeys span / (rows D)).  BF16, 8 KV heads of 128,
@@ -1669,7 +1680,7 @@ inline AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group
     p.rows_chunk = p.tile_chunk = kMinChunk;
     const uint64_t groups = (uint64_t)b.seqs * c->kv_heads * p.row_blocks;
     const uint64_t values = (uint64_t)b.tokens * group * c->kv_heads * c->head_dim;
-    if (p.rows) split_keys(span, rows_wanted(span, groups), p.rows_chunk, p.rows_splits);
+    if (p.rows) split_keys(span, tree ? kTreeFill / groups : rows_wanted(span, groups), p.rows_chunk, p.rows_splits);
     if (p.tiles) {
         // Trees count the workgroups that there are, not the slots that other
         // lengths could need: 16 of up to 8,192, 61 tokens of 32 heads, E4M3 134 us
@@ -1691,6 +1702,8 @@ inline AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group
         p.fold = all <= 2 * cus ? (uint32_t)std::max<uint64_t>(1, cus / ((uint64_t)p.tiles_each * c->kv_heads)) : b.seqs;
     p.fused = p.rows_splits > 1 && p.rows_splits <= kFusedSplits && p.tile_splits == 1 &&
               groups * p.rows_splits <= kFusedGroups;
+    const uint64_t rows = p.row_blocks > 1 ? kRowsMax : std::min<uint64_t>((uint64_t)b.max_new * group, p.rows_limit);
+    if (tree && p.rows_splits * rows * c->head_dim > kTreeJoin) p.fused = false;
     return p;
 }
 
