@@ -74,7 +74,7 @@ struct AttnArgs {
     uint32_t rows_limit;      // sequences of up to so many rows are sz_attn_rows's
     uint32_t rows_chunk, rows_splits;      // keys of a chunk, chunks (sz_attn_rows)
     uint32_t tile_chunk, tile_splits;      // (sz_attn_tiles)
-    static constexpr bool kTree = false;
+    static constexpr bool kTree = false, kOrdered = false;
 };
 
 // Of trees of drafted tokens: the kernels are the same, told apart by their
@@ -85,7 +85,13 @@ struct TreeArgs : AttnArgs {
     uint32_t tiles_each;      // slots of a sequence, 0: as many as its tokens need, and one
     uint32_t fold;            // sequences in the order of their lengths (by_length), 0: in their own
     uint32_t row_blocks;      // of a sequence's rows in sz_attn_rows
+    uint32_t rows_fold;       // as fold, where sz_attn_rows takes OrderedArgs
     static constexpr bool kTree = true;
+};
+// sz_attn_rows with its sequences in the order of their lengths.  A kernel of its
+// own: finding the order costs the others 1.2 us.
+struct OrderedArgs : TreeArgs {
+    static constexpr bool kOrdered = true;
 };
 
 // First key of sequence s that any of its new tokens sees, rounded down.
@@ -441,6 +447,23 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, uint32_t head, co
     }
 }
 
+// The k-th of up to 64 sequences by length: the longest `fold` first, longest
+// in front, then the others, shortest in front.  One wave, a lane each; equal
+// lengths, and those past 2^25, in their own order.  No loop: with a block of
+// code in front, sz_attn_rows spilled 13 to 63 registers.
+__device__ __forceinline__ uint32_t by_length(const PagedBatch &b, uint32_t k, uint32_t fold)
+{
+    const uint32_t lane = lane_id();
+    const int32_t len = min(max(b.lens[min(lane, b.seqs - 1)], 0), (1 << 25) - 1);
+    const int32_t key = lane < b.seqs ? len << 6 | (int32_t)(63 - lane) : -1;
+    uint32_t rank = 0;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) rank += __builtin_amdgcn_readlane(key, j) > key ? 1 : 0;
+    const uint32_t at = k >= fold ? b.seqs - 1 - (k - fold) : k;
+    const uint64_t mine = __ballot(lane < b.seqs && rank == at);
+    return (uint32_t)__builtin_ctzll(mine);
+}
+
 template <int DT, int D, int NB, typename Args>
 __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void sz_attn_rows(Args a)
 {
@@ -463,7 +486,9 @@ __global__ __launch_bounds__(kAttnThreads, NB == 2 ? 2 : D == 64 ? 4 : 3) void s
         row0 = unit % a.row_blocks * ROWS;
         unit /= a.row_blocks;
     }
-    const uint32_t seq = unit % a.b.seqs, split = unit / a.b.seqs;
+    uint32_t seq = unit % a.b.seqs;
+    const uint32_t split = unit / a.b.seqs;
+    if constexpr (Args::kOrdered) seq = by_length(a.b, seq, a.rows_fold);
     const Sequence s = sequence(a.b, seq);
     const uint64_t all_rows = (uint64_t)s.n * a.group;
     if (TREE ? all_rows <= row0 || all_rows > a.rows_limit : all_rows == 0 || all_rows > min(a.rows_limit, ROWS)) return;
@@ -1025,23 +1050,6 @@ __device__ __forceinline__ bf16x8 v_operand(LdsPtr v, uint32_t place, uint32_t b
     return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// The k-th of up to 64 sequences by length: the longest `fold` first, longest
-// in front, then the others, shortest in front.  One wave; equal lengths in
-// their own order.
-__device__ __forceinline__ uint32_t by_length(const PagedBatch &b, uint32_t k, uint32_t fold)
-{
-    const uint32_t lane = lane_id();
-    const int32_t len = lane < b.seqs ? b.lens[lane] : INT32_MIN;
-    uint32_t rank = 0;
-    for (uint32_t j = 0; j < b.seqs; ++j) {
-        const int32_t other = __builtin_amdgcn_readlane(len, (int)j);
-        rank += other > len || (other == len && j < lane) ? 1 : 0;
-    }
-    if (k >= fold) k = b.seqs - 1 - (k - fold);
-    const uint64_t mine = __ballot(lane < b.seqs && rank == k);
-    return (uint32_t)__builtin_ctzll(mine);
-}
-
 template <int DT, int D, int WAVES, typename Args>
 __global__ __launch_bounds__(64 * WAVES, 2) void sz_attn_tiles(Args a, uint32_t slots)
 {
@@ -1515,7 +1523,7 @@ struct AttnPlan {
     uint32_t rows_limit;              // of sz_attn_rows
     uint32_t rows_chunk, rows_splits, tile_chunk, tile_splits, slots, tiles_each;
     uint32_t grid_slots;              // that the launch has: slots, or fewer
-    uint32_t fold, row_blocks;
+    uint32_t fold, rows_fold, row_blocks;
     bool row_pairs;                   // two products of rows to a workgroup of sz_attn_rows
 };
 
@@ -1650,6 +1658,19 @@ inline bool rows_in_blocks(const sz_cache *c, const PagedBatch &b, uint32_t grou
            (uint64_t)b.seqs * c->kv_heads * row_blocks(b, group) * steps <= kBlocksBytes / row;
 }
 
+// How trees' workgroups, `each` of a sequence, follow the sequences' lengths, as
+// far as one wave can sort them and more than one comes to a CU (0: not): the long
+// ones first, and if no more than two come to a CU, the shortest beside the longest.
+// 64 trees of 8 tokens over up to 4,000 keys, 8 KV heads, E5M2 59 us (77), 50 of up
+// to 12,000 143 (205), 24 of up to 8,000 with 16 heads 96 (131); equal lengths the
+// same.
+inline uint32_t fold_of(const PagedBatch &b, uint64_t each, uint64_t cus)
+{
+    const uint64_t all = each * b.seqs;
+    if (b.seqs < 2 || b.seqs > 64 || all <= cus) return 0;
+    return all <= 2 * cus ? (uint32_t)std::max<uint64_t>(1, cus / each) : b.seqs;
+}
+
 inline AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group, uint32_t window, bool tree)
 {
     AttnPlan p{};
@@ -1694,12 +1715,8 @@ inline AttnPlan attn_plan(const sz_cache *c, const PagedBatch &b, uint32_t group
         const bool split = tiles_wanted(seen, tiles, p.tile_waves, values) > 1;
         split_keys(span, split ? tiles_wanted(span, tiles, p.tile_waves, values) : 1, p.tile_chunk, p.tile_splits);
     }
-    // Workgroups of sequences of different lengths, as long as one wave can sort
-    // them and more than one comes to a CU: the long ones first, and if no more than
-    // two come to a CU, the shortest beside the longest.
-    const uint64_t all = (uint64_t)p.grid_slots * c->kv_heads, cus = 256 * 4 / p.tile_waves;
-    if (p.tiles_each && p.tile_splits == 1 && b.seqs > 1 && b.seqs <= 64 && all > cus)
-        p.fold = all <= 2 * cus ? (uint32_t)std::max<uint64_t>(1, cus / ((uint64_t)p.tiles_each * c->kv_heads)) : b.seqs;
+    if (p.tiles_each && p.tile_splits == 1) p.fold = fold_of(b, (uint64_t)p.tiles_each * c->kv_heads, 256 * 4 / p.tile_waves);
+    if (tree && p.rows && p.rows_splits == 1) p.rows_fold = fold_of(b, (uint64_t)c->kv_heads * p.row_blocks, 256);
     p.fused = p.rows_splits > 1 && p.rows_splits <= kFusedSplits && p.tile_splits == 1 &&
               groups * p.rows_splits <= kFusedGroups;
     const uint64_t rows = p.row_blocks > 1 ? kRowsMax : std::min<uint64_t>((uint64_t)b.max_new * group, p.rows_limit);
@@ -1746,10 +1763,21 @@ int launch_attention(const Args &a, const AttnPlan &p, const JoinPlan &j, hipStr
     if (p.rows) {
         const uint64_t groups = (uint64_t)a.c.heads * a.b.seqs * p.rows_splits * p.row_blocks;
         LaunchScope scope("sz_attn_rows", s);
-        if (!p.row_pairs)
-            hipLaunchKernelGGL((sz_attn_rows<DT, D, 1, Args>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
-        else if constexpr (row_pairs(DT, D))
-            hipLaunchKernelGGL((sz_attn_rows<DT, D, 2, Args>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, a);
+        const auto launch = [&](const auto &args) {
+            using A = std::decay_t<decltype(args)>;
+            if (!p.row_pairs)
+                hipLaunchKernelGGL((sz_attn_rows<DT, D, 1, A>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, args);
+            else if constexpr (row_pairs(DT, D))
+                hipLaunchKernelGGL((sz_attn_rows<DT, D, 2, A>), dim3((uint32_t)groups), dim3(kAttnThreads), 0, s, args);
+        };
+        if constexpr (Args::kTree) {
+            if (p.rows_fold)
+                launch(OrderedArgs{a});
+            else
+                launch(a);
+        } else {
+            launch(a);
+        }
     }
     if (p.tiles) {
         const uint64_t groups = (uint64_t)a.c.heads * p.grid_slots * p.tile_splits;
@@ -1811,6 +1839,7 @@ int attend(Args a, const sz_cache *cache, const sz_batch *batch, const void *d_q
         a.tiles_each = p.tiles_each;
         a.fold = p.fold;
         a.row_blocks = p.row_blocks;
+        a.rows_fold = p.rows_fold;
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool wide = cache->head_dim == 128;

@@ -487,6 +487,30 @@ def test_tree_attention_of_many_sequences(dtype, D, seqs):
     assert ref.close(lse[keep], want_l[keep], tol_l[keep]) == ""
 
 
+@pytest.mark.parametrize("dtype,D,H,new,keys", [(E5M2, 128, 8, 8, 2500), (BF16, 128, 8, 4, 2500), (BF16, 64, 8, 8, 2500),
+                                                (E4M3, 64, 8, 2, 2500), (E4M3, 128, 4, 8, 120), (BF16, 64, 8, 9, 60)])
+@pytest.mark.parametrize("seqs", [33, 64, 65])
+def test_few_rows_of_many_sequences(dtype, D, H, new, keys, seqs):
+    """As above for rows that one workgroup takes, and for several blocks of 16."""
+    G, P = 4, 16
+    lens = [(37 * i) % 57 + 1 for i in range(seqs)]
+    lens[1] = lens[2] = 57
+    take = [min(new, n) for n in lens]
+    lens[0], take[0] = 0, 0
+    m = sz()
+    g = gen(seqs)
+    table, kv, starts, T, pages = ref.layout(lens, take, P, seed=4)
+    data, scales = filled(dtype, pages, H, P, D, 21)
+    masks = random_masks(lens, take, T, starts, 1, g, "tree")
+    q = torch.randn(T, H * G, D, generator=g).to(torch.bfloat16)
+    batch = batch_of(widened(table, P, keys), kv, starts, T, max_new=new, max_kv=keys)
+    out, lse = m.tree_attention(q.cuda(), on_gpu(dtype, data, scales), batch, masks.cuda(), lse=True)
+    keep = torch.arange(0, T, 3)
+    want, want_l, tol, tol_l = step.tree_attention(q, data, scales, table, kv, starts, P, D ** -0.5, 0, masks, only=set(keep.tolist()))
+    assert ref.close(out[keep], want[keep], tol[keep]) == ""
+    assert ref.close(lse[keep], want_l[keep], tol_l[keep]) == ""
+
+
 @pytest.mark.parametrize("case", ATTEND[2:9:2], ids=lambda c: "%s-%s" % (ref.NAMES[c[0]], "-".join(map(str, c[1:]))))
 def test_tree_attention_loose_bounds_and_spare_words(case):
     check_tree(case, "any", False, extra=2)
