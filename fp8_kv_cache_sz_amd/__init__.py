@@ -8,7 +8,8 @@ run in the library.  Tensors:
 * FP8 E5M2 data: ``torch.float8_e5m2`` or ``uint8`` tensors of raw bytes.
 * Streams: ``uint8`` device tensors.
 * Paged caches: ``[pages, 2, kv_heads, page_tokens, head_dim]`` tensors of
-  BF16, E5M2 or E4M3 (paged.py).
+  BF16, E5M2 or E4M3 (paged.py), and a serving step around them: pages, trees
+  of drafted tokens, rotary positions (step.py).
 """
 from __future__ import annotations
 

@@ -31,6 +31,19 @@
 //                 vector units.
 // Where there are few rows the keys are split into chunks whose partial
 // (m, l, o) sz_attn_join joins, always in the order of the chunks.
+//
+// Trees (TreeArgs) differ in what hides a score: cached keys j < len - n are seen
+// as by a causal token, of the n new ones those that the row's mask names.  So
+// only the blocks and tiles that reach the new tokens (or a window's start) look at
+// masks, 64 keys at a time, as one shifted 64-bit word of the row; all others run
+// the causal code.  A row's causal order is gone, which leaves equal work to all
+// tiles of a sequence, and room for other plans: equal slots (tiles_each), long
+// sequences first (fold_of), fewer and longer chunks (kTreeFill), small batches in
+// blocks of 16 rows (rows_in_blocks).  Measured (MI355X, 8 KV heads of 128, four
+// query heads each): 64 trees of 8 tokens over up to 4,000 keys, E5M2 58 us, 5.3
+// TB/s; 32 of 61 over up to 8,192, E4M3 200 us, 738 TFLOP/s (32 over 8,192 each 309
+// us, 849); 13 tokens over 1,000 in BF16 12.7 us, which is a chain of launch,
+// lengths, masks, page, K and V, join.
 #pragma once
 
 #include "paged.hpp"
@@ -1528,7 +1541,7 @@ struct AttnPlan {
 };
 
 constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;                // of a launch
-// Workgroups that sz_attn_rows wants: enough to fill the card (768 run at a
+// Workgroups that sz_attn_rows wants, but for trees: enough to fill the card (768 run at a
 // time, and some chunks are behind their sequence's end), and up to kRowsEven
 // while their chunks have kRowsLong keys, to even out lengths.  Against 2,048
 // whatever the chunk's length (8 KV heads of 128, four query heads each): 128

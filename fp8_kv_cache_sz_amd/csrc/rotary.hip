@@ -22,7 +22,9 @@
 // worked out once for the heads.  Its first rows are on their way before it
 // looks up whose its tokens are.  Bound by HBM in the large, in the small by the
 // latency of loads that wait for each other (starts and lengths, page or
-// position, the store).
+// position, the store).  Measured (MI355X): 32,254 tokens of prompts, 32 + 8 heads
+// of 128, E5M2 (727 MB) 111.5 us, 6.5 TB/s, what a large copy reaches; 64 trees of
+// up to 24 tokens, 28 + 4 heads in BF16 (28 MB) 8.7 us; one token 6.6 us on the GPU.
 #include "paged.hpp"
 
 #include <cmath>
