@@ -311,8 +311,8 @@ def cache_read(cache: PagedCache, batch: PageBatch, out=None, stream=None, check
 
 
 def attention_workspace(cache: PagedCache, batch: PageBatch, q_heads: int) -> torch.Tensor:
-    """A workspace for ``paged_attention`` of this batch's bounds, with any
-    window.  Its first ``ARRIVALS`` bytes are zero, as every call leaves them
+    """A workspace for ``paged_attention`` and ``tree_attention`` of this batch's
+    bounds, with any window.  Its first ``ARRIVALS`` bytes are zero, as every call leaves them
     (they are cleared on the current stream, before any call that uses it)."""
     if q_heads <= 0 or q_heads % cache.kv_heads:
         raise ValueError("q_heads is a multiple of the cache's %d KV heads, got %d" % (cache.kv_heads, q_heads))

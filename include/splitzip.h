@@ -451,8 +451,8 @@ int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void 
  * at most max_new tokens.  d_ws: ws_bytes >=
  * sz_pages_assign_workspace_size(batch); its first SZ_ASSIGN_COUNTERS bytes
  * are cleared once by the caller, and every call finds and leaves them 0.
- * pages <= 2^30.  Calls that share
- * a pool, a table or a workspace must not overlap. */
+ * pages <= 2^30.  Calls that share a pool, a table or a workspace must not
+ * overlap. */
 typedef struct sz_pool {
     uint32_t page_tokens;
     uint32_t pages;
@@ -519,8 +519,9 @@ typedef struct sz_rotary {
  * once to BF16 for BF16 caches (32 bits before that); for FP8 caches they are
  * computed in 64 bits, rounded to 32 and then quantised as sz_cache_write
  * quantises.  Values are written as sz_cache_write writes them.  Rows of
- * d_out of tokens without a place stay as they are.  Return codes as
- * sz_cache_write. */
+ * d_out of tokens of no sequence, or with p < 0, stay as they are; a token whose
+ * page is none of the cache's has its query turned, and SZ_E_FORMAT reported.
+ * Return codes as sz_cache_write. */
 int sz_rotary_write(const sz_cache *cache, const sz_batch *batch, const sz_rotary *rotary, const int32_t *d_positions,
                     const void *d_q, uint32_t q_heads, uint64_t q_token_stride, uint64_t q_head_stride, void *d_out,
                     uint64_t out_token_stride, uint64_t out_head_stride, const void *d_k, uint64_t k_token_stride,
