@@ -1663,7 +1663,10 @@ constexpr bool row_pairs(uint32_t dtype, uint32_t head_dim) { return dtype != SZ
 // up to 500, 104 rows, BF16: 29 us for 20).
 constexpr uint64_t kBlocksKeys = 2048;
 constexpr uint64_t kBlocksBytes = 1 << 17;       // workgroups times 128-key steps times bytes of a row
-inline uint64_t row_blocks(const PagedBatch &b, uint32_t group) { return ((uint64_t)b.max_new * group + kRowsMax - 1) / kRowsMax; }
+inline uint64_t row_blocks(const PagedBatch &b, uint32_t group)             // one also for no rows at all
+{
+    return std::max<uint64_t>(1, ((uint64_t)b.max_new * group + kRowsMax - 1) / kRowsMax);
+}
 inline bool rows_in_blocks(const sz_cache *c, const PagedBatch &b, uint32_t group)
 {
     const uint64_t steps = std::max<uint64_t>(1, ((uint64_t)b.max_kv + 127) / 128), row = c->head_dim * (c->dtype == SZ_BF16 ? 2 : 1);

@@ -2,6 +2,7 @@
 the Python layer (nothing is launched), the ends of what a tree's masks and
 frequencies may be, and the test reference against hand-worked values."""
 import ctypes
+import itertools
 import math
 
 import pytest
@@ -199,6 +200,20 @@ def test_attention_workspace_covers_trees_of_many_shapes():
             assert least in (ARG, WORKSPACE)
             short += least == WORKSPACE
     assert short > 100                                       # shapes that are split are among them
+
+
+def test_bounds_of_nothing_are_planned():
+    """Bounds that leave no new token, no key or one of them: the size covers
+    the call, which goes as far as its last refusal."""
+    nat = _native()
+    for dtype, heads, dim in itertools.product((0, 1, 2), (1, 1024), (64, 128)):
+        c = cache_of(nat, dtype=dtype, kv_heads=heads, head_dim=dim)
+        for seqs, tokens, new, max_kv, group in itertools.product((1, 3, 1 << 24), (1, 5), (0, 1), (0, 1, 16), (1, 63)):
+            b = batch_of(nat, seqs=seqs, tokens=tokens, max_new=new, max_kv=max_kv)
+            q_heads = heads * group
+            n = nat.lib.sz_paged_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), q_heads)
+            assert n >= 4096
+            assert attend(nat, c, b, ws_bytes=n, q_heads=q_heads, token=q_heads * dim, head=dim, out=None) == ARG
 
 
 def small():
