@@ -460,21 +460,33 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, uint32_t head, co
     }
 }
 
-// The k-th of up to 64 sequences by length: the longest `fold` first, longest
-// in front, then the others, shortest in front.  One wave, a lane each; equal
-// lengths, and those past 2^25, in their own order.  No loop: with a block of
-// code in front, sz_attn_rows spilled 13 to 63 registers.
+// The k-th of up to kOrdered sequences by length: the longest `fold` first,
+// longest in front, then the others, shortest in front; equal lengths, and those
+// past 2^23, in their own order.  The largest key that more than k keys reach, bit
+// by bit.  No loop: with a block of code in front, sz_attn_rows spilled 13 to 63
+// registers.
+constexpr uint32_t kOrdered = 256;
 __device__ __forceinline__ uint32_t by_length(const PagedBatch &b, uint32_t k, uint32_t fold)
 {
-    const uint32_t lane = lane_id();
-    const int32_t len = min(max(b.lens[min(lane, b.seqs - 1)], 0), (1 << 25) - 1);
-    const int32_t key = lane < b.seqs ? len << 6 | (int32_t)(63 - lane) : -1;
-    uint32_t rank = 0;
+    constexpr int EACH = kOrdered / 64;
+    int32_t key[EACH];
 #pragma unroll
-    for (int j = 0; j < 64; ++j) rank += __builtin_amdgcn_readlane(key, j) > key ? 1 : 0;
+    for (int e = 0; e < EACH; ++e) {
+        const uint32_t i = lane_id() + 64 * e;
+        const int32_t len = min(max(b.lens[min(i, b.seqs - 1)], 0), (1 << 23) - 1);
+        key[e] = i < b.seqs ? len << 8 | (int32_t)(kOrdered - 1 - i) : -1;
+    }
     const uint32_t at = k >= fold ? b.seqs - 1 - (k - fold) : k;
-    const uint64_t mine = __ballot(lane < b.seqs && rank == at);
-    return (uint32_t)__builtin_ctzll(mine);
+    uint32_t found = 0;
+#pragma unroll
+    for (int bit = 30; bit >= 0; --bit) {
+        const uint32_t next = found | 1u << bit;
+        uint32_t reach = 0;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) reach += (uint32_t)__popcll(__ballot(key[e] >= (int32_t)next));
+        found = reach > at ? next : found;
+    }
+    return kOrdered - 1 - found % kOrdered;
 }
 
 template <int DT, int D, int NB, typename Args>
@@ -1677,13 +1689,13 @@ inline bool rows_in_blocks(const sz_cache *c, const PagedBatch &b, uint32_t grou
 // How trees' workgroups, `each` of a sequence, follow the sequences' lengths, as
 // far as one wave can sort them and more than one comes to a CU (0: not): the long
 // ones first, and if no more than two come to a CU, the shortest beside the longest.
-// 64 trees of 8 tokens over up to 4,000 keys, 8 KV heads, E5M2 59 us (77), 50 of up
-// to 12,000 143 (205), 24 of up to 8,000 with 16 heads 96 (131); equal lengths the
-// same.
+// 64 trees of 8 tokens over up to 4,000 keys, 8 KV heads, E5M2 59 us (77), 128 of up
+// to 8,000 227 (279), of up to 1,000 48 (51), 24 of up to 8,000 with 16 heads 96
+// (131); 30 tokens in BF16, 128 of up to 8,000 453 (522); equal lengths the same.
 inline uint32_t fold_of(const PagedBatch &b, uint64_t each, uint64_t cus)
 {
     const uint64_t all = each * b.seqs;
-    if (b.seqs < 2 || b.seqs > 64 || all <= cus) return 0;
+    if (b.seqs < 2 || b.seqs > kOrdered || all <= cus) return 0;
     return all <= 2 * cus ? (uint32_t)std::max<uint64_t>(1, cus / each) : b.seqs;
 }
 

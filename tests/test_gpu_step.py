@@ -462,10 +462,10 @@ def test_tree_attention(case, kind, keys):
 
 
 @pytest.mark.parametrize("dtype,D", [(BF16, 128), (E4M3, 128), (E5M2, 64)])
-@pytest.mark.parametrize("seqs", [3, 40, 64, 70])
+@pytest.mark.parametrize("seqs", [3, 40, 64, 70, 200])
 def test_tree_attention_of_many_sequences(dtype, D, seqs):
     """More workgroups than the card holds at once, whose order follows the
-    sequences' lengths (up to 64 of them), equal and empty ones among them."""
+    sequences' lengths, equal and empty ones among them."""
     H, G, P = 8, 4, 16
     lens = [(37 * i) % 50 + 1 for i in range(seqs)]
     lens[1] = lens[2] = 50
@@ -481,7 +481,7 @@ def test_tree_attention_of_many_sequences(dtype, D, seqs):
     batch = batch_of(widened(table, P, 2500), kv, starts, max(T, 33 * seqs), max_new=33, max_kv=2500)
     pad = lambda t: torch.cat([t, t.new_zeros(max(0, 33 * seqs - T), *t.shape[1:])])
     out, lse = m.tree_attention(pad(q).cuda(), on_gpu(dtype, data, scales), batch, pad(masks).cuda(), lse=True)
-    keep = torch.arange(0, T, 7)                             # a seventh of the rows against 64 bits
+    keep = torch.arange(0, T, max(7, T // 250))              # some rows against 64 bits
     want, want_l, tol, tol_l = step.tree_attention(q, data, scales, table, kv, starts, P, D ** -0.5, 0, masks, only=set(keep.tolist()))
     assert ref.close(out[keep], want[keep], tol[keep]) == ""
     assert ref.close(lse[keep], want_l[keep], tol_l[keep]) == ""
@@ -489,7 +489,7 @@ def test_tree_attention_of_many_sequences(dtype, D, seqs):
 
 @pytest.mark.parametrize("dtype,D,H,new,keys", [(E5M2, 128, 8, 8, 2500), (BF16, 128, 8, 4, 2500), (BF16, 64, 8, 8, 2500),
                                                 (E4M3, 64, 8, 2, 2500), (E4M3, 128, 4, 8, 120), (BF16, 64, 8, 9, 60)])
-@pytest.mark.parametrize("seqs", [33, 64, 65])
+@pytest.mark.parametrize("seqs", [33, 64, 65, 130, 256, 257])
 def test_few_rows_of_many_sequences(dtype, D, H, new, keys, seqs):
     """As above for rows that one workgroup takes, and for several blocks of 16."""
     G, P = 4, 16
@@ -505,7 +505,7 @@ def test_few_rows_of_many_sequences(dtype, D, H, new, keys, seqs):
     q = torch.randn(T, H * G, D, generator=g).to(torch.bfloat16)
     batch = batch_of(widened(table, P, keys), kv, starts, T, max_new=new, max_kv=keys)
     out, lse = m.tree_attention(q.cuda(), on_gpu(dtype, data, scales), batch, masks.cuda(), lse=True)
-    keep = torch.arange(0, T, 3)
+    keep = torch.arange(0, T, max(3, T // 150))
     want, want_l, tol, tol_l = step.tree_attention(q, data, scales, table, kv, starts, P, D ** -0.5, 0, masks, only=set(keep.tolist()))
     assert ref.close(out[keep], want[keep], tol[keep]) == ""
     assert ref.close(lse[keep], want_l[keep], tol_l[keep]) == ""
