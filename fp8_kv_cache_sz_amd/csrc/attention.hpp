@@ -102,7 +102,7 @@ struct TreeArgs : AttnArgs {
     static constexpr bool kTree = true;
 };
 // sz_attn_rows with its sequences in the order of their lengths.  A kernel of its
-// own: finding the order costs the others 1.2 us.
+// own: finding the order costs a small call 1.6 us of 14.
 struct OrderedArgs : TreeArgs {
     static constexpr bool kOrdered = true;
 };
