@@ -4,9 +4,17 @@
 
 using namespace sz;
 
+// A size is asked for before any call has looked at the fields, and the plan's
+// divisions and products hold within what the calls take: nothing else has one.
+static bool has_plan(const sz_cache *c, const sz_batch *b, uint32_t q_heads)
+{
+    return c && b && check_rows_type(c->dtype, c->head_dim) == SZ_OK && c->kv_heads > 0 && c->kv_heads <= kMaxHeads &&
+           q_heads > 0 && q_heads <= kMaxQueryHeads && q_heads % c->kv_heads == 0 && check_counts(b) == SZ_OK;
+}
+
 extern "C" uint64_t sz_paged_attention_workspace_size(const sz_cache *cache, const sz_batch *batch, uint32_t q_heads)
 {
-    if (!cache || !batch || cache->kv_heads == 0 || q_heads == 0 || q_heads % cache->kv_heads) return 0;
+    if (!has_plan(cache, batch, q_heads)) return 0;
     PagedBatch b{};
     b.seqs = batch->seqs;
     b.tokens = batch->tokens;

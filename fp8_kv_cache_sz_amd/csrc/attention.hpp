@@ -1831,7 +1831,7 @@ int attend(Args a, const sz_cache *cache, const sz_batch *batch, const void *d_q
 {
     int rc = check_paged(cache, batch, d_status, a.c, a.b);
     if (rc != SZ_OK) return rc;
-    if (q_heads == 0 || q_heads > 0xFFFFu || q_heads % a.c.heads) return SZ_E_ARG;
+    if (q_heads == 0 || q_heads > kMaxQueryHeads || q_heads % a.c.heads) return SZ_E_ARG;
     a.c2 = scale * 1.44269504088896340736f;
     if (!(scale > 0.f) || !std::isfinite(a.c2) || window > 0x7FFFFFFFu) return SZ_E_ARG;
     if ((rc = check_rows(d_q, q_token_stride, q_head_stride, a.b.tokens, q_heads)) != SZ_OK) return rc;

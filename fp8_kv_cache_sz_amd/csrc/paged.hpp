@@ -39,13 +39,24 @@ struct Sequence {
 };
 
 constexpr uint32_t kMinPage = 16, kMaxPage = 1024;
-constexpr uint32_t kMaxHeads = 1024;
+constexpr uint32_t kMaxHeads = 1024, kMaxQueryHeads = 0xFFFF;
+
+// Host checks of single fields, which sizes of workspaces share.
+inline int check_rows_type(uint32_t dtype, uint32_t head_dim)
+{
+    if (dtype != SZ_BF16 && dtype != SZ_FP8_E5M2 && dtype != SZ_FP8_E4M3) return SZ_E_DTYPE;
+    return head_dim == 64 || head_dim == 128 ? SZ_OK : SZ_E_ARG;
+}
+inline int check_counts(const sz_batch *b)
+{
+    return b->seqs > (1u << 24) || b->tokens > kMaxTokens || b->max_kv > kMaxTokens ? SZ_E_ARG : SZ_OK;
+}
 
 // Host checks of a batch by itself, and of its pages' size (no device memory
 // is touched).
 inline int check_batch(const sz_batch *b, const int32_t *d_status, PagedBatch &pb)
 {
-    if (b->seqs > (1u << 24) || b->tokens > kMaxTokens || b->max_kv > kMaxTokens) return SZ_E_ARG;
+    if (check_counts(b) != SZ_OK) return SZ_E_ARG;
     if (b->seqs && (!b->starts || !b->kv_lens || (b->table_width && !b->page_table))) return SZ_E_ARG;
     for (const void *p : {(const void *)b->page_table, (const void *)b->kv_lens, (const void *)b->starts,
                           (const void *)d_status})
@@ -65,8 +76,8 @@ inline int page_size(uint32_t page_tokens, uint32_t &lg)
 inline int check_paged(const sz_cache *c, const sz_batch *b, const int32_t *d_status, PagedCache &pc, PagedBatch &pb)
 {
     if (!c || !b) return SZ_E_ARG;
-    if (c->dtype != SZ_BF16 && c->dtype != SZ_FP8_E5M2 && c->dtype != SZ_FP8_E4M3) return SZ_E_DTYPE;
-    if (c->head_dim != 64 && c->head_dim != 128) return SZ_E_ARG;
+    const int type = check_rows_type(c->dtype, c->head_dim);
+    if (type != SZ_OK) return type;
     uint32_t lg = 0;
     if (page_size(c->page_tokens, lg) != SZ_OK) return SZ_E_ARG;
     if (c->kv_heads == 0 || c->kv_heads > kMaxHeads || c->pages == 0 || c->pages > 0x7FFFFFFFull || !c->data)

@@ -405,7 +405,7 @@ extern "C" int sz_rotary_write(const sz_cache *cache, const sz_batch *batch, con
     int rc = check_paged(cache, batch, d_status, a.c, a.b);
     if (rc != SZ_OK) return rc;
     if (!rotary || rotary->dim < 8 || rotary->dim % 8 || rotary->dim > cache->head_dim || !rotary->d_turns) return SZ_E_ARG;
-    if (rotary->interleaved > 1 || !std::isfinite((float)rotary->amplitude) || q_heads > 0xFFFFu) return SZ_E_ARG;
+    if (rotary->interleaved > 1 || !std::isfinite((float)rotary->amplitude) || q_heads > kMaxQueryHeads) return SZ_E_ARG;
     if (reinterpret_cast<uintptr_t>(rotary->d_turns) & 7u || reinterpret_cast<uintptr_t>(d_positions) & 3u) return SZ_E_ALIGN;
     if (q_heads) {
         if ((rc = check_rows(d_q, q_token_stride, q_head_stride, a.b.tokens, q_heads)) != SZ_OK) return rc;

@@ -411,8 +411,9 @@ int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uin
  * are the same bit for bit, whatever the other sequences hold and wherever in
  * the batch it stands; under others the last bits differ.
  * d_ws: ws_bytes >=
- * sz_paged_attention_workspace_size(cache, batch, q_heads) (0 for heads that
- * do not divide; host fields of cache and batch only).  Its first
+ * sz_paged_attention_workspace_size(cache, batch, q_heads) (host fields of
+ * cache and batch only; 0 for heads that do not divide, and for a type,
+ * head_dim, number of heads or counts that the calls refuse).  Its first
  * SZ_ATTENTION_COUNTERS bytes are counters of chunks done: the caller clears
  * them once, and every call finds and leaves them 0, whatever shapes the
  * calls that share the workspace have.  Returns SZ_OK, SZ_E_DTYPE, SZ_E_ARG,
