@@ -192,6 +192,11 @@ __device__ __forceinline__ const int32_t *page_at(const Pool &p, const PagedBatc
 template <int COUNT>
 __device__ __forceinline__ void token_sequences(const PagedBatch &b, const int32_t *starts, uint32_t t0, int32_t (&seq)[COUNT])
 {
+    if (b.seqs == 0) {                               // and starts may be null
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) seq[k] = -1;
+        return;
+    }
     const int32_t first = wave_last_not_above(b.seqs + 1, t0, [&](uint32_t j) { return (int64_t)starts[j]; });
     const uint32_t base = (uint32_t)max(first, 0), lane = lane_id();
     const int32_t start = base + lane <= b.seqs ? starts[base + lane] : INT32_MAX;
@@ -269,7 +274,7 @@ __global__ __launch_bounds__(kSumThreads) void sz_pages_assign_one(Pool p, Paged
         len[k] = b.seqs ? b.lens[i] : 0;
         held[k] = b.seqs ? p.held[i] : 0;
     }
-    if (p.slots) {
+    if (p.slots && b.seqs) {
         for (uint32_t i = threadIdx.x; i <= b.seqs; i += kSumThreads) starts[i] = b.starts[i];
         for (uint32_t i = threadIdx.x; i < b.seqs; i += kSumThreads) lens[i] = b.lens[i];
     }

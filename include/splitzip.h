@@ -442,7 +442,8 @@ int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void 
  *     the same result.
  *   - d_slots (may be NULL), int64 [tokens]: page * page_tokens + row of each
  *     of the batch's tokens after the call, -1 for tokens without a place (of
- *     no sequence, p < 0, or of no page).
+ *     no sequence, p < 0, or of no page).  Of a batch without sequences, whose
+ *     arrays may be NULL, all are.
  * A page has one holder: one that two rows hold would come back twice.  A
  * sequence whose length leaves [0, max_kv] or whose d_held leaves [0,
  * table_width] is skipped (its d_held_out is its d_held), ends that contradict
