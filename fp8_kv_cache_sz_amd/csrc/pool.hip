@@ -142,11 +142,13 @@ __device__ __forceinline__ void store_held(const Pool &p, uint32_t i, const Move
 }
 
 // The ring after the call.  More pages than the ring has: some sequence holds
-// what it does not own.
+// what it does not own.  A shortage is a state that the caller serves by and by:
+// it is reported where nothing else is, so that what is wrong (plain stores, in
+// this launch or an earlier call's) stays to be seen whichever comes first.
 __device__ __forceinline__ void store_ends(const Pool &p, const PagedBatch &b, const Ring &r, uint32_t wanted, uint32_t served,
                                            uint32_t given)
 {
-    if (wanted > r.count) *b.status = SZ_E_CAPACITY;
+    if (wanted > r.count) atomicCAS(b.status, SZ_OK, SZ_E_CAPACITY);
     uint32_t count = r.count - served + given;                       // below 2^30 + 2^31
     if (count > r.pages) {
         flag_batch(b);

@@ -132,7 +132,8 @@ def pages_assign(pool: PagePool, batch: PageBatch, held: torch.Tensor, held_out:
     are updated, or with ``held_out`` and ``ends_out`` (int32 ``[2]``) left,
     and those written.  If the free pages do not reach for a sequence and all
     before it, it and those behind it that need more keep what they had, their
-    fresh entries are -1 and the pool's status is ``SZ_E_CAPACITY``.
+    fresh entries are -1 and the pool's status is ``SZ_E_CAPACITY``, unless
+    something wrong was reported there.
     ``slots``: true, or an int64 ``[tokens]`` tensor, for the batch's tokens'
     page * page_tokens + row (-1: no place), which are returned."""
     index = pool._index

@@ -433,7 +433,8 @@ int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void 
  *     and then of the row.  A sequence gets all of its missing pages if the
  *     free ones reach for it and all before it, else none: d_held_out[i] is
  *     then d_held[i], its fresh entries become -1 (which no call of the cache
- *     reads or writes at) and *d_status SZ_E_CAPACITY.
+ *     reads or writes at) and *d_status SZ_E_CAPACITY, unless it holds another
+ *     code: what a call finds wrong is not covered by what it has too few of.
  *   - Pages beyond need (a sequence that got shorter, or is done: length 0)
  *     go behind the ring's free pages, in the same order, for later calls;
  *     their entries of the row stay as they are.
