@@ -13,7 +13,10 @@
 // Free pages leave at one end of a ring and come back at the other: what a
 // call takes and what it gives never meet, so every entry moves by itself once
 // the two prefix sums are known, and a page that was given up is not handed
-// out again while the step that read it may still run.
+// out again while the step that read it may still run.  The pages that are free
+// and those that rows hold are the ring's size at most, unless a row holds what
+// it does not own: what then comes back beyond the ring's free places, where it
+// would meet the free pages that others read, is dropped and reported.
 //
 // Bound by latency: a launch, the lengths, the sums, the entries.  Up to
 // kOneSeqs sequences every workgroup of one launch works out all sums for
@@ -37,7 +40,7 @@ constexpr uint32_t kWaveTokens = 256;        // four a lane
 constexpr uint64_t kOneTokens = 1u << 18;    // that get slots, one a lane
 constexpr uint64_t kOneCounts = 128;
 constexpr uint32_t kNothing = 0xFFFFFFFFu;
-constexpr uint32_t kMaxPages = 1u << 30;     // ring positions: four times this stays in 32 bits
+constexpr uint32_t kMaxPages = 1u << 30;     // ring positions: twice this stays in 32 bits
 constexpr uint32_t kMany = 0x7FFFFFFFu;      // sums stop here: above any ring's pages
 
 // What happens to a sequence, or happened: where its fresh entries come from
@@ -74,13 +77,12 @@ __device__ __forceinline__ uint32_t given(const Move &m) { return m.held > m.nee
 // The ring's free pages; none if the two numbers contradict the ring.
 struct Ring {
     uint32_t head, count, pages;
-    __device__ __forceinline__ uint32_t at(uint32_t behind) const             // below 3 pages
+    __device__ __forceinline__ uint32_t at(uint32_t behind) const             // up to pages
     {
-        uint32_t x = head + behind;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) x = x >= pages ? x - pages : x;
-        return x;
+        const uint32_t x = head + behind;
+        return x >= pages ? x - pages : x;
     }
+    __device__ __forceinline__ uint32_t room() const { return pages - count; }       // of pages that come back
 };
 __device__ __forceinline__ Ring ring(const Pool &p, const PagedBatch &b)
 {
@@ -129,7 +131,7 @@ __device__ __forceinline__ Pair group_sum(Pair *lds, Pair mine, Pair &all)
 __device__ __forceinline__ Move placed(const Ring &r, Move m, Pair before)
 {
     if (m.held != kNothing && plus(before.take, taken(m)) <= r.count) m.take_at = before.take;
-    m.give_at = before.give < r.pages ? before.give : 0;             // over that: reported with the ends
+    m.give_at = before.give;
     return m;
 }
 __device__ __forceinline__ void store_held(const Pool &p, uint32_t i, const Move &m)
@@ -141,21 +143,16 @@ __device__ __forceinline__ void store_held(const Pool &p, uint32_t i, const Move
     }
 }
 
-// The ring after the call.  More pages than the ring has: some sequence holds
-// what it does not own.  A shortage is a state that the caller serves by and by:
+// The ring after the call.  A shortage is a state that the caller serves by and by:
 // it is reported where nothing else is, so that what is wrong (plain stores, in
 // this launch or an earlier call's) stays to be seen whichever comes first.
 __device__ __forceinline__ void store_ends(const Pool &p, const PagedBatch &b, const Ring &r, uint32_t wanted, uint32_t served,
                                            uint32_t given)
 {
     if (wanted > r.count) atomicCAS(b.status, SZ_OK, SZ_E_CAPACITY);
-    uint32_t count = r.count - served + given;                       // below 2^30 + 2^31
-    if (count > r.pages) {
-        flag_batch(b);
-        count = r.pages;
-    }
+    if (given > r.room()) flag_batch(b);
     p.ends_out[0] = (int32_t)r.at(served);
-    p.ends_out[1] = (int32_t)count;
+    p.ends_out[1] = (int32_t)(r.count - served + min(given, r.room()));
 }
 
 // One sequence's entries, a wave's worth at a time.
@@ -164,8 +161,8 @@ __device__ __forceinline__ void move_entries(const Pool &p, const PagedBatch &b,
     int32_t *row = p.table + (uint64_t)i * b.width;
     for (uint32_t e = lane_id(); e < taken(m); e += 64)
         row[m.held + e] = m.take_at == kNothing ? -1 : p.queue[r.at(m.take_at + e)];
-    const uint32_t most = min(given(m), r.pages);
-    for (uint32_t e = lane_id(); e < most; e += 64)
+    const uint32_t fits = r.room() > m.give_at ? min(given(m), r.room() - m.give_at) : 0;
+    for (uint32_t e = lane_id(); e < fits; e += 64)
         p.queue[r.at(r.count + m.give_at + e)] = row[m.need + e];
 }
 

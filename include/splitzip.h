@@ -448,8 +448,9 @@ int sz_paged_attention(const sz_cache *cache, const sz_batch *batch, const void 
  * A page has one holder: one that two rows hold would come back twice.  A
  * sequence whose length leaves [0, max_kv] or whose d_held leaves [0,
  * table_width] is skipped (its d_held_out is its d_held), ends that contradict
- * the ring count as no free pages, and more free pages than the ring has are
- * cut to that many; each sets *d_status to SZ_E_FORMAT.  seqs, table_width,
+ * the ring count as no free pages, and pages that go back beyond the ring's
+ * places (with more free and held pages than it has) are dropped; each sets
+ * *d_status to SZ_E_FORMAT.  seqs, table_width,
  * tokens and max_kv as in the calls above; slots are those of sequences with
  * at most max_new tokens.  d_ws: ws_bytes >=
  * sz_pages_assign_workspace_size(batch); its first SZ_ASSIGN_COUNTERS bytes

@@ -83,3 +83,81 @@ def test_a_shortage_hides_nothing_that_is_wrong(seqs, tokens, beside):
     assert run(2, word=CAPACITY)[0] == CAPACITY and run(0, word=CAPACITY, ends=[-1, 5])[0] == FORMAT
     if seqs < 40:
         assert run(seqs)[0] == 0 and run(seqs, word=FORMAT)[0] == FORMAT
+
+
+def assign_within(page, queue, ends, table, lens, held):
+    """(queue, ends, table, held, too many) after a call whose free pages
+    suffice; pages that come back behind the last of the ring's free places are
+    dropped."""
+    queue, table, out = queue.tolist(), [r[:] for r in table.tolist()], held.tolist()
+    (head, count), pages = ends.tolist(), len(queue)
+    old, room = queue[:], pages - count
+    taken, back = 0, []
+    for i, n in enumerate(lens.tolist()):
+        need = -(-n // page)
+        for w in range(out[i], need):
+            table[i][w] = old[(head + taken) % pages]
+            taken += 1
+        back += table[i][need:out[i]]
+        out[i] = need
+    assert taken <= count
+    for k, x in enumerate(back[:room]):
+        queue[(head + count + k) % pages] = x
+    return queue, [(head + taken) % pages, count - taken + min(len(back), room)], table, out, len(back) > room
+
+
+# pages, free ones, sequences, pages that the first one takes, pages that each other one holds, and how many of them give theirs back
+OVERFULL = [(20, 10, 6, 6, 3, 5), (20, 20, 3, 20, 4, 2), (20, 0, 9, 0, 4, 8), (3, 2, 3, 1, 3, 2), (4000, 3000, 200, 900, 20, 150),
+            (5000, 4000, 1500, 300, 4, 1400), (6000, 5000, 2600, 400, 3, 2590), (1000, 990, 2600, 300, 3, 2600)]
+
+
+@pytest.mark.parametrize("case", OVERFULL, ids=str)
+@pytest.mark.parametrize("beside", [False, True])
+def test_pages_of_two_holders_do_not_reach_the_free_ones(case, beside):
+    """Rows that hold what others hold, or what is free, give back more pages
+    than the ring has places for, while another sequence takes some: those that
+    are taken are the ring's free ones all the same, and it is reported."""
+    print("overfull", case, beside, flush=True)
+    m = sz()
+    pages, free, seqs, take, each, givers = case
+    head = pages - 2
+    queue = torch.full((pages,), -3, dtype=torch.int32)
+    queue[(head + torch.arange(free)) % pages] = torch.arange(free, dtype=torch.int32)
+    width = max(take, each) + 1
+    table = (torch.arange(seqs * width, dtype=torch.int32) % pages).view(seqs, width)
+    held = ints([0] + [each] * (seqs - 1))
+    lens = ints([take * P] + [0] * min(givers, seqs - 1) + [each * P] * max(0, seqs - 1 - givers))
+    T = take * P
+    starts = ints([0] + [T] * seqs)
+    want = assign_within(P, queue, ints([head, free]), table, lens, held)
+    assert want[4]
+    for rep in range(3):
+        pool = m.PagePool(P, queue.cuda(), ints([head, free]).cuda())
+        batch = batch_of(table, lens, starts, T, max_kv=width * P)
+        h = held.cuda()
+        kw = dict(held_out=torch.full_like(h, -1), ends_out=torch.full_like(pool.ends, -1)) if beside else {}
+        slots = m.pages_assign(pool, batch, h, slots=True, check=False, **kw)
+        assert int(pool.status.item()) == FORMAT
+        assert pool.queue.tolist() == want[0] and kw.get("ends_out", pool.ends).tolist() == want[1]
+        assert batch.page_table.tolist() == want[2] and kw.get("held_out", h).tolist() == want[3]
+        assert slots.tolist() == [want[2][0][p // P] * P + p % P for p in range(T)]
+
+
+def test_a_full_ring_is_not_too_many():
+    """Every page is free or held, some are taken and as many given back: nothing is reported."""
+    m = sz()
+    seqs = 100                                               # half of them hold 2 pages and want 4, the others give 4 back
+    order = torch.randperm(400, generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    table = torch.full((seqs, 4), -1, dtype=torch.int32)
+    table[:50, :2], table[50:] = order[:100].view(50, 2), order[100:300].view(50, 4)
+    queue = torch.full((400,), -3, dtype=torch.int32)
+    queue[:100] = order[300:]
+    lens, held = ints([4 * P] * 50 + [0] * 50), ints([2] * 50 + [4] * 50)
+    want = assign_within(P, queue, ints([0, 100]), table, lens, held)
+    assert not want[4] and want[1] == [100, 200]
+    pool = m.PagePool(P, queue.cuda(), ints([0, 100]).cuda())
+    batch = batch_of(table, lens, torch.zeros(seqs + 1, dtype=torch.int32), 0, max_kv=4 * P)
+    h = held.cuda()
+    m.pages_assign(pool, batch, h)
+    assert pool.queue.tolist() == want[0] and pool.ends.tolist() == want[1] and batch.page_table.tolist() == want[2]
+    assert h.tolist() == want[3]
