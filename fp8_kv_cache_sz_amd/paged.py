@@ -151,11 +151,13 @@ class PageBatch(_Fixed):
 
     def _ref(self, page_tokens: int):
         """The sz_batch for caches of this page size (max_kv defaults to a
-        full table's tokens)."""
+        full table's tokens), or 0: for calls that look at no page."""
         ref = self._by_page.get(page_tokens)
         if ref is None:
             top = 2 ** 32 - 1
-            max_kv = min(self.width * page_tokens, 1 << 30) if self.max_kv is None else self.max_kv
+            max_kv = self.max_kv
+            if max_kv is None:
+                max_kv = min(self.width * page_tokens, 1 << 30) if page_tokens else 1 << 30
             if max(self.tokens, self.seqs, self.width, self.max_new, max_kv) > top:
                 raise ValueError("the batch is too large")
             b = _native.sz_batch(self.page_table.data_ptr(), self.kv_lens.data_ptr(), self.starts.data_ptr(),

@@ -26,7 +26,7 @@ from .paged import (PageBatch, PagedCache, SplitZipError, _attend, _BAD_BATCH, _
 
 _int32, _int64, _empty_like, _contiguous = torch.int32, torch.int64, torch.empty_like, torch.contiguous_format
 COUNTERS = 256          # bytes at the start of an assignment's workspace
-_ANY_PAGE = 1 << 30     # the page size of calls that look at no page: bounds of 2^30 tokens
+_NO_PAGE = 0            # the page size of calls that look at no page
 
 
 def _ints(name, t, shape, index):
@@ -116,7 +116,7 @@ def assign_workspace(batch: PageBatch) -> torch.Tensor:
     """A workspace for ``pages_assign`` of batches of so many sequences.  Its
     first ``COUNTERS`` bytes are zero, as every call leaves them (they are
     cleared on the current stream, before any call that uses it)."""
-    n = _native.sz_pages_assign_workspace_size(batch._ref(_ANY_PAGE))
+    n = _native.sz_pages_assign_workspace_size(batch._ref(_NO_PAGE))
     ws = torch.empty(n, dtype=torch.uint8, device=batch.device)
     ws[:COUNTERS].zero_()
     return ws
@@ -215,7 +215,7 @@ def draft_tree(batch: PageBatch, parents: torch.Tensor, out=None, status: torch.
     else:
         own = status
     _launch("sz_draft_tree", _native.lib.sz_draft_tree, index, batch.device,
-            (batch._by_page.get(_ANY_PAGE) or batch._ref(_ANY_PAGE), at, masks.data_ptr(), words, positions.data_ptr(),
+            (batch._by_page.get(_NO_PAGE) or batch._ref(_NO_PAGE), at, masks.data_ptr(), words, positions.data_ptr(),
              None if own is None else own.data_ptr()), stream, owned)
     if check:
         _raise_word(own, stream)

@@ -161,3 +161,15 @@ def test_a_full_ring_is_not_too_many():
     m.pages_assign(pool, batch, h)
     assert pool.queue.tolist() == want[0] and pool.ends.tolist() == want[1] and batch.page_table.tolist() == want[2]
     assert h.tolist() == want[3]
+
+
+@pytest.mark.parametrize("new", [1, 5, 70])
+def test_trees_of_a_batch_without_a_table(new):
+    """Masks and positions need no page: a table of no columns will do."""
+    m = sz()
+    starts, lens = ints([0, new, 2 * new]), ints([500, new])
+    parents = ints([i - 1 for i in range(new)] * 2).cuda()
+    masks, positions = m.draft_tree(batch_of(torch.zeros(2, 0, dtype=torch.int32), lens, starts, 2 * new, max_new=new), parents)
+    assert positions.tolist() == list(range(500 - new, 500)) + list(range(new))
+    want = [[(1 << min(64, max(0, i + 1 - 64 * w))) - 1 for w in range(-(-new // 64))] for i in range(new)]
+    assert [[x % 2 ** 64 for x in row] for row in masks.tolist()] == want * 2
