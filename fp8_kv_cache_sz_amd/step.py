@@ -296,7 +296,7 @@ class Rotary(_Fixed):
         if dim < 8 or dim % 8 or dim > 128:
             raise ValueError("4, 8, ... or 64 frequencies turn 8, 16, ... or 128 values, got %d" % len(frequencies))
         values = frequencies.double().tolist()
-        if not all(map(math.isfinite, values)) or not abs(amplitude) < 2.0 ** 128:
+        if not all(map(math.isfinite, values)) or not abs(amplitude) < 2.0 ** 128 - 2.0 ** 103:
             raise ValueError("frequencies are finite, amplitude is in 32 bits")
         turns = torch.tensor([_turn(f) for f in values], dtype=torch.int64)
         if device is None:
