@@ -40,10 +40,13 @@
 // tiles of a sequence, and room for other plans: equal slots (tiles_each), long
 // sequences first (fold_of), fewer and longer chunks (kTreeFill), small batches in
 // blocks of 16 rows (rows_in_blocks).  Measured (MI355X, 8 KV heads of 128, four
-// query heads each): 64 trees of 8 tokens over up to 4,000 keys, E5M2 58 us, 5.3
-// TB/s; 32 of 61 over up to 8,192, E4M3 200 us, 738 TFLOP/s (32 over 8,192 each 309
-// us, 849); 13 tokens over 1,000 in BF16 12.7 us, which is a chain of launch,
-// lengths, masks, page, K and V, join.
+// query heads each, calls one after another; a launch by itself, traced, takes 4 to
+// 8 % more): 64 trees of 8 tokens over up to 4,000 keys, E5M2 58 us, 5.3 TB/s; 32 of
+// 61 over up to 8,192, E4M3 200 us, 738 TFLOP/s (32 over 8,192 each 291 to 309 us,
+// 902 to 849, on two cards); 13 tokens over 1,000 in BF16 12.7 us, which is a chain
+// of launch, lengths, masks, page, K and V, join.
+// Which kernel a batch gets, and with it whether probabilities are held to 2^-15
+// or rounded to BF16, follows the host's bounds (attn_plan) and not the lengths.
 #pragma once
 
 #include "paged.hpp"
@@ -1602,12 +1605,15 @@ inline uint64_t rows_wanted(uint64_t span, uint64_t groups)
 // (4 to 5 us): no more of them than one a CU.  Over 676 shapes (1 to 200 sequences,
 // 500 to 32,000 keys, 4 to 32 rows, every type, lengths equal and not) that takes
 // 0.86 of the time of the rule above, 320 as many 0.87, 192 and 384 0.91.  8 KV
-// heads of 128, E5M2, 32 rows: 32 sequences of 2,000 30 us (57), 64 of 4,000 94
-// (122), 64 of up to 4,000 74 (83); 4 rows in BF16, 64 of up to 8,192 255 (220).
+// heads of 128, E5M2, 32 rows: 32 sequences of 2,000 30 us (57), 64 of 4,000 95
+// (120), and with the longest first (fold_of) 64 of up to 4,000 58 (82); 4 rows in
+// BF16, 64 of up to 8,192 186 (210), 4 of up to 30,000 65 (72).  Where neither the
+// order nor more chunks even out lengths it is the worse: 4 rows, 16 of up to 8,000
+// 75 us (64), in E5M2 42 (37).
 constexpr uint64_t kTreeFill = 256;
 // Up to so many values of partials are joined in the launch: 8 KV heads of 128,
-// E5M2, 4 sequences of 16,000 in 8 chunks, 4 rows 27.5 us (29.1 with a launch), 16
-// rows 30.6 (29.1), 32 rows 38.2 (34.2).
+// E5M2, 4 sequences of 16,000 in 8 chunks, 4 rows 27.6 us (28.6 with a launch), 16
+// rows 30.8 (29.0), 32 rows 37.9 (33.4).
 constexpr uint64_t kTreeJoin = 1 << 14;
 // A chunk's partials cost their way out and back, rows D 8 bytes; its keys are
 // the time that the others do not take.  span / n + rows D n / kPartialKeys is
@@ -1668,11 +1674,14 @@ constexpr bool row_pairs(uint32_t dtype, uint32_t head_dim) { return dtype != SZ
 // workgroup, which read the same keys out of the L2.  Such calls wait for
 // latency, and its workgroups start and join sooner than sz_attn_tiles'.  Over
 // 374 shapes within these limits (1 to 16 sequences, 60 to 3,000 keys, 20 to 800
-// rows, every type) it takes 0.79 of the time, 8 heads of 128, BF16: 13 tokens of
-// four heads over 300 keys 11.3 us (13.6), over 1,000 13.6 (15.2); FP8 over 300
-// 10.7 (15.0).  Over 3,000 keys one workgroup joins more chunks than that saves
-// (20 us for 15), and with twice as much to do the products win (16 sequences of
-// up to 500, 104 rows, BF16: 29 us for 20).
+// rows, every type) it took 0.79 of the time.  8 heads of 128, one sequence, 13
+// tokens of four heads each in BF16: over 300 keys 10.8 us (11.8), 1,000 12.9
+// (13.2), 1,900 13.2 (15.4); FP8 over 300 10.5 (12.4).  Far beyond the limits the
+// products win (16 sequences of up to 500, 104 rows, BF16: 25.2 us for 19.2; 9 of
+// 25 tokens over up to 22,943, three heads, 198 for 57).  They are on the low side,
+// as they were set when one workgroup joined all chunks of a block: now 13 tokens
+// over 3,000 keys, E4M3, would take 14.0 us in blocks (17.8), 26 of four sequences
+// of up to 500, BF16, 10.0 (16.4).
 constexpr uint64_t kBlocksKeys = 2048;
 constexpr uint64_t kBlocksBytes = 1 << 17;       // workgroups times 128-key steps times bytes of a row
 inline uint64_t row_blocks(const PagedBatch &b, uint32_t group)             // one also for no rows at all
@@ -1689,9 +1698,9 @@ inline bool rows_in_blocks(const sz_cache *c, const PagedBatch &b, uint32_t grou
 // How trees' workgroups, `each` of a sequence, follow the sequences' lengths, as
 // far as one wave can sort them and more than one comes to a CU (0: not): the long
 // ones first, and if no more than two come to a CU, the shortest beside the longest.
-// 64 trees of 8 tokens over up to 4,000 keys, 8 KV heads, E5M2 59 us (77), 128 of up
-// to 8,000 227 (279), of up to 1,000 48 (51), 24 of up to 8,000 with 16 heads 96
-// (131); 30 tokens in BF16, 128 of up to 8,000 453 (522); equal lengths the same.
+// 64 trees of 8 tokens over up to 4,000 keys, 8 KV heads, E5M2 58 us (74), 128 of up
+// to 8,000 223 (278), of up to 1,000 47 (50), 24 of up to 8,000 with 16 heads 97
+// (130); 30 tokens in BF16, 128 of up to 8,000 445 (509); equal lengths the same.
 inline uint32_t fold_of(const PagedBatch &b, uint64_t each, uint64_t cus)
 {
     const uint64_t all = each * b.seqs;

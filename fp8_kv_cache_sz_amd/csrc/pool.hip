@@ -22,12 +22,12 @@
 // kOneSeqs sequences every workgroup of one launch works out all sums for
 // itself (they are a few KB, which the L2 has) and moves its share.  Where held
 // or the ring's ends are updated in place, the workgroup that arrives last
-// writes them, when all have read them; a count costs 10 ns or more, one after
+// writes them, when all have read them; a count costs 4 to 11 ns, one after
 // another, so beyond kOneCounts workgroups, as for more sequences, a launch of one
 // workgroup sums and a second one moves.  Measured (MI355X): a step of 256
 // sequences 5.6 us on the GPU (launch, lengths, sums, a page's number, its entry);
 // 1,000 prompts of up to 2,048 tokens, 73,000 pages of 16 and 1.15M slots (9.8 MB)
-// 10 us, with two launches 16.8.
+// 10.1 us, in place 10.8.
 #include "paged.hpp"
 
 namespace sz {
@@ -38,6 +38,10 @@ constexpr uint32_t kThreads = 256;
 constexpr uint32_t kOneSeqs = 2048;          // of one launch: their moves fill 32 KB of LDS
 constexpr uint32_t kWaveTokens = 256;        // four a lane
 constexpr uint64_t kOneTokens = 1u << 18;    // that get slots, one a lane
+// In place, one launch (two), prompts of pages of 16 whose slots make so many
+// workgroups: 1,000 sequences 128 7.2 us (8.4), 196 7.9 (8.4), 254 8.8 (8.5), 281
+// 12.2 (10.8); 256 sequences 196 7.4 (7.9), 281 11.8 (9.8); 16 sequences 128 6.8
+// (7.7), 196 7.7 (7.6), 281 18.7 (15.6), and 69 of more tokens each 9.2 (7.9).
 constexpr uint64_t kOneCounts = 128;
 constexpr uint32_t kNothing = 0xFFFFFFFFu;
 constexpr uint32_t kMaxPages = 1u << 30;     // ring positions: twice this stays in 32 bits

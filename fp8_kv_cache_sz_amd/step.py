@@ -241,7 +241,10 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, batch: PageBatch, masks: 
     token sees what its sequence has cached before the new tokens, and of the
     new ones those that its row of ``masks`` (``draft_tree``; any masks will
     do) names.  With ``window`` > 0 a token that names c new ones sees the last
-    window - max(c, 1) of the cached ones."""
+    window - max(c, 1) of the cached ones.  Where the
+    batch's ``max_new`` times the query heads of a KV head is over 16,
+    probabilities may be rounded to bfloat16, else they are held to 2^-15; its
+    bounds (``max_kv`` too) decide, not its lengths."""
     words = _mask_words("masks", masks, batch, cache._index)
     return _attend("sz_tree_attention", _native.lib.sz_tree_attention, (masks.data_ptr(), words), q, cache, batch, scale,
                    window, out, lse, ws, stream, check)

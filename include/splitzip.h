@@ -397,9 +397,9 @@ int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uin
  * or NULL.  A token that sees no key gets 0 and -inf.  Keys that a token does
  * not see do not reach its result, NaN and infinities included (but for its
  * last bits, where other tokens of the sequence see them).
- * Sums, scores and lse are 32-bit.  With more than 16 rows (new tokens times
- * query heads of a KV head) in a sequence its probabilities may be rounded to
- * BF16; with 16 or less they are held to 2^-15 of each, or 2^-133.  One below
+ * Sums, scores and lse are 32-bit.  Where max_new times the query heads of a KV
+ * head is over 16, probabilities may be rounded to BF16 (2^-8 of each at most);
+ * else they are held to 2^-15 of each, or 2^-133.  One below
  * 2^-126 may count as 0 (and 0 times an infinite value is a NaN), or as up to
  * 2^-140 where later keys outweigh it (so that an infinite value of that kind
  * stays infinite).  The sums of exp(s_j - m) V_j, with an m up to 8 / log2 e
@@ -413,7 +413,8 @@ int sz_cache_check(const sz_cache *cache, const sz_batch *batch, void *d_ws, uin
  * d_ws: ws_bytes >=
  * sz_paged_attention_workspace_size(cache, batch, q_heads) (host fields of
  * cache and batch only; 0 for heads that do not divide, and for a type,
- * head_dim, number of heads or counts that the calls refuse).  Its first
+ * head_dim, number of heads or counts that the calls refuse): what the larger
+ * of this call and sz_tree_attention takes; each is served by its own.  Its first
  * SZ_ATTENTION_COUNTERS bytes are counters of chunks done: the caller clears
  * them once, and every call finds and leaves them 0, whatever shapes the
  * calls that share the workspace have.  Returns SZ_OK, SZ_E_DTYPE, SZ_E_ARG,
@@ -491,7 +492,10 @@ int sz_draft_tree(const sz_batch *batch, const int32_t *d_parents, uint64_t *d_m
  * new ones sees the last window - max(c, 1) of the cached ones, and all that
  * it names.  A token that sees no key gets 0 and -inf.  words as above.  Other
  * arguments, d_ws, its size and the return codes as sz_paged_attention, of
- * which this is the same computation. */
+ * which this is the same computation, the rounding of probabilities included.
+ * Which of the two a batch beyond 16 rows gets follows its host fields (small
+ * ones of short max_kv and max_new have 2^-15 throughout): other bounds of the
+ * same tokens may give the other. */
 int sz_tree_attention(const sz_cache *cache, const sz_batch *batch, const uint64_t *d_masks, uint32_t words,
                       const void *d_q, uint32_t q_heads, uint64_t q_token_stride, uint64_t q_head_stride, float scale,
                       uint32_t window, void *d_out, float *d_lse, void *d_ws, uint64_t ws_bytes, int32_t *d_status,
@@ -538,7 +542,8 @@ int sz_rotary_write(const sz_cache *cache, const sz_batch *batch, const sz_rotar
  * page_tokens, kv_heads, head_dim) and different memory.  d_kept, int32
  * [seqs][kept_width], ascends strictly in each row, from 0 or more to below n;
  * counts lie in [0, kept_width] and are at most n: a sequence that breaks this
- * is left as it is and SZ_E_FORMAT reported.  The caller's next lengths are
+ * is left as it is and SZ_E_FORMAT reported (with a kept_width of 0, or a batch
+ * of no tokens, nothing is kept and the counts are not read).  The caller's next lengths are
  * kv_lens - n + counts.  Rows behind the kept ones keep their contents; tokens
  * with p < 0 are not moved, nor are rows whose page is none of the cache's.
  * The places of different sequences' new tokens must be distinct
