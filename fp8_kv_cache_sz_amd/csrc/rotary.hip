@@ -10,8 +10,10 @@
 // gives f_i / 2 pi as a 64-bit fraction F_i of a turn, and p F_i wraps around
 // exactly as the angle does, off by at most p 2^-65 turns at any position
 // (2^-34 at 2^31), where 32-bit p f_i has lost a turn's 2^-7 at 2^17.  What is
-// left after the nearest quarter turn, at most pi/4, goes through the Taylor
-// series of sine and cosine, to the last bit of its type.
+// left after the nearest quarter turn, at most pi/4, is rounded to its type as it
+// is, not at a fixed place (cut at 2^-32 turns, a frequency of 10^7's base was off
+// by 1 % where a value's partner is 0), and goes through the Taylor series of sine
+// and cosine, to the last bits of its type.
 //
 // Queries, and keys of BF16 caches, are computed in 32 bits.  Keys of FP8
 // caches in 64, rounded to 32: a row's scale depends on which side of a power
@@ -79,8 +81,9 @@ __device__ __forceinline__ void sin_cos(uint64_t turn, T &s, T &c)
     const uint64_t quarter = (turn + (1ull << 61)) >> 62;
     const int64_t rest = (int64_t)(turn - (quarter << 62));              // [-1/8, 1/8) of a turn
     T x;
-    if constexpr (std::is_same<T, float>::value)
-        x = (float)(int32_t)(rest >> 32) * (float)(6.283185307179586476925 / 4294967296.0);
+    if constexpr (std::is_same<T, float>::value)         // both halves: a small angle keeps its 24 bits
+        x = fmaf((float)(int32_t)(rest >> 32), (float)(6.283185307179586476925 / 4294967296.0),
+                 (float)(uint32_t)rest * (float)(6.283185307179586476925 / 18446744073709551616.0));
     else
         x = (double)rest * (6.283185307179586476925 / 18446744073709551616.0);
     T a, b;
