@@ -11,9 +11,9 @@
 // exactly as the angle does, off by at most p 2^-65 turns at any position
 // (2^-34 at 2^31), where 32-bit p f_i has lost a turn's 2^-7 at 2^17.  What is
 // left after the nearest quarter turn, at most pi/4, is rounded to its type as it
-// is, not at a fixed place (cut at 2^-32 turns, a frequency of 10^7's base was off
-// by 1 % where a value's partner is 0), and goes through the Taylor series of sine
-// and cosine, to the last bits of its type.
+// is, not at a fixed place (cut at 2^-32 turns, the slowest pairs of base 10^7 were
+// off by 1 % at the first positions where a value's partner is 0), and goes through
+// the Taylor series of sine and cosine, to the last bits of its type.
 //
 // Queries, and keys of BF16 caches, are computed in 32 bits.  Keys of FP8
 // caches in 64, rounded to 32: a row's scale depends on which side of a power
